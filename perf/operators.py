@@ -169,7 +169,7 @@ def _quantise(x, bits):
     """Codes and row scales of x [..., d]: r = max|x| / qmax (1 for a row of zeros), the nearest integer to x * fl(1 / r)."""
     qmax = 2 ** (bits - 1) - 1
     x = x.float()
-    r = x.abs().amax(-1) / qmax
+    r = x.abs().amax(-1) / torch.full((), qmax, device=x.device)     # a division, rounded once
     r = torch.where(r < torch.finfo(torch.float32).tiny, torch.ones_like(r), r)
     # ties and near-ties of the product are decided in 64 bits
     z = torch.round(x.double() * (1.0 / r).double().unsqueeze(-1)).clamp(-qmax, qmax)
@@ -390,7 +390,7 @@ def _exact_cache(s):
     qmax, out = 2 ** (s["case"]["bits"] - 1) - 1, []
     for i, x in enumerate((s["k_new"], s["v_new"])):
         old = _exact_rows(s["codes"][i], s["scales"][i])
-        r = (x.double().abs().max(-1, keepdim=True).values.float() / qmax)
+        r = (x.double().abs().max(-1, keepdim=True).values / torch.tensor(qmax, device="cuda", dtype=torch.float64)).float()
         r = torch.where(r < 2.0 ** -126, torch.ones((), device="cuda"), r)
         z = (x.double() * (1 / r).double()).round()
         old[s["place_new"]] = z.clamp(-qmax, qmax) * r.double()
