@@ -271,6 +271,135 @@ int stepq_prefill(stepq_ctx *ctx, void *pool, const int32_t *slots, int n_req, i
                   const float *q, const float *k, const float *v, const float *alpha, const float *beta,
                   float *o, float *workspace, int from_zero);
 
+/* ---- the gated delta rule as a served layer calls it ---------------------- */
+/* The recurrence of the header comment on fp32 states, without
+ * requantization, in the form a model's layers call it: one layer at a time,
+ * tokens in the activations' type, q and k heads shared by groups of value
+ * heads, rows inside a wider projection output, ragged batches.
+ *   u_t = beta_t (v_t - S'_t^T k_t), S'_t = Diag(alpha_t) S_{t-1},
+ *   S_t = S'_t + k_t u_t^T,  o_t = S_t^T q_t. */
+
+/* Type of the token rows (q, k, v, o; K, V and q, o of the cache below). */
+#define STEPQ_FP32 0
+#define STEPQ_FP16 1
+#define STEPQ_BF16 2
+
+/* A slot (or cache place) of -1 marks padding: the request is skipped and
+ * what it would write is left as it was. */
+#define STEPQ_PAD (-1)
+
+/* Token rows of one layer.  Row t of q and k holds n_qk_heads x d values, of v
+ * and o n_heads x d; value head h reads q and k head h / (n_heads / n_qk_heads).
+ * Row t of q starts at q + t * q_stride elements (likewise k, v, o): a stride
+ * is at least the row's width and a multiple of 16 bytes, and the arrays are
+ * 16-byte aligned, so q, k and v may be slices of one wider row.  alpha
+ * (fp32) is dense, [tokens][n_heads] for per-head plans, [tokens][n_heads][d]
+ * (16-byte aligned) for per-row plans; beta (fp32) is [tokens][n_heads]. */
+typedef struct stepq_tokens {
+    int dtype;       /* STEPQ_FP32, STEPQ_FP16 or STEPQ_BF16 */
+    int n_qk_heads;  /* divides the plan's n_heads */
+    const void *q, *k, *v;
+    const float *alpha, *beta;
+    void *o;
+    int64_t q_stride, k_stride, v_stride, o_stride; /* elements */
+} stepq_tokens;
+
+/* States S of the two calls below (fp32, 16-byte aligned): with `slots`
+ * (device int32), the fp32 pool [n_slots][n_layers][n_heads][d][d] of
+ * stepq_fp32_decode_step; with slots NULL, [n_seq][n_heads][d][d] (what
+ * stepq_unpack leaves and stepq_requant_pack takes for one layer).  A slot
+ * of STEPQ_PAD skips its sequence; any other slot outside [0, n_slots) sets
+ * the device error word and skips it.  Slots of one call must be distinct.
+ * Both calls read the initial state, leave the final one in its place, write
+ * o for every token in the tokens' type (rounded once, from fp32 sums), and
+ * are enqueued on `main`.  They can be captured into a CUDA graph. */
+
+/* n_tok tokens (n_tok >= 1) for each of n_seq requests; token i of request r
+ * is row r * n_tok + i.  The form for decoding (n_tok = 1) and for checking
+ * drafted tokens. */
+int stepq_delta_step(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, int n_seq, int n_tok,
+                     const stepq_tokens *tokens);
+
+/* A ragged batch of prompts: sequence s has the rows
+ * [cu_seqlens[s], cu_seqlens[s + 1]) (device int32[n_seq + 1], not decreasing,
+ * within [0, n_tokens]; a sequence that is not sets the device error word and
+ * is skipped).  Sequences may be empty.  Where fresh (device uint8[n_seq], NULL: none) is
+ * nonzero the sequence starts from S = 0 (an empty one leaves zeros).
+ * alpha in (0, 1]: a gate outside it sets the device error word and that
+ * head's results are not valid. */
+int stepq_delta_prefill(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, const uint8_t *fresh,
+                        int n_seq, const int32_t *cu_seqlens, int n_tokens, const stepq_tokens *tokens);
+
+/* Order the context's main stream after the work enqueued so far on a
+ * stream of the caller (a cudaStream_t on the context's device), and the
+ * other way round. */
+int stepq_ctx_wait_stream(stepq_ctx *ctx, void *stream);
+int stepq_stream_wait_ctx(stepq_ctx *ctx, void *stream);
+
+/* ---- quantised key-value cache -------------------------------------------- */
+/* The cache of the softmax-attention layers that hybrid models put between
+ * delta-rule layers, quantised as it is written with the per-row
+ * absmax quantizer of STEPQ_QUANT_ABSMAX, a row being one token's key (or value)
+ * of one head:
+ *   r = fl(max_j |x_j| / qmax), 1 where that is below 2^-126 (a row of zeros);
+ *   z_j = nearest integer, ties to even, to the exact x_j * fl(1/r), in
+ *   [-qmax, qmax]; it reads back as fl(r z_j), rounded to the type asked for.
+ *   A row that holds an infinity or NaN gets r = NaN and reads back as NaN.
+ * qmax = 127 (8 bits) or 7 (4 bits).  Codes are offset-binary (z + 128, or
+ * z + 8 with element 2m in the low half of byte m).
+ * Layout: the cache is n_pages pages of page_tokens tokens; a page holds, for
+ * each head, K codes [page_tokens][d bits/8] | V codes likewise | K scales
+ * fp32[page_tokens] | V scales.  A token's place is page * page_tokens +
+ * its row in the page.  Any initial contents will do: what lies behind a
+ * sequence's length is never used. */
+typedef struct stepq_kv stepq_kv; /* opaque: geometry, device, 4-byte error word */
+
+/* bits 4 or 8; d 64, 128 or 256; page_tokens a multiple of 16, at most 65536.  Bound to the
+ * current device. */
+int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, int n_pages, stepq_kv **out);
+void stepq_kv_free(stepq_kv *kv);
+/* Bytes of the cache buffer (the caller's, 128-byte aligned). */
+size_t stepq_kv_bytes(const stepq_kv *kv);
+
+/* Each call below is enqueued on `stream` (a cudaStream_t; NULL: the legacy
+ * default stream) and can be captured. */
+
+/* Quantise n_tokens rows of k and v ([n_tokens][n_heads][d], row strides in
+ * elements, as in stepq_tokens) into the cache at places[t] (device int64;
+ * STEPQ_PAD skips the token; a place outside the cache sets the error word and
+ * is skipped; of several tokens with one place, which one stays is undefined). */
+int stepq_kv_append(stepq_kv *kv, void *cache, int dtype, int n_tokens, const void *k, const void *v,
+                    int64_t k_stride, int64_t v_stride, const int64_t *places, void *stream);
+
+/* Sequences: lens[s] (device int32) tokens, token t of sequence s on page
+ * page_table[s * max_pages + t / page_tokens] (device int32).  A length below 0
+ * marks padding (skipped, outputs left as they were); a length above
+ * max_pages * page_tokens, or a page outside the cache, sets the error word and
+ * the sequence's outputs are not valid. */
+
+/* Read the sequences back: token t of sequence s to row cu_seqlens[s] + t of
+ * k and v (rows outside [0, n_rows) set the error word and are not written). */
+int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const int32_t *page_table, int max_pages,
+                  const int32_t *lens, const int32_t *cu_seqlens, int64_t n_rows, int dtype, void *k, void *v,
+                  int64_t k_stride, int64_t v_stride, void *stream);
+
+/* Attention of each sequence's newest n_tok tokens over the cache:
+ * q, o: row s * n_tok + i, [n_q_heads][d]; query head h reads cache head
+ * h / (n_q_heads / n_heads); token i sees positions t <= lens[s] - n_tok + i.
+ *   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max)
+ * lse (fp32 [n_seq][n_tok][n_q_heads], or NULL) receives the logarithm of
+ * sum_t exp(scale q.k_t).  A token that sees nothing gets o = 0 and lse =
+ * -infinity.  scale is finite and above 0.  workspace: stepq_kv_attend_workspace_bytes (of the same
+ * arguments) bytes, 16-byte aligned, used by one call at a time. */
+int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const int32_t *page_table, int max_pages,
+                    const int32_t *lens, int dtype, int n_tok, int n_q_heads, const void *q, int64_t q_stride,
+                    float scale, void *o, int64_t o_stride, float *lse, void *workspace, void *stream);
+size_t stepq_kv_attend_workspace_bytes(const stepq_kv *kv, int n_seq, int n_tok, int n_q_heads, int max_pages);
+
+/* Wait for `stream` and return the error word (STEPQ_OK or STEPQ_EDEVICE; the
+ * word is cleared). */
+int stepq_kv_check(stepq_kv *kv, void *stream);
+
 /* Pack fp32 states S into the pool records of (slots, layers [lb, le)):
  * the requantizer of the header comment (used for S_0).  Enqueued on main. */
 int stepq_requant_pack(stepq_ctx *ctx, void *pool, const int32_t *slots, int n_req, int lb, int le,

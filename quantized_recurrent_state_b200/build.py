@@ -16,14 +16,16 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libstepq.so")
-SOURCES = ["stepq_api.cu", "stepq_step.cu", "stepq_head.cu", "stepq_head_tm.cu", "stepq_aux.cu", "stepq_prefill.cu", "stepq_prefill_tc.cu", "stepq_tc_selftest.cu"]
-HEADERS = ["stepq_dev.cuh", "stepq_pipe.cuh", "stepq_head.cuh", "stepq_prefill.cuh", "stepq_tc.cuh", os.path.join("..", "..", "include", "stepq.h")]
+SOURCES = ["stepq_api.cu", "stepq_step.cu", "stepq_head.cu", "stepq_head_tm.cu", "stepq_aux.cu", "stepq_prefill.cu", "stepq_prefill_tc.cu", "stepq_tc_selftest.cu",
+           "stepq_delta.cu", "stepq_kv.cu", "stepq_kv_attend.cu", "stepq_kv_api.cu"]
+HEADERS = ["stepq_dev.cuh", "stepq_pipe.cuh", "stepq_head.cuh", "stepq_prefill.cuh", "stepq_tc.cuh", "stepq_delta.cuh",
+           "stepq_kv.cuh", "stepq_host.h", os.path.join("..", "..", "include", "stepq.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
 def nvcc_cmd(out: str, extra=()):
     return [NVCC, "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
-            "--fmad=false", "-Xcompiler", "-fPIC,-ffp-contract=off", "-shared", "-o", out,
+            "--fmad=false", "--threads", "0", "-Xcompiler", "-fPIC,-ffp-contract=off", "-shared", "-o", out,
             *[os.path.join(CSRC, s) for s in SOURCES], *extra]
 
 

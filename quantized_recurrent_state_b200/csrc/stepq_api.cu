@@ -21,10 +21,10 @@
 #include <thread>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/stepq.h"
+#include "stepq_delta.cuh"
 #include "stepq_dev.cuh"
+#include "stepq_host.h"
 #include "stepq_prefill.cuh"
 
 namespace stepq {
@@ -41,9 +41,9 @@ cudaError_t run_tc_selftest(const float *A, const float *B1, const float *B2, fl
                             int *word);
 }  // namespace stepq
 
-namespace {
+static thread_local std::string g_err;
 
-thread_local std::string g_err;
+namespace stepq {
 
 int fail(int code, const char *fmt, ...) {
     char buf[512];
@@ -58,6 +58,34 @@ int fail(int code, const char *fmt, ...) {
 int cuda_fail(cudaError_t e, const char *what) {
     return fail(STEPQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+int check_ptr(const void *p, size_t align, const char *name) {
+    if (!p) return fail(STEPQ_EINVAL, "%s is null", name);
+    if (reinterpret_cast<uintptr_t>(p) % align) return fail(STEPQ_EINVAL, "%s is not %zu-byte aligned", name, align);
+    return STEPQ_OK;
+}
+
+int check_dtype(int dtype, const char *what) {
+    if (dtype == STEPQ_FP32 || dtype == STEPQ_FP16 || dtype == STEPQ_BF16) return STEPQ_OK;
+    return fail(STEPQ_EINVAL, "%s: dtype %d", what, dtype);
+}
+
+int check_rows(const void *p, int dtype, long long stride, long long width, const char *name) {
+    if (int rc = check_ptr(p, 16, name)) return rc;
+    const long long size = dtype == STEPQ_FP32 ? 4 : 2;
+    if (stride < width) return fail(STEPQ_EINVAL, "%s: row stride %lld below the row's %lld values", name, stride, width);
+    if (stride * size % 16) return fail(STEPQ_EINVAL, "%s: row stride of %lld bytes is not a multiple of 16", name, stride * size);
+    return STEPQ_OK;
+}
+
+}  // namespace stepq
+
+namespace {
+
+using stepq::check_ptr;
+using stepq::cuda_fail;
+using stepq::fail;
+using stepq::NvtxRange;
 
 // CRC-32 (IEEE 802.3, reflected polynomial 0xEDB88320).
 uint32_t crc32(const uint8_t *p, size_t n) {
@@ -90,14 +118,6 @@ T rd(const uint8_t *p) {
 // ---------------------------------------------------------------------------
 // plan
 // ---------------------------------------------------------------------------
-
-// NVTX range around a public call (a no-op unless a profiler is attached).
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
 
 struct stepq_plan {
     int mode = 0, L = 0, H = 0, D = 0, n_units = 0, n_pivots = 0;
@@ -619,6 +639,7 @@ struct stepq_ctx {
     std::vector<cudaEvent_t> side_done;  // per layer
     std::vector<cudaEvent_t> dec_done;   // per chunk index
     cudaEvent_t ev_main = nullptr, ev_side = nullptr;
+    cudaEvent_t ev_join = nullptr;  // orders main and a caller's stream
     int *err = nullptr;
     void *tables_mem = nullptr;
     stepq::Tables t{};
@@ -635,12 +656,6 @@ struct stepq_ctx {
 };
 
 namespace {
-
-int check_ptr(const void *p, size_t align, const char *name) {
-    if (!p) return fail(STEPQ_EINVAL, "%s is null", name);
-    if (reinterpret_cast<uintptr_t>(p) % align) return fail(STEPQ_EINVAL, "%s is not %zu-byte aligned", name, align);
-    return STEPQ_OK;
-}
 
 int check_range(const stepq_ctx *c, int n_req, int lb, int le) {
     if (!c) return fail(STEPQ_EINVAL, "null context");
@@ -826,6 +841,7 @@ extern "C" int stepq_ctx_create(const stepq_plan *plan, void *main_stream, void 
     }
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_main, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_side, cudaEventDisableTiming);
+    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&c->ev_join, cudaEventDisableTiming);
     if (e != cudaSuccess) { stepq_ctx_free(c); return cuda_fail(e, "event creation"); }
     c->layer_max_rec.assign(p->L, 128);
     for (int l = 0; l < p->L; ++l)
@@ -849,6 +865,7 @@ extern "C" void stepq_ctx_free(stepq_ctx *c) {
     for (auto ev : c->dec_done) if (ev) cudaEventDestroy(ev);
     if (c->ev_main) cudaEventDestroy(c->ev_main);
     if (c->ev_side) cudaEventDestroy(c->ev_side);
+    if (c->ev_join) cudaEventDestroy(c->ev_join);
     if (c->err) cudaFree(c->err);
     if (c->tables_mem) cudaFree(c->tables_mem);
     delete c;
@@ -1038,9 +1055,10 @@ extern "C" int stepq_sync(stepq_ctx *c, int timeout_ms) {
     if (word) {
         cudaMemset(c->err, 0, sizeof(int));
         if (word & stepq::kErrTmemDrain) c->poisoned = true;
-        return fail(STEPQ_EDEVICE, "device error word 0x%x (%s%s%s%s%s)", word,
+        return fail(STEPQ_EDEVICE, "device error word 0x%x (%s%s%s%s%s%s)", word,
                     (word & stepq::kErrBadSlot) ? "slot out of range " : "", (word & stepq::kErrWait) ? "copy wait gave up " : "",
                     (word & stepq::kErrArgs) ? "bad width " : "", (word & stepq::kErrGateRange) ? "prefill gate out of range " : "",
+                    (word & stepq::kErrSeq) ? "sequence outside the batch's tokens " : "",
                     (word & stepq::kErrTmemDrain) ? "tensor memory freed with a product in flight (context now unusable) " : "");
     }
     return STEPQ_OK;
@@ -1124,6 +1142,97 @@ extern "C" int stepq_prefill(stepq_ctx *c, void *pool, const int32_t *slots, int
     lt.done();
     return STEPQ_OK;
 }
+
+// ---------------------------------------------------------------------------
+// the gated delta rule as a served layer calls it
+// ---------------------------------------------------------------------------
+
+static int delta_args(stepq_ctx *c, int layer, float *S, const int32_t *slots, int n_seq, long long n_tokens,
+                      const stepq_tokens *t, stepq::DeltaArgs &a) {
+    int rc = check_range(c, n_seq, layer, layer + 1);
+    if (rc) return rc;
+    if (!t) return fail(STEPQ_EINVAL, "tokens is null");
+    if ((rc = stepq::check_dtype(t->dtype, "tokens"))) return rc;
+    const int H = c->plan->H, D = c->plan->D, Hk = t->n_qk_heads;
+    if (Hk <= 0 || H % Hk) return fail(STEPQ_EINVAL, "n_qk_heads %d does not divide the plan's %d heads", Hk, H);
+    if (n_tokens < 0 || n_tokens > 0x7fffffffll) return fail(STEPQ_EINVAL, "%lld tokens", n_tokens);
+    if ((rc = check_ptr(S, 16, "S"))) return rc;
+    if (slots && (rc = check_ptr(slots, 4, "slots"))) return rc;
+    if (n_tokens > 0) {
+        if ((rc = stepq::check_rows(t->q, t->dtype, t->q_stride, (long long)Hk * D, "q")) ||
+            (rc = stepq::check_rows(t->k, t->dtype, t->k_stride, (long long)Hk * D, "k")) ||
+            (rc = stepq::check_rows(t->v, t->dtype, t->v_stride, (long long)H * D, "v")) ||
+            (rc = stepq::check_rows(t->o, t->dtype, t->o_stride, (long long)H * D, "o")) ||
+            (rc = check_ptr(t->alpha, c->plan->mode == 1 ? 16 : 4, "alpha")) || (rc = check_ptr(t->beta, 4, "beta")))
+            return rc;
+    }
+    a.S = S;
+    a.slots = slots;
+    a.n_slots = c->n_slots;
+    a.n_layers = c->plan->L;
+    a.layer = layer;
+    a.n_seq = n_seq;
+    a.n_tokens = (int)n_tokens;
+    a.H = H;
+    a.Hk = Hk;
+    a.q = t->q; a.k = t->k; a.v = t->v; a.o = t->o;
+    a.alpha = t->alpha; a.beta = t->beta;
+    a.qs = t->q_stride; a.ks = t->k_stride; a.vs = t->v_stride; a.os = t->o_stride;
+    a.err = c->err;
+    return STEPQ_OK;
+}
+
+extern "C" int stepq_delta_step(stepq_ctx *c, int layer, float *S, const int32_t *slots, int n_seq, int n_tok,
+                                const stepq_tokens *tokens) {
+    NvtxRange nvtx_range("stepq_delta_step");
+    if (n_tok < 1) return fail(STEPQ_EINVAL, "delta_step: n_tok %d", n_tok);
+    stepq::DeltaArgs a{};
+    int rc = delta_args(c, layer, S, slots, n_seq, (long long)n_seq * n_tok, tokens, a);
+    if (rc) return rc;
+    if (n_seq == 0) return STEPQ_OK;
+    a.n_tok = n_tok;
+    const stepq::DeviceScope dev(c->device);
+    if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
+    LaunchTimer lt(c, 3, c->main);
+    const cudaError_t e = stepq::launch_delta_seq(c->plan->D, tokens->dtype, c->plan->mode == 1, a, c->main);
+    if (e != cudaSuccess) return cuda_fail(e, "delta_step launch");
+    lt.done();
+    return STEPQ_OK;
+}
+
+extern "C" int stepq_delta_prefill(stepq_ctx *c, int layer, float *S, const int32_t *slots, const uint8_t *fresh,
+                                   int n_seq, const int32_t *cu_seqlens, int n_tokens, const stepq_tokens *tokens) {
+    NvtxRange nvtx_range("stepq_delta_prefill");
+    stepq::DeltaArgs a{};
+    int rc = delta_args(c, layer, S, slots, n_seq, n_tokens, tokens, a);
+    if (rc) return rc;
+    if (n_seq == 0) return STEPQ_OK;
+    if ((rc = check_ptr(cu_seqlens, 4, "cu_seqlens"))) return rc;
+    a.cu = cu_seqlens;
+    a.fresh = fresh;
+    a.check_gates = 1;
+    const stepq::DeviceScope dev(c->device);
+    if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
+    LaunchTimer lt(c, 4, c->main);
+    const cudaError_t e = stepq::launch_delta_seq(c->plan->D, tokens->dtype, c->plan->mode == 1, a, c->main);
+    if (e != cudaSuccess) return cuda_fail(e, "delta_prefill launch");
+    lt.done();
+    return STEPQ_OK;
+}
+
+static int join_streams(stepq_ctx *c, void *stream, bool main_waits) {
+    if (!c) return fail(STEPQ_EINVAL, "null context");
+    const cudaStream_t other = static_cast<cudaStream_t>(stream);
+    if (other == c->main) return STEPQ_OK;
+    const stepq::DeviceScope dev(c->device);
+    cudaError_t e = dev.error();
+    if (e == cudaSuccess) e = cudaEventRecord(c->ev_join, main_waits ? other : c->main);
+    if (e == cudaSuccess) e = cudaStreamWaitEvent(main_waits ? c->main : other, c->ev_join, 0);
+    return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "stream join");
+}
+
+extern "C" int stepq_ctx_wait_stream(stepq_ctx *c, void *stream) { return join_streams(c, stream, true); }
+extern "C" int stepq_stream_wait_ctx(stepq_ctx *c, void *stream) { return join_streams(c, stream, false); }
 
 extern "C" int stepq_selftest_tc(const float *A, const float *B1, const float *B2, float *D1, float *D2, float *D3) {
     int rc;

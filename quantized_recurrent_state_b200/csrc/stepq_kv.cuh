@@ -1,0 +1,73 @@
+// Geometry and launch arguments of the quantised key-value cache
+// (stepq_kv.cu, stepq_kv_attend.cu), shared with the C ABI that fills them.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace stepq {
+
+constexpr int kErrKvPlace = 1;  // device error word: a place, page or output row out of range
+constexpr int kErrKvLen = 2;    // a length above max_pages * page_tokens
+
+struct KvGeo {
+    int bits, H, d, page_tokens, n_pages;
+    int *err;
+    __host__ __device__ int row_bytes() const { return d * bits / 8; }
+    __host__ __device__ int64_t head_bytes() const { return (int64_t)page_tokens * (2 * row_bytes() + 8); }
+    __host__ __device__ int64_t page_bytes() const { return head_bytes() * H; }
+    // offset of the (K: which = 0, V: 1) codes of a page's head, and of its scales
+    __host__ __device__ int64_t codes_at(int64_t page, int h, int which) const {
+        return page * page_bytes() + h * head_bytes() + (int64_t)which * page_tokens * row_bytes();
+    }
+    __host__ __device__ int64_t scales_at(int64_t page, int h, int which) const {
+        return page * page_bytes() + h * head_bytes() + (int64_t)page_tokens * (2 * row_bytes() + 4 * which);
+    }
+};
+
+struct KvAppendArgs {
+    KvGeo g;
+    uint8_t *cache;
+    const void *x[2];       // k, v
+    int64_t stride[2];
+    const int64_t *places;
+    int n_tokens;
+};
+
+struct KvReadArgs {
+    KvGeo g;
+    const uint8_t *cache;
+    const int32_t *table, *lens, *cu;
+    int n_seq, max_pages;
+    int64_t n_rows;
+    void *x[2];
+    int64_t stride[2];
+};
+
+struct KvAttendArgs {
+    KvGeo g;
+    const uint8_t *cache;
+    const int32_t *table, *lens;
+    int n_seq, max_pages, n_tok, Hq, dtype;
+    const void *q;
+    void *o;
+    int64_t qs, os;
+    float scale;
+    float *lse;
+    float *part;            // split results: [unit][split][row][d + 2] (d sums, reference, total)
+    int n_splits, row_tiles;
+};
+
+// dtype 0 fp32, 1 fp16, 2 bf16
+cudaError_t launch_kv_append(int dtype, const KvAppendArgs &a, cudaStream_t st);
+cudaError_t launch_kv_read(int dtype, const KvReadArgs &a, cudaStream_t st);
+
+// How a call is cut up: rows of query heads and tokens that share a cache head, eight to an MMA column
+// tile, NR tiles to a block; the length into n_splits parts.
+struct KvSplit {
+    int nr, row_tiles, n_splits;
+};
+KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, int n_sms);
+cudaError_t launch_kv_attend(const KvAttendArgs &a, int nr, cudaStream_t st);
+
+}  // namespace stepq

@@ -1,0 +1,542 @@
+// Attention of the newest tokens over the quantised cache (definitions:
+// include/stepq.h).
+//
+// Bound: HBM, the codes and scales of the sequence read once (d bits / 4 + 8
+// bytes a token and head).  The codes never become floating-point rows in memory: each
+// lane loads its own 16-byte pieces of them straight into the registers that the
+// tensor cores read (mma.sync m16n8k16; one query row per column, so a group of eight
+// query heads or drafted tokens fills a tile; the fifth-generation instruction needs
+// 128 rows and its operands in shared memory, which eight rows cannot pay for).
+//   S^T = K q^T    A: 16 tokens x 16 of d, B: q, in shared memory in fragment order
+//   O^T += V^T P^T A: 16 of d x 16 tokens, B: P, moved from the C to the B layout
+//                  by two 8 x 8 transposes
+// The index summed over may be permuted at will, so a lane's codes need not be
+// neighbours in the fragment's order: a lane takes contiguous bytes, q is stored to
+// match.  Codes become fp16 exactly (1024 + u has the code in its low bits;
+// one subtraction, or for the high nibbles one fma, leaves z).  The row scales stay
+// outside the products: r_k multiplies the score, r_v the weight.
+//
+// The weight p r_v has to fit fp16, whatever r_v is, so the running reference of a row
+// is the largest s + log2 r_v instead of the largest s (lr below).  It moves only
+// when a weight would exceed 2^8: sums are fp32, and 2^8 leaves fp16 room; a move costs
+// three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry 2^-12 of
+// themselves as rounding error; fp32 outputs take them (and q) as sums of two fp16 values.
+//
+// A warp works on its own tiles of 16 tokens, the block's warps in turn, and keeps
+// its own reference, total and sums; they are joined once at the end, in warp order.  A
+// sequence is cut into n_splits parts when the batch does not fill the SMs; a second
+// kernel joins them in order, so results do not depend on timing.
+#include <float.h>
+
+#include <type_traits>
+
+#include "stepq_delta.cuh"
+#include "stepq_kv.cuh"
+
+namespace stepq {
+
+namespace {
+
+constexpr int kWarps = 4, kTile = 16;
+constexpr float kSlack = 8.0f;           // log2 of the largest weight
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
+// (1024 + u) pairs -> u - zero
+__device__ __forceinline__ uint32_t minus(uint32_t x, uint32_t c) { return bits_of(__hsub2(half2_of(x), half2_of(c))); }
+
+// Bytes of a code row that one lane loads: PER of them (a quarter of a K row, an eighth of a V row), in pieces of V
+// bytes, piece n of lane i of LANES at byte (n LANES + i) V.
+template <int PER>
+struct Piece {
+    static constexpr int V = PER < 16 ? PER : 16, N = PER / V, W = PER / 4;
+    template <int LANES>
+    static __device__ __forceinline__ void load(const uint8_t *row, int i, uint32_t (&w)[W]) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint8_t *p = row + (n * LANES + i) * V;
+            if constexpr (V == 16) {
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p));
+                w[4 * n] = y.x; w[4 * n + 1] = y.y; w[4 * n + 2] = y.z; w[4 * n + 3] = y.w;
+            } else if constexpr (V == 8) {
+                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(p));
+                w[0] = y.x; w[1] = y.y;
+            } else {
+                w[0] = __ldg(reinterpret_cast<const unsigned int *>(p));
+            }
+        }
+    }
+};
+
+template <int BITS, int D, int NR>
+struct Geo {
+    static constexpr int RB = D * BITS / 8;              // bytes of a code row
+    using K = Piece<RB / 4>;
+    using V = Piece<RB / 8>;
+    static constexpr int CW = 32 / BITS;                 // codes in a word
+    static constexpr int KS = D / 16;                    // K steps of the scores, and 16-column tiles of the sums
+    static constexpr int R = 8 * NR;                     // rows of a block
+    // place of q element dd in the fragments: step, register, half, lane quarter
+    static __device__ __forceinline__ int q_at(int dd, int r, int &plane_words) {
+        constexpr int CV = K::V * CW / 4;                // codes of a piece
+        const int piece = dd / (4 * CV), c = dd / CV % 4, idx = piece * CV + dd % CV;
+        int ks, reg, half;
+        if constexpr (BITS == 8) {
+            ks = idx / 4; reg = idx / 2 % 2; half = idx % 2;
+        } else {
+            ks = idx / 8 * 2 + idx % 4 / 2; reg = idx % 2; half = idx / 4 % 2;
+        }
+        plane_words = KS * NR * 32 * 2;
+        return ((((ks * NR + r / 8) * 32 + (r % 8) * 4 + c) * 2) + reg) * 2 + half;
+    }
+    // value column of sum tile mt, half hi (rows g or g + 8 of the tile), lane group g
+    static __device__ __forceinline__ int col_of(int mt, int hi, int g) {
+        constexpr int CV = V::V * CW / 4;
+        const int idx = 2 * mt + hi;
+        return (idx / CV * 8 + g) * CV + idx % CV;
+    }
+};
+
+template <int BITS, int D>
+struct Tile {                                            // one lane's codes and scales of 16 tokens
+    uint32_t k[2][D * BITS / 128], v[4][D * BITS / 256];
+    float rk[2], rv[2];
+};
+
+template <int BITS, int D, int NR, int TERMS>
+__global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
+    using G = Geo<BITS, D, NR>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __half *qf = reinterpret_cast<__half *>(smem);                              // [TERMS][KS][NR][32][2] half pairs
+    float *qe = reinterpret_cast<float *>(smem + TERMS * G::KS * NR * 256);     // [R] score factor of the row
+    float *join = qe + G::R;                                                    // [kWarps][R][D + 2]
+    const KvGeo &g = a.g;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lc = lane & 3;
+    const int group = a.Hq / g.H, rows = a.n_tok * group;
+    int64_t u = blockIdx.x;
+    const int split = (int)(u % a.n_splits);
+    u /= a.n_splits;
+    const int64_t unit = u;
+    const int rt = (int)(u % a.row_tiles);
+    u /= a.row_tiles;
+    const int h = (int)(u % g.H), s = (int)(u / g.H);
+    const int r0 = rt * G::R, nrow = min(G::R, rows - r0);
+
+    const int len = a.lens[s];
+    if (len < 0) return;
+    if (len > (int64_t)a.max_pages * g.page_tokens) {
+        if (threadIdx.x == 0) atomicOr(g.err, kErrKvLen);
+        return;
+    }
+    // this block's tokens: a part of the length in whole steps of the block
+    constexpr int kStep = kWarps * kTile;
+    const int per = (int)(((int64_t)len + (int64_t)a.n_splits * kStep - 1) / ((int64_t)a.n_splits * kStep)) * kStep;
+    const int begin = (int)min((int64_t)len, (int64_t)split * per), end = (int)min((int64_t)len, (int64_t)begin + per);
+    if (a.n_splits > 1 && split > 0 && begin >= len) return;                    // the joining kernel knows it is empty
+
+    // q rows as fp16 fragments, scaled by a power of two to below 1
+    for (int r = warp; r < G::R; r += kWarps) {
+        float x[D / 32], m = 0.0f;
+        if (r < nrow) {
+            const int i = (r0 + r) / group, hq = h * group + (r0 + r) % group;
+            const int64_t at = ((int64_t)s * a.n_tok + i) * a.qs + (int64_t)hq * D;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                const int64_t p = at + e * 32 + lane;
+                x[e] = a.dtype == 0   ? static_cast<const float *>(a.q)[p]
+                       : a.dtype == 1 ? to_f32(static_cast<const __half *>(a.q)[p])
+                                      : to_f32(static_cast<const __nv_bfloat16 *>(a.q)[p]);
+                m = fmaxf(m, fabsf(x[e]));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
+        }
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+        int ex = 0;
+        if (m > 0.0f && m <= FLT_MAX) frexpf(m, &ex);
+        // 2^-ex in two factors, each of which is a normal number
+        const int e1 = ex / 2, e2 = ex - e1;
+        const float f1 = ldexpf(1.0f, -e1), f2 = ldexpf(1.0f, -e2);
+        int plane;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            const float y = x[e] * f1 * f2;
+            const int at = G::q_at(e * 32 + lane, r, plane);
+            const __half hi = __float2half_rn(y);
+            qf[at] = hi;
+            if constexpr (TERMS == 2) qf[2 * plane + at] = __float2half_rn(y - __half2float(hi));
+        }
+        if (lane == 0) qe[r] = ldexpf(a.scale * kLog2e, ex);
+    }
+    __syncthreads();
+
+    float ref[2 * NR], total[2 * NR], lift[2 * NR];
+    int limit[2 * NR];                                   // first token that the row does not see
+    float acc[G::KS][NR][4];
+#pragma unroll
+    for (int j = 0; j < 2 * NR; ++j) {
+        const int r = 8 * (j / 2) + 2 * lc + j % 2;
+        ref[j] = -INFINITY;
+        total[j] = 0.0f;
+        lift[j] = qe[r];
+        limit[j] = r < nrow ? len - a.n_tok + 1 + (r0 + r) / group : 0;   // a row without a query sees nothing
+    }
+#pragma unroll
+    for (int mt = 0; mt < G::KS; ++mt)
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) acc[mt][nr][0] = acc[mt][nr][1] = acc[mt][nr][2] = acc[mt][nr][3] = 0.0f;
+
+    const int32_t *table = a.table + (int64_t)s * a.max_pages;
+    auto page_of = [&](int t) -> int {
+        if (t >= end) return 0;
+        const int page = __ldg(table + t / g.page_tokens);
+        if (page >= 0 && page < g.n_pages) return page;
+        if (lane == 0) atomicOr(g.err, kErrKvPlace);
+        return 0;
+    };
+    // the tile that starts at token t (t + 15 is in the same page: pages and tiles are whole sixteens)
+    auto fetch = [&](Tile<BITS, D> &x, int page, int t) {
+        const int at = t % g.page_tokens;
+        const uint8_t *kb = a.cache + g.codes_at(page, h, 0) + (int64_t)at * G::RB;
+        const uint8_t *vb = kb + (int64_t)g.page_tokens * G::RB;
+        const float *sc = reinterpret_cast<const float *>(a.cache + g.scales_at(page, h, 0)) + at;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) G::K::template load<4>(kb + (lg + 8 * i) * G::RB, lc, x.k[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) G::V::template load<8>(vb + (2 * lc + (i & 1) + 8 * (i >> 1)) * G::RB, lg, x.v[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x.rk[i] = __ldg(sc + lg + 8 * i);
+            x.rv[i] = __ldg(sc + g.page_tokens + lg + 8 * i);
+        }
+    };
+
+    auto work = [&](const Tile<BITS, D> &x, int t0) {
+        // scores of 16 tokens (rows lg, lg + 8 of the tile) by R query rows
+        float sc[NR][4];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) sc[nr][0] = sc[nr][1] = sc[nr][2] = sc[nr][3] = 0.0f;
+        const uint2 *qs = reinterpret_cast<const uint2 *>(qf) + lane;
+        auto score = [&](int ks, const uint32_t (&f)[4]) {
+#pragma unroll
+            for (int p = 0; p < TERMS; ++p)
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    const uint2 b = qs[((p * G::KS + ks) * NR + nr) * 32];
+                    mma16816(sc[nr], f, b.x, b.y);
+                }
+        };
+#pragma unroll
+        for (int w = 0; w < G::K::W; ++w) {
+            if constexpr (BITS == 8) {
+                uint32_t f[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f[i] = minus(__byte_perm(x.k[i][w], 0x64646464u, 0x4140), 0x64806480u);
+                    f[2 + i] = minus(__byte_perm(x.k[i][w], 0x64646464u, 0x4342), 0x64806480u);
+                }
+                score(w, f);
+            } else {
+                uint32_t f[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t y = x.k[i][w] >> (8 * m);
+                        f[m][i] = minus((y & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        f[m][2 + i] = bits_of(__hfma2(half2_of((y & 0x00f000f0u) | 0x64006400u), half2_of(0x2c002c00u),
+                                                      half2_of(0xd480d480u)));   // (1024 + 16 u) / 16 - 72
+                    }
+                score(2 * w, f[0]);
+                score(2 * w + 1, f[1]);
+            }
+        }
+        // weights
+        const float lr[2] = {fmaxf(__log2f(x.rv[0]), -60.0f), fmaxf(__log2f(x.rv[1]), -60.0f)};
+        bool far = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 2 * nr + (e & 1), i = e >> 1;
+                const float y = sc[nr][e] * x.rk[i] * lift[j];
+                sc[nr][e] = t0 + lg + 8 * i < limit[j] ? y : -INFINITY;
+                far = far || sc[nr][e] + lr[i] > ref[j] + kSlack;
+            }
+        if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+            for (int j = 0; j < 2 * NR; ++j) {
+                float m = fmaxf(sc[j / 2][j & 1] + lr[0], sc[j / 2][2 + (j & 1)] + lr[1]);
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                const float to = fmaxf(m, ref[j]);
+                const float f = to > ref[j] ? exp2f(ref[j] - to) : 1.0f;
+                ref[j] = to;
+                total[j] *= f;
+#pragma unroll
+                for (int mt = 0; mt < G::KS; ++mt) {
+                    acc[mt][j / 2][j & 1] *= f;
+                    acc[mt][j / 2][2 + (j & 1)] *= f;
+                }
+            }
+        }
+        uint32_t pb[TERMS][NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float wgt[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int j = 2 * nr + b;
+                    const float y = sc[nr][2 * i + b];
+                    const float p = exp2f(y - (ref[j] == -INFINITY ? 0.0f : ref[j]));
+                    total[j] += p;
+                    wgt[b] = y == -INFINITY ? 0.0f : p * x.rv[i];    // nothing of a masked row, whatever its scale
+                }
+                const __half2 hi = __floats2half2_rn(wgt[0], wgt[1]);
+                pb[0][nr][i] = transpose8(bits_of(hi));
+                if constexpr (TERMS == 2) {
+                    const float2 back = __half22float2(hi);
+                    pb[1][nr][i] = transpose8(bits_of(__floats2half2_rn(wgt[0] - back.x, wgt[1] - back.y)));
+                }
+            }
+        // sums
+        auto add = [&](int mt, const uint32_t (&f)[4]) {
+#pragma unroll
+            for (int p = 0; p < TERMS; ++p)
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) mma16816(acc[mt][nr], f, pb[p][nr][0], pb[p][nr][1]);
+        };
+#pragma unroll
+        for (int w = 0; w < G::V::W; ++w) {
+            if constexpr (BITS == 8) {
+                uint32_t f[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t lo = __byte_perm(x.v[2 * i][w], x.v[2 * i + 1][w], 0x5140);
+                    const uint32_t hi = __byte_perm(x.v[2 * i][w], x.v[2 * i + 1][w], 0x7362);
+                    f[0][2 * i] = minus(__byte_perm(lo, 0x64646464u, 0x4140), 0x64806480u);
+                    f[0][2 * i + 1] = minus(__byte_perm(lo, 0x64646464u, 0x4342), 0x64806480u);
+                    f[1][2 * i] = minus(__byte_perm(hi, 0x64646464u, 0x4140), 0x64806480u);
+                    f[1][2 * i + 1] = minus(__byte_perm(hi, 0x64646464u, 0x4342), 0x64806480u);
+                }
+                add(2 * w, f[0]);
+                add(2 * w + 1, f[1]);
+            } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t y = __byte_perm(x.v[2 * i][w], x.v[2 * i + 1][w], half ? 0x7632 : 0x5410);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t z = y >> (8 * m);
+                            f[m][2 * i] = minus((z & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                            f[m][2 * i + 1] = bits_of(__hfma2(half2_of((z & 0x00f000f0u) | 0x64006400u),
+                                                              half2_of(0x2c002c00u), half2_of(0xd480d480u)));
+                        }
+                    }
+                    add(4 * w + 2 * half, f[0]);
+                    add(4 * w + 2 * half + 1, f[1]);
+                }
+            }
+        }
+    };
+
+    {
+        Tile<BITS, D> x;
+        int t = begin + warp * kTile;
+        int page = page_of(t), page2 = page_of(t + kStep);
+        if (t < end) fetch(x, page, t);
+#pragma unroll 1
+        for (; t < end; t += kStep) {
+            Tile<BITS, D> y;
+            const int t2 = t + kStep;
+            page = page2;
+            page2 = page_of(t2 + kStep);
+            if (t2 < end) fetch(y, page, t2);
+            work(x, t);
+            x = y;
+        }
+    }
+
+    // join the warps, in order
+#pragma unroll
+    for (int j = 0; j < 2 * NR; ++j) {
+        total[j] += __shfl_xor_sync(0xffffffffu, total[j], 4);
+        total[j] += __shfl_xor_sync(0xffffffffu, total[j], 8);
+        total[j] += __shfl_xor_sync(0xffffffffu, total[j], 16);
+        const int r = 8 * (j / 2) + 2 * lc + j % 2;
+        float *out = join + (warp * G::R + r) * (D + 2);
+        if (lg == 0) {
+            out[D] = ref[j];
+            out[D + 1] = total[j];
+        }
+#pragma unroll
+        for (int mt = 0; mt < G::KS; ++mt) {
+            out[G::col_of(mt, 0, lg)] = acc[mt][j / 2][j & 1];
+            out[G::col_of(mt, 1, lg)] = acc[mt][j / 2][2 + (j & 1)];
+        }
+    }
+    __syncthreads();
+    for (int r = warp; r < nrow; r += kWarps) {
+        const float *in = join + r * (D + 2);
+        float m = -INFINITY, l = 0.0f, f[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, in[w * G::R * (D + 2) + D]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float y = in[w * G::R * (D + 2) + D];
+            f[w] = y == -INFINITY ? 0.0f : exp2f(y - m);
+            // a warp that saw only NaN rows keeps the reference -infinity and a NaN total
+            l += y == -INFINITY ? in[w * G::R * (D + 2) + D + 1] : f[w] * in[w * G::R * (D + 2) + D + 1];
+        }
+        const int i = (r0 + r) / group, hq = h * group + (r0 + r) % group;
+        const int64_t tok = (int64_t)s * a.n_tok + i;
+        float *part = a.n_splits > 1 ? a.part + ((unit * a.n_splits + split) * G::R + r) * (D + 2) : nullptr;
+        for (int c = lane; c < D; c += 32) {
+            float y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float z = in[w * G::R * (D + 2) + c];
+                y += f[w] == 0.0f ? 0.0f : f[w] * z;
+            }
+            if (part) {
+                part[c] = y;
+                continue;
+            }
+            y = l == 0.0f ? 0.0f : y / l;
+            const int64_t at = tok * a.os + (int64_t)hq * D + c;
+            if (a.dtype == 0) static_cast<float *>(a.o)[at] = y;
+            else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(y);
+            else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
+        }
+        if (lane == 0) {
+            if (part) {
+                part[D] = m;
+                part[D + 1] = l;
+            } else if (a.lse) {
+                a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m * kLn2 + logf(l));
+            }
+        }
+    }
+}
+
+// Joins the parts of a row, in order: a warp per row.
+__global__ void __launch_bounds__(128) k_kv_join(KvAttendArgs a, int R) {
+    const KvGeo &g = a.g;
+    const int lane = threadIdx.x & 31, D = g.d;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int group = a.Hq / g.H, rows = a.n_tok * group;
+    if (row >= (int64_t)a.n_seq * g.H * rows) return;
+    const int rr = (int)(row % rows);
+    const int64_t sh = row / rows;
+    const int h = (int)(sh % g.H), s = (int)(sh / g.H);
+    const int len = a.lens[s];
+    if (len < 0 || len > (int64_t)a.max_pages * g.page_tokens) return;
+    constexpr int kStep = kWarps * kTile;
+    const int per = (int)(((int64_t)len + (int64_t)a.n_splits * kStep - 1) / ((int64_t)a.n_splits * kStep)) * kStep;
+    const int parts = len == 0 ? 1 : (int)(((int64_t)len + per - 1) / per);
+    const float *in = a.part + ((sh * a.row_tiles + rr / R) * a.n_splits * R + rr % R) * (D + 2);
+    const int64_t step = (int64_t)R * (D + 2);
+    float m = -INFINITY;
+    for (int p = lane; p < parts; p += 32) m = fmaxf(m, in[p * step + D]);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    float l = 0.0f;
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < parts; ++p) {
+        const float *x = in + p * step;
+        const float e = x[D];
+        const float f = e == -INFINITY ? 0.0f : exp2f(e - m);
+        l += e == -INFINITY ? x[D + 1] : f * x[D + 1];
+        if (f != 0.0f)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c * 32 < D) y[c] += f * x[c * 32 + lane];
+    }
+    const int64_t tok = (int64_t)s * a.n_tok + rr / group;
+    const int hq = h * group + rr % group;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        if (c * 32 >= D) continue;
+        const float z = l == 0.0f ? 0.0f : y[c] / l;
+        const int64_t at = tok * a.os + (int64_t)hq * D + c * 32 + lane;
+        if (a.dtype == 0) static_cast<float *>(a.o)[at] = z;
+        else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(z);
+        else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(z);
+    }
+    if (lane == 0 && a.lse)
+        a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m * kLn2 + logf(l));
+}
+
+template <int BITS, int D, int NR, int TERMS>
+cudaError_t launch_one(const KvAttendArgs &a, cudaStream_t st) {
+    using G = Geo<BITS, D, NR>;
+    const int64_t blocks = (int64_t)a.n_seq * a.g.H * a.row_tiles * a.n_splits;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const size_t smem = (size_t)TERMS * G::KS * NR * 256 + G::R * 4 + (size_t)kWarps * G::R * (D + 2) * 4;
+    auto *kern = k_kv_attend<BITS, D, NR, TERMS>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<(unsigned)blocks, 32 * kWarps, smem, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && a.n_splits > 1) {
+        const int64_t rows = (int64_t)a.n_seq * a.n_tok * a.Hq;
+        k_kv_join<<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, G::R);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+template <int BITS, int D>
+cudaError_t launch_d(const KvAttendArgs &a, int nr, cudaStream_t st) {
+    if (a.dtype == 0) return nr == 1 ? launch_one<BITS, D, 1, 2>(a, st) : launch_one<BITS, D, 2, 2>(a, st);
+    return nr == 1 ? launch_one<BITS, D, 1, 1>(a, st) : launch_one<BITS, D, 2, 1>(a, st);
+}
+
+}  // namespace
+
+KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, int n_sms) {
+    KvSplit k;
+    const int64_t rows = (int64_t)n_tok * (Hq / g.H);
+    k.nr = rows <= 8 ? 1 : 2;
+    k.row_tiles = (int)((rows + 8 * k.nr - 1) / (8 * k.nr));
+    // about eight blocks for every SM, but no part shorter than four steps of a block
+    const int64_t units = (int64_t)n_seq * g.H * k.row_tiles, steps = (int64_t)max_pages * g.page_tokens / (kWarps * kTile);
+    int64_t n = units > 0 ? (8 * (int64_t)n_sms + units - 1) / units : 1;
+    if (n > (steps + 3) / 4) n = (steps + 3) / 4;
+    k.n_splits = n < 1 ? 1 : (int)n;
+    return k;
+}
+
+cudaError_t launch_kv_attend(const KvAttendArgs &a, int nr, cudaStream_t st) {
+    if (a.g.bits == 8) {
+        if (a.g.d == 64) return launch_d<8, 64>(a, nr, st);
+        if (a.g.d == 128) return launch_d<8, 128>(a, nr, st);
+        return launch_d<8, 256>(a, nr, st);
+    }
+    if (a.g.d == 64) return launch_d<4, 64>(a, nr, st);
+    if (a.g.d == 128) return launch_d<4, 128>(a, nr, st);
+    return launch_d<4, 256>(a, nr, st);
+}
+
+}  // namespace stepq

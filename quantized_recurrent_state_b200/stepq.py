@@ -28,7 +28,12 @@ EXPORTED = [
     "stepq_decode_step_noalloc", "stepq_plan_build_uniform", "stepq_ctx_set_wait_limit", "stepq_plan_slice", "stepq_prefill_fp32", "stepq_prefill",
     "stepq_prefill_workspace_bytes", "stepq_selftest_tc", "stepq_ctx_set_prefill_kernel",
     "stepq_ctx_set_step_kernel",
+    "stepq_delta_step", "stepq_delta_prefill", "stepq_ctx_wait_stream", "stepq_stream_wait_ctx",
+    "stepq_kv_create", "stepq_kv_free", "stepq_kv_bytes", "stepq_kv_append", "stepq_kv_read", "stepq_kv_attend",
+    "stepq_kv_attend_workspace_bytes", "stepq_kv_check",
 ]
+FP32, FP16, BF16 = 0, 1, 2   # types of token rows
+PAD = -1                     # slot or cache place of a padding request
 STEP_REGISTERS = 0    # fused step kernel: state in registers
 STEP_TMEM = 1         # fused step kernel: state in tensor memory (per-head plans, d = 128)
 PREFILL_MMA_SYNC = 0   # prefill kernel: mma.sync tiles, state in shared memory
@@ -58,6 +63,14 @@ class PlanInfo(ctypes.Structure):
 _lib = None
 P = ctypes.c_void_p
 I = ctypes.c_int
+I64 = ctypes.c_int64
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("n_qk_heads", ctypes.c_int), ("q", P), ("k", P), ("v", P), ("alpha", P), ("beta", P),
+        ("o", P), ("q_stride", I64), ("k_stride", I64), ("v_stride", I64), ("o_stride", I64),
+    ]
 
 
 def lib():
@@ -108,6 +121,21 @@ def lib():
         l.stepq_ctx_set_wait_limit.argtypes = [P, ctypes.c_uint32, ctypes.c_uint32]
         l.stepq_kernel_stats.argtypes = [P, P, P]
         l.stepq_decode_step_noalloc.argtypes = [P, P, P, I, I, I, P, P, P, P, P, P]
+        l.stepq_delta_step.argtypes = [P, I, P, P, I, I, ctypes.POINTER(Tokens)]
+        l.stepq_delta_prefill.argtypes = [P, I, P, P, P, I, P, I, ctypes.POINTER(Tokens)]
+        l.stepq_ctx_wait_stream.argtypes = [P, P]
+        l.stepq_stream_wait_ctx.argtypes = [P, P]
+        l.stepq_kv_create.argtypes = [I, I, I, I, I, ctypes.POINTER(P)]
+        l.stepq_kv_free.argtypes = [P]
+        l.stepq_kv_free.restype = None
+        l.stepq_kv_bytes.argtypes = [P]
+        l.stepq_kv_bytes.restype = ctypes.c_size_t
+        l.stepq_kv_append.argtypes = [P, P, I, I, P, P, I64, I64, P, P]
+        l.stepq_kv_read.argtypes = [P, P, I, P, I, P, P, I64, I, P, P, I64, I64, P]
+        l.stepq_kv_attend.argtypes = [P, P, I, P, I, P, I, I, I, P, I64, ctypes.c_float, P, I64, P, P, P]
+        l.stepq_kv_attend_workspace_bytes.argtypes = [P, I, I, I, I]
+        l.stepq_kv_attend_workspace_bytes.restype = ctypes.c_size_t
+        l.stepq_kv_check.argtypes = [P, P]
         _lib = l
     return _lib
 
@@ -122,6 +150,47 @@ def _ptr(t):
     if t is None:
         return None
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _dtype_codes():
+    import torch
+    return {torch.float32: FP32, torch.float16: FP16, torch.bfloat16: BF16}
+
+
+def _want(ok, msg):
+    if not ok:
+        raise StepqError(EINVAL, msg)
+
+
+def _on(t, device, name):
+    _want(t.is_cuda and t.device.index == device, f"{name} is on {t.device}, not on cuda:{device}")
+
+
+def _dense(t, device, dtype, numel, name):
+    """A contiguous device tensor of `numel` elements: its address."""
+    _on(t, device, name)
+    _want(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
+    _want(t.is_contiguous(), f"{name} is not contiguous")
+    _want(t.numel() == numel, f"{name} has {t.numel()} elements, not {numel}")
+    return t.data_ptr()
+
+
+def _row_stride(t, lead, heads, d, name):
+    """Stride in elements of the rows of t [*lead, heads, d], which have to lie evenly spaced."""
+    _want(tuple(t.shape) == (*lead, heads, d), f"{name} has the shape {tuple(t.shape)}, not {(*lead, heads, d)}")
+    st = t.stride()
+    _want((d == 1 or st[-1] == 1) and (heads == 1 or st[-2] == d), f"{name}: a row's heads are not contiguous")
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1:
+        _want(st[0] == lead[1] * st[1], f"{name}: the rows are not evenly spaced")
+        return st[1]
+    return next((s for n, s in zip(lead, st) if n > 1), heads * d)
+
+
+def _rows(t, device, dtype, lead, heads, d, name):
+    """Device token rows [*lead, heads, d]: (address, stride in elements)."""
+    _on(t, device, name)
+    _want(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
+    return t.data_ptr(), _row_stride(t, lead, heads, d, name)
 
 
 class Plan:
@@ -208,6 +277,7 @@ class Context:
                                       ctypes.byref(h)))
         self._h = h
         self.n_slots = n_slots
+        self.device = torch.cuda.current_device()
 
     def _after_caller(self):
         """Order the context's main stream after the caller's current torch
@@ -264,6 +334,60 @@ class Context:
         return _check(lib().stepq_prefill_fp32(self._h, _ptr(S), n_req, lb, le, int(T), _ptr(q), _ptr(k), _ptr(v),
                                                _ptr(alpha), _ptr(beta), _ptr(o), 1 if zero_init else 0))
 
+    def _delta(self, S, slots, n_seq, lead, q, k, v, alpha, beta, o):
+        """Checked arguments shared by delta_step and delta_prefill: (S, slots, Tokens)."""
+        import torch
+        p, dev = self.plan, self.device
+        code = _dtype_codes().get(q.dtype)
+        _want(code is not None, f"q is {q.dtype}: float32, float16 or bfloat16 tokens")
+        _want(q.dim() == len(lead) + 2, f"q has {q.dim()} dimensions")
+        hk, n_tok = q.shape[-2], lead[0] * (lead[1] if len(lead) > 1 else 1)
+        t = Tokens(dtype=code, n_qk_heads=hk)
+        t.q, t.q_stride = _rows(q, dev, q.dtype, lead, hk, p.d, "q")
+        t.k, t.k_stride = _rows(k, dev, q.dtype, lead, hk, p.d, "k")
+        t.v, t.v_stride = _rows(v, dev, q.dtype, lead, p.n_heads, p.d, "v")
+        t.o, t.o_stride = _rows(o, dev, q.dtype, lead, p.n_heads, p.d, "o")
+        t.alpha = _dense(alpha, dev, torch.float32, n_tok * p.n_heads * (p.d if p.mode else 1), "alpha")
+        t.beta = _dense(beta, dev, torch.float32, n_tok * p.n_heads, "beta")
+        per = p.n_heads * p.d * p.d
+        if slots is None:
+            return _dense(S, dev, torch.float32, n_seq * per, "S"), None, t
+        return (_dense(S, dev, torch.float32, self.n_slots * p.n_layers * per, "S"),
+                _dense(slots, dev, torch.int32, n_seq, "slots"), t)
+
+    def _ordered(self, call, *args):
+        """call(*args) on main, after the caller's current stream and before what it enqueues next."""
+        import torch
+        cur, l = torch.cuda.current_stream(self.device).cuda_stream, lib()
+        if cur == self.main.cuda_stream:
+            return _check(call(self._h, *args))
+        _check(l.stepq_ctx_wait_stream(self._h, cur))
+        _check(call(self._h, *args))
+        return _check(l.stepq_stream_wait_ctx(self._h, cur))
+
+    def delta_step(self, S, slots, q, k, v, alpha, beta, o, layer: int = 0):
+        """The gated delta rule for the next token(s) of every request: q, k [n_seq, n_tok, n_qk_heads, d],
+        v, o [n_seq, n_tok, n_heads, d] (float32, float16 or bfloat16; rows may be slices of wider ones),
+        alpha, beta as in stepq.h; S the fp32 pool (slots given) or [n_seq, n_heads, d, d], updated."""
+        _want(q.dim() == 4, f"q has {q.dim()} dimensions, not 4")
+        n, n_tok = q.shape[0], q.shape[1]
+        S, slots, t = self._delta(S, slots, n, (n, n_tok), q, k, v, alpha, beta, o)
+        return self._ordered(lib().stepq_delta_step, layer, S, slots, n, n_tok, ctypes.byref(t))
+
+    def delta_prefill(self, S, slots, cu_seqlens, q, k, v, alpha, beta, o, layer: int = 0, fresh=None):
+        """The gated delta rule over a ragged batch: sequence s has the rows [cu_seqlens[s], cu_seqlens[s + 1])
+        of q, k [n_tokens, n_qk_heads, d] and v, o [n_tokens, n_heads, d]; fresh [n_seq] uint8 or bool marks those
+        that start from a zero state."""
+        import torch
+        n = cu_seqlens.numel() - 1
+        _want(n >= 0, "cu_seqlens is empty")
+        cu = _dense(cu_seqlens, self.device, torch.int32, n + 1, "cu_seqlens")
+        if fresh is not None:
+            fresh = _dense(fresh, self.device, torch.bool if fresh.dtype == torch.bool else torch.uint8, n, "fresh")
+        tokens = q.shape[0]
+        S, slots, t = self._delta(S, slots, n, (tokens,), q, k, v, alpha, beta, o)
+        return self._ordered(lib().stepq_delta_prefill, layer, S, slots, fresh, n, cu, tokens, ctypes.byref(t))
+
     def set_step_kernel(self, kernel: int):
         return _check(lib().stepq_ctx_set_step_kernel(self._h, kernel))
 
@@ -313,6 +437,98 @@ class Context:
     def close(self):
         if getattr(self, "_h", None):
             lib().stepq_ctx_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """Geometry of a quantised key-value cache on the current CUDA device.  The cache itself is the caller's: a uint8
+    tensor of `bytes` bytes.  Calls run on the caller's current stream."""
+
+    def __init__(self, bits: int, n_heads: int, d: int, page_tokens: int, n_pages: int):
+        import torch
+        self._h = None
+        h = P()
+        _check(lib().stepq_kv_create(bits, n_heads, d, page_tokens, n_pages, ctypes.byref(h)))
+        self._h = h
+        self.bits, self.n_heads, self.d, self.page_tokens, self.n_pages = bits, n_heads, d, page_tokens, n_pages
+        self.device = torch.cuda.current_device()
+        self.bytes = int(lib().stepq_kv_bytes(h))
+
+    def _stream(self):
+        import torch
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _cache(self, cache):
+        import torch
+        return _dense(cache, self.device, torch.uint8, self.bytes, "cache")
+
+    def _table(self, page_table, lens):
+        import torch
+        _want(page_table.dim() == 2, f"page_table has {page_table.dim()} dimensions, not 2")
+        n, most = page_table.shape
+        return (n, _dense(page_table, self.device, torch.int32, n * most, "page_table"), most,
+                _dense(lens, self.device, torch.int32, n, "lens"))
+
+    def append(self, cache, k, v, places):
+        """Quantise the rows k, v [n_tokens, n_heads, d] into the cache at places [n_tokens] (int64)."""
+        import torch
+        code, n = _dtype_codes().get(k.dtype), k.shape[0]
+        _want(code is not None, f"k is {k.dtype}: float32, float16 or bfloat16")
+        kp, ks = _rows(k, self.device, k.dtype, (n,), self.n_heads, self.d, "k")
+        vp, vs = _rows(v, self.device, k.dtype, (n,), self.n_heads, self.d, "v")
+        places = _dense(places, self.device, torch.int64, n, "places")
+        return _check(lib().stepq_kv_append(self._h, self._cache(cache), code, n, kp, vp, ks, vs, places, self._stream()))
+
+    def read(self, cache, page_table, lens, cu_seqlens, k, v):
+        """Read the sequences back into the rows k, v [n_rows, n_heads, d], sequence s from row cu_seqlens[s] on."""
+        import torch
+        code, rows = _dtype_codes().get(k.dtype), k.shape[0]
+        _want(code is not None, f"k is {k.dtype}: float32, float16 or bfloat16")
+        n, table, most, lens = self._table(page_table, lens)
+        _on(cu_seqlens, self.device, "cu_seqlens")
+        _want(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= n,
+              f"cu_seqlens: {n} contiguous int32 row numbers (or {n + 1})")
+        kp, ks = _rows(k, self.device, k.dtype, (rows,), self.n_heads, self.d, "k")
+        vp, vs = _rows(v, self.device, k.dtype, (rows,), self.n_heads, self.d, "v")
+        return _check(lib().stepq_kv_read(self._h, self._cache(cache), n, table, most, lens, cu_seqlens.data_ptr(), rows, code,
+                                          kp, vp, ks, vs, self._stream()))
+
+    def attend(self, cache, q, page_table, lens, scale, o, workspace, lse=None):
+        """Attention of the newest tokens q [n_seq, n_tok, n_q_heads, d] over their sequences; o likewise, lse
+        [n_seq, n_tok, n_q_heads] float32 or None."""
+        import torch
+        _want(q.dim() == 4, f"q has {q.dim()} dimensions, not 4")
+        code, (n, n_tok, hq, _) = _dtype_codes().get(q.dtype), q.shape
+        _want(code is not None, f"q is {q.dtype}: float32, float16 or bfloat16")
+        rows, table, most, lens = self._table(page_table, lens)
+        _want(rows == n, f"page_table has {rows} rows for {n} sequences")
+        qp, qs = _rows(q, self.device, q.dtype, (n, n_tok), hq, self.d, "q")
+        op, os_ = _rows(o, self.device, q.dtype, (n, n_tok), hq, self.d, "o")
+        if lse is not None:
+            lse = _dense(lse, self.device, torch.float32, n * n_tok * hq, "lse")
+        _on(workspace, self.device, "workspace")
+        need = self.attend_workspace_bytes(n, n_tok, hq, most)
+        _want(workspace.is_contiguous() and workspace.numel() * workspace.element_size() >= need,
+              f"workspace: {need} contiguous bytes")
+        return _check(lib().stepq_kv_attend(self._h, self._cache(cache), n, table, most, lens, code, n_tok, hq, qp, qs,
+                                            scale, op, os_, lse, workspace.data_ptr(), self._stream()))
+
+    def attend_workspace_bytes(self, n_seq: int, n_tok: int, n_q_heads: int, max_pages: int) -> int:
+        return int(lib().stepq_kv_attend_workspace_bytes(self._h, n_seq, n_tok, n_q_heads, max_pages))
+
+    def check(self):
+        """Wait for the caller's current stream; raises if a call found a place, page or length out of range."""
+        return _check(lib().stepq_kv_check(self._h, self._stream()))
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().stepq_kv_free(self._h)
             self._h = None
 
     def __del__(self):

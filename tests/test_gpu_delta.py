@@ -1,0 +1,280 @@
+"""The served-layer gated delta rule on the GPU against the recurrence in 64 bits.
+
+Tolerance.  With |k| = 1, alpha <= 1 and beta <= 1 one token maps a column's
+error e to A e + delta with |A| <= 1, so errors add up and no more.  Token by
+token in fp32, delta has: the gate's rounding, a dot product of D / 8 fma and
+three additions (Cauchy: at most (D / 8 + 3) 2^-24 |S_j|), two roundings of u
+and one of the update; with C the largest column norm plus |v| on the way that
+is at most (D / 8 + 8) 2^-24 C a token, in the column's 2-norm.  k rows of 16-bit
+types are not unit vectors to the last bit: |k| <= 1 + 2^-8, so |A| <= 1 + 2^-6 in the worst
+direction; a factor of 4 covers it for the lengths tested with long memories
+(the contraction of the tested gates, alpha <= 2^(-1/40), outweighs it).
+o adds |q| times that, its own dot product, and half a step of its type.
+The chunked form is held to CHUNK_STEP for each of its tokens instead of (D / 8 + 8) 2^-24: see there.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def stepq():
+    from quantized_recurrent_state_b200 import build as qbuild
+    qbuild.build()
+    from quantized_recurrent_state_b200 import stepq as s
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return s
+
+
+def _inputs(seed, tokens, H, Hk, D, dtype, rows=False, wide=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    def n(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    def u(*s):
+        return torch.rand(*s, generator=g, device="cuda")
+    dt = TYPES[dtype]
+    pad = 3 * 8 if wide else 0
+    x = torch.full((tokens, (2 * Hk + H) * D + pad), float("nan"), dtype=dt, device="cuda")
+    q, k, v = (x[:, a * D:b * D].view(tokens, b - a, D) if tokens else x[:, a * D:b * D].reshape(0, b - a, D)
+               for a, b in ((0, Hk), (Hk, 2 * Hk), (2 * Hk, 2 * Hk + H)))
+    kk = n(tokens, Hk, D)
+    q.copy_(n(tokens, Hk, D) * D ** -0.5)
+    k.copy_(kk / kk.norm(dim=-1, keepdim=True))
+    v.copy_(n(tokens, H, D))
+    if not wide:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    alpha = torch.exp2(-1.0 / (1 + 39 * u(tokens, H, D) if rows else 1 + 39 * u(tokens, H)))
+    return dict(q=q, k=k, v=v, alpha=alpha, beta=u(tokens, H), o=torch.full((tokens, H, D), 7.0, dtype=dt, device="cuda"))
+
+
+def _reference(S, x, rows):
+    """S [H, D, D] float64 through the tokens of x: (S, o, C)."""
+    H = x["v"].shape[1]
+    rep = H // x["q"].shape[1]
+    out = []
+    C = S.norm(dim=1).max().item() if S.numel() else 0.0
+    for t in range(x["q"].shape[0]):
+        q, k = (x[n][t].double().repeat_interleave(rep, 0) for n in ("q", "k"))
+        a = x["alpha"][t].double()
+        S = S * (a.unsqueeze(-1) if rows else a.view(-1, 1, 1))
+        u = x["beta"][t].double().unsqueeze(-1) * (x["v"][t].double() - torch.einsum("hi,hij->hj", k, S))
+        S = S + k.unsqueeze(-1) * u.unsqueeze(-2)
+        out.append(torch.einsum("hi,hij->hj", q, S))
+        C = max(C, S.norm(dim=1).max().item() + x["v"][t].abs().max().item())
+    return S, torch.stack(out) if out else torch.zeros(0, H, S.shape[-1], dtype=torch.float64, device="cuda"), C
+
+
+def _slice(x, a, b):
+    return {n: y[a:b] for n, y in x.items()}
+
+
+def _check(S, o, S_ref, o_ref, C, tokens, D, dtype, q, step=None):
+    step = (D / 8 + 8) * 2.0 ** -24 if step is None else step
+    bound = 4 * max(tokens, 1) * step * C
+    es = (S.double() - S_ref).norm(dim=1).max().item()
+    assert es <= bound, (es, bound)
+    if tokens:
+        half = torch.finfo(TYPES[dtype]).eps / 2
+        qn = q.double().norm(dim=-1).max().item()
+        eo = ((o.double() - o_ref).abs() - half * o_ref.abs()).max().item()
+        assert eo <= qn * (bound + (D / 8 + 4) * 2.0 ** -24 * C) + 2.0 ** -25 * (dtype == "fp16"), (eo, bound, qn)
+    return es / max(C, 1e-30)
+
+
+def _ctx(stepq, H, D, n_slots, rows=False, layers=1):
+    return stepq.Context(stepq.Plan.build_uniform(1 if rows else 0, layers, H, D, 6), n_slots)
+
+
+@pytest.mark.parametrize("D, rows", [(16, False), (32, False), (64, False), (128, False), (128, True)])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("n_tok", [1, 3])
+def test_step(stepq, D, rows, dtype, n_tok):
+    n, H, Hk = 3, 6, 2
+    ctx = _ctx(stepq, H, D, 5, rows, layers=2)
+    x = _inputs(1, n * n_tok, H, Hk, D, dtype, rows, wide=True)
+    pool = torch.randn(5, 2, H, D, D, device="cuda")
+    before = pool.clone()
+    slots = torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda")
+    y = {m: t.unflatten(0, (n, n_tok)) for m, t in x.items()}
+    ctx.delta_step(pool, slots, y["q"], y["k"], y["v"], y["alpha"], y["beta"], y["o"], layer=1)
+    ctx.sync()
+    for r, slot in enumerate([4, 0, 2]):
+        part = _slice(x, r * n_tok, (r + 1) * n_tok)
+        S, o, C = _reference(before[slot, 1].double(), part, rows)
+        _check(pool[slot, 1], part["o"], S, o, C, n_tok, D, dtype, part["q"])
+    assert torch.equal(pool[:, 0], before[:, 0])                       # the other layer
+    assert torch.equal(pool[[1, 3]], before[[1, 3]])                   # idle slots
+
+
+LENS = [[1], [0], [5, 0, 64, 130, 1], [63, 65, 128], [200]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("dtype, D, rows", [("bf16", 128, False), ("fp16", 128, False), ("fp32", 128, False), ("bf16", 128, True),
+                                            ("bf16", 64, False), ("fp16", 16, False)])
+def test_prefill_ragged(stepq, lens, dtype, D, rows):
+    n, H, Hk = len(lens), 4, 2
+    ctx = _ctx(stepq, H, D, n + 1, rows)
+    x = _inputs(2, sum(lens), H, Hk, D, dtype, rows, wide=True)
+    pool = torch.randn(n + 1, 1, H, D, D, device="cuda")
+    before = pool.clone()
+    order = torch.randperm(n + 1, generator=torch.Generator().manual_seed(3))[:n].tolist()
+    cu = np.cumsum([0] + lens).tolist()
+    fresh = torch.tensor([i % 2 == 1 for i in range(n)], device="cuda")
+    ctx.delta_prefill(pool, torch.tensor(order, dtype=torch.int32, device="cuda"),
+                      torch.tensor(cu, dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"], x["alpha"], x["beta"],
+                      x["o"], fresh=fresh)
+    ctx.sync()
+    for s, slot in enumerate(order):
+        part = _slice(x, cu[s], cu[s + 1])
+        S0 = torch.zeros_like(before[slot, 0]) if fresh[s] else before[slot, 0]
+        S, o, C = _reference(S0.double(), part, rows)
+        if lens[s] == 0:
+            assert torch.equal(pool[slot, 0], S0)
+        _check(pool[slot, 0], part["o"], S, o, C, lens[s], D, dtype, part["q"])
+    idle = [i for i in range(n + 1) if i not in order]
+    assert torch.equal(pool[idle], before[idle])
+
+
+def test_prefill_dense_states_and_one_head_group(stepq):
+    """slots None: states [n_seq][H][D][D]; every value head with its own q and k."""
+    lens, H, D = [70, 3], 3, 128
+    ctx = _ctx(stepq, H, D, 1)
+    x = _inputs(4, 73, H, H, D, "bf16")
+    S = torch.randn(2, H, D, D, device="cuda")
+    before = S.clone()
+    ctx.delta_prefill(S, None, torch.tensor([0, 70, 73], dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"],
+                      x["alpha"], x["beta"], x["o"])
+    ctx.sync()
+    for s, (a, b) in enumerate([(0, 70), (70, 73)]):
+        part = _slice(x, a, b)
+        R, o, C = _reference(before[s].double(), part, False)
+        _check(S[s], part["o"], R, o, C, b - a, D, "bf16", part["q"])
+
+
+def test_padding_and_bad_slots(stepq):
+    n, H, D = 4, 2, 128
+    ctx = _ctx(stepq, H, D, 3)
+    x = _inputs(5, n, H, 1, D, "bf16")
+    y = {m: t.unflatten(0, (n, 1)) for m, t in x.items()}
+    pool = torch.randn(3, 1, H, D, D, device="cuda")
+    before = pool.clone()
+    args = [y[m] for m in ("q", "k", "v", "alpha", "beta", "o")]
+    ctx.delta_step(pool, torch.tensor([1, stepq.PAD, 0, stepq.PAD], dtype=torch.int32, device="cuda"), *args)
+    ctx.sync()
+    assert torch.equal(pool[2], before[2])
+    assert (x["o"][[1, 3]] == 7.0).all() and not (x["o"][[0, 2]] == 7.0).all()
+    for bad in (3, -2):
+        before = pool.clone()
+        x["o"].fill_(7.0)
+        ctx.delta_step(pool, torch.tensor([2, bad, stepq.PAD, stepq.PAD], dtype=torch.int32, device="cuda"), *args)
+        with pytest.raises(stepq.StepqError, match="slot out of range"):
+            ctx.sync()
+        assert torch.equal(pool[:2], before[:2]) and (x["o"][1:] == 7.0).all()
+        ctx.sync()                                                     # the word was cleared
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_prefill_bad_ranges_and_gates(stepq, dtype):
+    H, D = 2, 128
+    ctx = _ctx(stepq, H, D, 3)
+    x = _inputs(6, 90, H, 1, D, dtype)
+    pool = torch.randn(3, 1, H, D, D, device="cuda")
+    before = pool.clone()
+    slots = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    args = [x[m] for m in ("q", "k", "v", "alpha", "beta", "o")]
+    for cu in ([0, 80, 70, 90], [-5, 10, 20, 90], [0, 10, 20, 91]):
+        ctx.delta_prefill(pool, slots, torch.tensor(cu, dtype=torch.int32, device="cuda"), *args)
+        with pytest.raises(stepq.StepqError, match="sequence outside"):
+            ctx.sync()
+        ok = [s for s in range(3) if 0 <= cu[s] <= cu[s + 1] <= 90]
+        bad = [s for s in range(3) if s not in ok]
+        assert torch.equal(pool[bad], before[bad])
+        pool.copy_(before)
+    for gate in (0.0, -0.5, 1.5, float("nan")):
+        alpha = x["alpha"].clone()
+        alpha[33, 1] = gate
+        ctx.delta_prefill(pool, slots, torch.tensor([0, 10, 70, 90], dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"],
+                          alpha, x["beta"], x["o"])
+        with pytest.raises(stepq.StepqError, match="gate out of range"):
+            ctx.sync()
+        S, o, C = _reference(before[0, 0].double(), _slice(x, 0, 10), False)
+        _check(pool[0, 0], x["o"][:10], S, o, C, 10, D, dtype, x["q"], step=CHUNK_STEP)
+        pool.copy_(before)
+
+
+CHUNK_STEP = 24 * 2.0 ** -24
+
+
+def test_refusals(stepq):
+    H, D = 4, 64
+    ctx = _ctx(stepq, H, D, 2)
+    x = _inputs(7, 4, H, 2, D, "bf16")
+    y = {m: t.unflatten(0, (2, 2)) for m, t in x.items()}
+    pool = torch.zeros(2, 1, H, D, D, device="cuda")
+    slots = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+
+    def call(**kw):
+        a = {**y, "pool": pool, "slots": slots, "layer": 0, **kw}
+        ctx.delta_step(a["pool"], a["slots"], a["q"], a["k"], a["v"], a["alpha"], a["beta"], a["o"], layer=a["layer"])
+
+    for kw in (dict(layer=1), dict(layer=-1), dict(q=y["q"].double()), dict(k=y["k"].float()), dict(v=y["v"][:, :, :3]),
+               dict(o=y["o"].transpose(0, 1)), dict(alpha=y["alpha"].half()), dict(beta=y["beta"][:1]),
+               dict(slots=slots.long()), dict(slots=slots[:1]), dict(pool=pool[:1]), dict(pool=pool.bfloat16()),
+               dict(q=y["q"].cpu()), dict(q=y["q"][:, :, :1].expand(2, 2, 2, D)),
+               dict(q=y["q"].repeat(1, 1, 2, 1)[:, :, :3], k=y["k"].repeat(1, 1, 2, 1)[:, :, :3])):
+        with pytest.raises(stepq.StepqError) as e:
+            call(**kw)
+        assert e.value.code == stepq.EINVAL, kw.keys()
+    # rows that are not a multiple of 16 bytes apart, and a pointer off a 16-byte boundary
+    odd = torch.zeros(4, 2 * D + 4, dtype=torch.bfloat16, device="cuda")
+    for q in (odd[:, :2 * D], odd.flatten()[4:4 + 4 * 2 * D].view(4, 2 * D)):
+        with pytest.raises(stepq.StepqError) as e:
+            call(q=q.unflatten(1, (2, D)).unflatten(0, (2, 2)))
+        assert e.value.code == stepq.EINVAL
+    assert ctx.launches == 0
+    ctx.delta_step(pool, slots[:0], *(y[m][:0] for m in ("q", "k", "v", "alpha", "beta", "o")))     # no requests: nothing to do
+    assert ctx.launches == 0
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_captured_and_replayed_on_another_stream(stepq, many):
+    """A captured call replays on new inputs; the caller's streams need no hand-made ordering."""
+    lens, H, D = ([100, 20] if many else [1, 1]), 2, 128
+    ctx = _ctx(stepq, H, D, 2)
+    x = _inputs(8, sum(lens), H, 2, D, "bf16")
+    S = torch.randn(2, 1, H, D, D, device="cuda")
+    S0 = S.clone()
+    slots = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32, device="cuda")
+
+    def call():
+        if many:
+            ctx.delta_prefill(S, slots, cu, x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["o"])
+        else:
+            ctx.delta_step(S, slots, *(x[m].unsqueeze(1) for m in ("q", "k", "v", "alpha", "beta", "o")))
+
+    call()
+    torch.cuda.synchronize()
+    first_S, first_o = S.clone(), x["o"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    S.copy_(S0)
+    x["o"].fill_(7.0)
+    graph.replay()
+    assert torch.equal(S, first_S) and torch.equal(x["o"], first_o)    # bit for bit, in stream order
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        S.copy_(S0)
+        x["v"].mul_(2.0)
+        call()
+        got = S.clone()
+    other.synchronize()
+    R, _, C = _reference(S0[1, 0].double(), _slice(x, 0, lens[0]), False)
+    _check(got[1, 0], x["o"][:lens[0]], R, _, C, lens[0], D, "bf16", x["q"], step=CHUNK_STEP)
