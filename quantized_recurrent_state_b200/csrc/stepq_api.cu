@@ -1214,7 +1214,9 @@ extern "C" int stepq_delta_prefill(stepq_ctx *c, int layer, float *S, const int3
     const stepq::DeviceScope dev(c->device);
     if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
     LaunchTimer lt(c, 4, c->main);
-    const cudaError_t e = stepq::launch_delta_seq(c->plan->D, tokens->dtype, c->plan->mode == 1, a, c->main);
+    const bool chunked = c->plan->D == 128 && c->plan->mode == 0 && tokens->dtype != STEPQ_FP32;
+    const cudaError_t e = chunked ? stepq::launch_delta_chunk(tokens->dtype, a, c->main)
+                                  : stepq::launch_delta_seq(c->plan->D, tokens->dtype, c->plan->mode == 1, a, c->main);
     if (e != cudaSuccess) return cuda_fail(e, "delta_prefill launch");
     lt.done();
     return STEPQ_OK;

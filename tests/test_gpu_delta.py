@@ -10,7 +10,14 @@ types are not unit vectors to the last bit: |k| <= 1 + 2^-8, so |A| <= 1 + 2^-6 
 direction; a factor of 4 covers it for the lengths tested with long memories
 (the contraction of the tested gates, alpha <= 2^(-1/40), outweighs it).
 o adds |q| times that, its own dot product, and half a step of its type.
-The chunked form is held to CHUNK_STEP for each of its tokens instead of (D / 8 + 8) 2^-24: see there.
+
+The chunked form (d = 128, per-head gates, 16-bit tokens, prompts) sums in another order, and takes S, U and the
+triangular inverse as two bfloat16 terms (2^-18 of each value is left out).  For one token that is
+2^-18 |S_j| of k^T S, 2^-17 (128 fp32 additions), and twice two terms of the solve, whose rows sum to at most 2 for the
+tested gates: 2^-15 C together at the worst.  Those are roundings of different values from token to token, so they add up as
+the root of the number of tokens.  Its readout of bfloat16 tokens takes S, U and A rounded once (2^-8 at the worst, half of that
+on average, each against |q| C): 2^-6 |q| C is above the three together, and a
+wrong term is of the order |q| C.  That of fp16 tokens takes two terms of each: 2^-13 |q| C.
 """
 import numpy as np
 import pytest
@@ -72,16 +79,16 @@ def _slice(x, a, b):
     return {n: y[a:b] for n, y in x.items()}
 
 
-def _check(S, o, S_ref, o_ref, C, tokens, D, dtype, q, step=None):
-    step = (D / 8 + 8) * 2.0 ** -24 if step is None else step
-    bound = 4 * max(tokens, 1) * step * C
+def _check(S, o, S_ref, o_ref, C, tokens, D, dtype, q, chunked=False):
+    bound = 2.0 ** -15 * max(tokens, 1) ** 0.5 * C if chunked else 4 * max(tokens, 1) * (D / 8 + 8) * 2.0 ** -24 * C
     es = (S.double() - S_ref).norm(dim=1).max().item()
     assert es <= bound, (es, bound)
     if tokens:
         half = torch.finfo(TYPES[dtype]).eps / 2
         qn = q.double().norm(dim=-1).max().item()
         eo = ((o.double() - o_ref).abs() - half * o_ref.abs()).max().item()
-        assert eo <= qn * (bound + (D / 8 + 4) * 2.0 ** -24 * C) + 2.0 ** -25 * (dtype == "fp16"), (eo, bound, qn)
+        own = (D / 8 + 4) * 2.0 ** -24 if not chunked else 2.0 ** -6 if dtype == "bf16" else 2.0 ** -13
+        assert eo <= qn * (bound + own * C) + 2.0 ** -25 * (dtype == "fp16"), (eo, bound, qn)
     return es / max(C, 1e-30)
 
 
@@ -110,7 +117,7 @@ def test_step(stepq, D, rows, dtype, n_tok):
     assert torch.equal(pool[[1, 3]], before[[1, 3]])                   # idle slots
 
 
-LENS = [[1], [0], [5, 0, 64, 130, 1], [63, 65, 128], [200]]
+LENS = [[1], [0], [5, 0, 64, 130, 1], [63, 65, 128], [200], [450, 2]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=str)
@@ -135,7 +142,7 @@ def test_prefill_ragged(stepq, lens, dtype, D, rows):
         S, o, C = _reference(S0.double(), part, rows)
         if lens[s] == 0:
             assert torch.equal(pool[slot, 0], S0)
-        _check(pool[slot, 0], part["o"], S, o, C, lens[s], D, dtype, part["q"])
+        _check(pool[slot, 0], part["o"], S, o, C, lens[s], D, dtype, part["q"], D == 128 and not rows and dtype != "fp32")
     idle = [i for i in range(n + 1) if i not in order]
     assert torch.equal(pool[idle], before[idle])
 
@@ -153,7 +160,7 @@ def test_prefill_dense_states_and_one_head_group(stepq):
     for s, (a, b) in enumerate([(0, 70), (70, 73)]):
         part = _slice(x, a, b)
         R, o, C = _reference(before[s].double(), part, False)
-        _check(S[s], part["o"], R, o, C, b - a, D, "bf16", part["q"])
+        _check(S[s], part["o"], R, o, C, b - a, D, "bf16", part["q"], chunked=True)
 
 
 def test_padding_and_bad_slots(stepq):
@@ -203,11 +210,8 @@ def test_prefill_bad_ranges_and_gates(stepq, dtype):
         with pytest.raises(stepq.StepqError, match="gate out of range"):
             ctx.sync()
         S, o, C = _reference(before[0, 0].double(), _slice(x, 0, 10), False)
-        _check(pool[0, 0], x["o"][:10], S, o, C, 10, D, dtype, x["q"], step=CHUNK_STEP)
+        _check(pool[0, 0], x["o"][:10], S, o, C, 10, D, dtype, x["q"], chunked=dtype != "fp32")
         pool.copy_(before)
-
-
-CHUNK_STEP = 24 * 2.0 ** -24
 
 
 def test_refusals(stepq):
@@ -276,5 +280,47 @@ def test_captured_and_replayed_on_another_stream(stepq, many):
         call()
         got = S.clone()
     other.synchronize()
-    R, _, C = _reference(S0[1, 0].double(), _slice(x, 0, lens[0]), False)
-    _check(got[1, 0], x["o"][:lens[0]], R, _, C, lens[0], D, "bf16", x["q"], step=CHUNK_STEP)
+    R, o, C = _reference(S0[1, 0].double(), _slice(x, 0, lens[0]), False)
+    _check(got[1, 0], x["o"][:lens[0]], R, o, C, lens[0], D, "bf16", x["q"], chunked=many)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_prefill_masked_rows_and_fast_gates(stepq, dtype):
+    """What stands behind a sequence's last token (another sequence's NaN and infinite rows) does not reach it; gates that
+    forget within a token and gates of exactly 1 neither overflow nor underflow into NaN."""
+    lens, H, D = [70, 30, 65], 3, 128
+    ctx = _ctx(stepq, H, D, 3)
+    x = _inputs(9, sum(lens), H, 1, D, dtype)
+    x["alpha"][:, 0] = 1e-30
+    x["alpha"][:, 1] = 1.0
+    x["alpha"][::2, 2] = 1e-3
+    for m in ("q", "k", "v"):
+        x[m][70:100:2] = float("nan")
+        x[m][71:100:2] = float("inf")
+    S = torch.randn(3, H, D, D, device="cuda")
+    before = S.clone()
+    ctx.delta_prefill(S, None, torch.tensor([0, 70, 100, 165], dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"],
+                      x["alpha"], x["beta"], x["o"])
+    ctx.sync()
+    assert torch.isnan(S[1]).any()
+    for s, (a, b) in ((0, (0, 70)), (2, (100, 165))):
+        part = _slice(x, a, b)
+        R, o, C = _reference(before[s].double(), part, False)
+        _check(S[s], part["o"], R, o, C, b - a, D, dtype, part["q"], chunked=True)
+
+
+def test_prefill_zero_beta_leaves_the_state(stepq):
+    """alpha = 1, beta = 0: S stays what it was, bit for bit, and o = S^T q."""
+    H, D = 2, 128
+    ctx = _ctx(stepq, H, D, 1)
+    x = _inputs(10, 150, H, 2, D, "bf16")
+    x["alpha"].fill_(1.0)
+    x["beta"].zero_()
+    S = torch.randn(1, H, D, D, device="cuda")
+    before = S.clone()
+    ctx.delta_prefill(S, None, torch.tensor([0, 150], dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"],
+                      x["alpha"], x["beta"], x["o"])
+    ctx.sync()
+    assert torch.equal(S, before)
+    ref = torch.einsum("thi,hij->thj", x["q"].double(), before[0].double())
+    assert ((x["o"].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -6 * 2).all()
