@@ -10,7 +10,9 @@
 
 namespace stepq {
 
-constexpr int kErrSeq = 32;  // device error word: a sequence's token range is not within the batch
+// device error word
+constexpr int kErrSeq = 32;    // a sequence's token range is not within the batch
+constexpr int kErrRange = 64;  // the chunked form left the range of its operands
 
 struct DeltaArgs {
     float *S;               // slots: [n_slots][n_layers][H][D][D]; else [n_seq][H][D][D]

@@ -1,32 +1,37 @@
 // The gated delta rule over a ragged batch in chunks of 64 tokens on the fifth-generation tensor
 // cores: d = 128, per-head gates, bfloat16 or fp16 tokens, fp32 states.
 //
-// With gamma_t the running product of the gates in a chunk, Gamma_ts = gamma_t / gamma_s and
-// S_0 the state before it:
-//   N_ts = beta_t Gamma_ts k_t.k_s (s < t),  T = (I + N)^-1 diag(beta)
-//   U = T (V - diag(gamma) K S_0)
-//   O = diag(gamma) Q S_0 + A U,  A_ts = Gamma_ts q_t.k_s (s <= t)
-//   S_C = gamma_C S_0 + K^T diag(gamma_C / gamma) U
+// With gamma_t the running product of the gates in a chunk, Gamma_ts = gamma_t / gamma_s and S the
+// state before it; k'_t = k_t / ks_t and q'_t = q_t / qs_t, ks_t and qs_t powers of two that bring
+// the row's largest value to [1, 2); u'_t = ks_t u_t:
+//   X = (I + N)^-1,  N_ts = beta_t ks_t^2 Gamma_ts k'_t.k'_s (s < t)
+//   U' = X R,        R_t = beta_t ks_t (v_t - gamma_t ks_t S^T k'_t)
+//   O_t = qs_t (gamma_t S^T q'_t + sum_s A_ts u'_s),  A_ts = Gamma_ts q'_t.k'_s (s <= t)
+//   S  <- gamma_C S + K'^T diag(gamma_C / gamma) U'
 // Every Gamma is at most 1, so nothing overflows however fast a gate decays.
 //
+// Precision: q' and k' are exact fp16 operands (bfloat16 tokens: to 2^-25 of the row's largest value).  fp32
+// operands (S, R, U', X) enter as the sum of two fp16 values, 2^-22 of the value: each value column's S, and its R and U',
+// are scaled by a power of two taken from an upper bound, which may be 2^13 too large before a bit is
+// lost.  Accumulators are fp32, S is held in fp32.  The readout uses the leading terms alone for bfloat16
+// outputs (2^-12 of a term against their own 2^-9) and both terms for fp16.  X stays below 2^5 while beta |k|^2 <= 2, where the recurrence
+// does not grow; a chunk whose X or U' leaves fp16 sets kErrRange.
+//
 // One block per (sequence, head) walks the chunks; blocks of heads that share k and q are neighbours.  The
-// chain S_0 -> U -> S_C is serial, so the block is split by what it waits for:
-//   warps 0-7  (state)  thread = value column j and half of the key rows: S in 64 registers, fp32.
-//   warps 8-11 (prepare) the next chunk: loads, gates, K K^T and Q K^T, the triangular inverse, A.
-// All products are tcgen05 with the value columns j in the lanes (W^T = S^T K^T and so on), so what
-// one product leaves in a thread's lane is what the thread feeds to the next one.
+// chain S -> R -> U' -> S is serial, so the block is split by what it waits for:
+//   warps 0-7  (state)   thread = value column j and half of the key rows: S in registers; R, U', S as operands;
+//                        thread 0 issues the products that need them
+//   warps 8-15 (prepare) the next chunk's loads, scales, gates, [K; Q] K^T, X, A; the last chunk's output
+// The register file is split 168 : 88 between them (2 x 168 + 2 x 88 = 4 x 128 in each quarter of the SM).
+// The value columns j are the lanes of every product (W^T = S^T K'^T and so on), so what a
+// product leaves in a thread's lane is what the thread feeds to the next one.
 //
-// Precision: bfloat16 tokens are exact operands; fp32 operands (S, U, T, V - gamma K S) enter as the sum of
-// two bfloat16 values (2^-18 of the value is left out), accumulators are fp32.  The readout uses the leading term
-// alone for bfloat16 outputs (2^-9 of a term, as the output's own rounding) and both for fp16.  fp16 tokens are the
-// sum of two bfloat16 values exactly.
+// Tensor memory columns: S^T terms 0-127 (hi, lo, two values a column), later diag(gamma_C / gamma) U' (0-63) and U'
+// (64-127); W^T 128-191 and R terms 192-255, later the state's increment; Y^T = S^T Q'^T 256-383, two chunks;
+// U'^T 384-447, later A U'; [K; Q] K^T 448-511.
 //
-// Tensor memory: S^T terms 0-127 (hi, lo, two values a column), W^T | Y^T 128-255 and later the state's
-// increment, the right side's terms 256-319 and later U's, U^T 320-383 and later A U, (U f)^T terms 384-447,
-// [K; Q] K^T 448-511.  All 512 columns, one block per SM.
-//
-// Every wait is bounded: a wait that gives up sets kErrWait, its group leaves the loop together, and the other
-// group's waits run out in turn.
+// Every wait is bounded: a wait that gives up ends its warp's or group's part and sets kErrWait; what waits for that
+// part gives up in turn.
 #include <type_traits>
 
 #include "stepq_dev.cuh"
@@ -38,41 +43,84 @@ namespace stepq {
 
 namespace {
 
-constexpr int D = 128, C = 64, NS = 256, NP = 128, NT = NS + NP;
+constexpr int D = 128, C = 64, NS = 256, NP = 256, NT = NS + NP;
 constexpr uint32_t kPolls = 1u << 22;
-constexpr uint32_t TSH = 0, TSL = 64, TWY = 128, TR = 256, TU = 320, TF = 384, TG = 448;
+constexpr uint32_t TSH = 0, TSL = 64, TFH = 0, TFL = 32, TUH = 64, TUL = 96, TW = 128, TRH = 192, TRL = 224, TD = 128, TY = 256,
+                   TU = 384, TG = 448;
 constexpr uint32_t kHalf = 128 * 128;   // bytes of 64 columns of [K; Q]
-constexpr uint32_t kTerm = 2 * kHalf;   // bytes of one term of [K; Q]
-constexpr int SN = C + 4;               // row stride of the fp32 scratch matrices
+constexpr int SN = C + 4;               // row stride of the fp32 scratch matrix
+constexpr int kTopS = 13, kTopR = 6;    // the scaled bounds of S and R are 2^kTop
+constexpr float kHalfMax = 65504.0f, kFloatMax = 3.402823466e38f;
 
-// KT: bfloat16 terms of a token value (1: bfloat16 tokens, 2: fp16 tokens).  VB: buffers of V.
-template <int KT>
+template <class T>
 struct Smem {
-    static constexpr int VB = 3 - KT;
-    alignas(1024) uint8_t kq[2][KT * kTerm];   // [buffer][term][column half][K rows, Q rows][128 bytes]
-    alignas(1024) uint8_t t[2][2 * C * 128];   // T, two terms
-    alignas(1024) uint8_t a[2][KT * C * 128];  // A, KT terms
-    alignas(16) uint16_t v[VB][C * D];
+    static constexpr int AT = std::is_same<T, __half>::value ? 2 : 1;   // terms of A (and of S and U' in the readout)
+    alignas(1024) uint8_t kq[2][2 * kHalf];    // [buffer][column half][K rows, Q rows][128 bytes]
+    alignas(1024) uint8_t x[2][2 * C * 128];   // X, two terms
+    alignas(1024) uint8_t a[2][AT * C * 128];  // A
+    alignas(16) T v[2][C * D];                 // V, later the chunk's output
     alignas(16) float n[C * SN];               // N, its inverse in place
-    alignas(16) float gam[2][C], f[2][C];
-    alignas(16) float lg[C], beta[C];
-    alignas(8) uint64_t full[2], ready[2], empty[2], v_free, wy, u, d, z, g, drain[2];
+    alignas(16) float gk[2][C], bk[2][C];      // gamma ks, beta ks
+    alignas(16) float f[2][C];                 // gamma_C / gamma
+    alignas(16) float go[2][C], qs[2][C];      // gamma qs, qs
+    alignas(16) float ks[C], lg[C], be[C];     // prepare's own: ks, log2 gamma, beta ks^2
+    float gl[2], mb[2], mg[2];                 // gamma_C, the largest beta ks, the largest gamma ks
+    float smx[2][D], vmx[2][D], umx[2][D];     // largest |S|, |v|, |u'| of a lane, by half
+    float ss[2][D], sr[2][D];                  // a lane's scales of the S and R terms
+    alignas(8) uint64_t full[2], ready[2], empty[2], sput, rput, uput, wy, u, d, z, g, out, drain[2];
     uint32_t taddr;
 };
 
 __device__ __forceinline__ void mbar_init_n(uint64_t *bar, uint32_t n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc::smem_addr(bar)), "r"(n) : "memory");
 }
-
-// 16 bytes of global memory into shared memory, or zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool take) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+// A warp's wait: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kPolls));
 }
+// 16 bytes of global memory into shared memory, or zeros.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_addr(dst)), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair_of(const uint32_t *v, int i) {
+    return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
+// The power of two that brings `bound` (>= 0) to at most 2^top (bounds below 2^-86 as 2^-86), and its inverse.
+__device__ __forceinline__ void scale_for(float bound, int top, float &s, float &inv) {
+    const int e = min(max((int)(__float_as_uint(bound) >> 23), 41), 240) + 1 - top;
+    s = __uint_as_float((uint32_t)e << 23);
+    inv = __uint_as_float((uint32_t)(254 - e) << 23);
+}
+// The power of two at or below x (0, infinity, NaN: 1), within 2^+-100.
+__device__ __forceinline__ int exponent_of(float x) {
+    const int e = (int)(__float_as_uint(x) >> 23);
+    return e == 0 || e == 255 ? 127 : min(max(e, 27), 227);
+}
+template <class T>
+struct Pair;
+template <>
+struct Pair<__half> {
+    using type = __half2;
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    using type = __nv_bfloat162;
+};
+__device__ __forceinline__ float2 to_f32x2(__half2 x) { return __half22float2(x); }
+__device__ __forceinline__ float2 to_f32x2(__nv_bfloat162 x) { return __bfloat1622float2(x); }
 
-template <int KT, class T>
+template <class T>
 __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
-    using Sm = Smem<KT>;
+    using Sm = Smem<T>;
+    using T2 = typename Pair<T>::type;
+    constexpr bool TWO = Sm::AT == 2;
     Sm &sm = *reinterpret_cast<Sm *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int s = blockIdx.x / a.H, h = blockIdx.x % a.H, hk = h / (a.H / a.Hk);
@@ -94,7 +142,8 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             mbar_init_n(&sm.ready[b], NP);
             mbar_init_n(&sm.empty[b], NS);
         }
-        mbar_init_n(&sm.v_free, NS);
+        for (uint64_t *b : {&sm.sput, &sm.rput, &sm.uput}) mbar_init_n(b, NS);
+        mbar_init_n(&sm.out, NP);
         for (uint64_t *b : {&sm.wy, &sm.u, &sm.d, &sm.z, &sm.g, &sm.drain[0], &sm.drain[1]}) mbar_init_n(b, 1);
         fence_mbar_init();
     }
@@ -107,307 +156,389 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
 
     if (warp < NS / 32) {
         // ---- state ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         const int hh = warp >> 2, j = 32 * (warp & 3) + lane;   // key rows [64 hh, 64 hh + 64), value column
         const uint32_t quad = tm + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t kq0 = tc::smem_addr(sm.kq), t0 = tc::smem_addr(sm.t), a0 = tc::smem_addr(sm.a);
-        float S[64];
+        float2 S[32];
+        T2 v[16];
+        float sS, smax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = fresh ? 0.0f : Sg[(size_t)(64 * hh + i) * D + j];
-        auto put_state = [&]() {
-            uint32_t hi[32], lo[32];
+        for (int i = 0; i < 32; ++i) {
+            S[i].x = fresh ? 0.0f : Sg[(size_t)(64 * hh + 2 * i) * D + j];
+            S[i].y = fresh ? 0.0f : Sg[(size_t)(64 * hh + 2 * i + 1) * D + j];
+            smax = fmaxf(smax, fmaxf(fabsf(S[i].x), fabsf(S[i].y)));
+        }
+        sm.smx[hh][j] = smax;
+        tc16::group_and(1, NS, true);
+        // S as operand of chunk c, and the chunk's V into registers
+        auto put = [&](int c, float bound) {
+            const int b = c & 1;
+            float inv;
+            scale_for(bound, kTopS, sS, inv);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) tc16::split2(S[2 * i], S[2 * i + 1], hi[i], lo[i]);
-            tc16::st32(quad + TSH + 32 * hh, hi);
-            tc16::st32(quad + TSL + 32 * hh, lo);
+            for (int p = 0; p < 2; ++p) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tc16::split2(mul2(S[16 * p + i], both(inv)), hi[i], lo[i]);
+                tc16::st16(quad + TSH + 32 * hh + 16 * p, hi);
+                tc16::st16(quad + TSL + 32 * hh + 16 * p, lo);
+            }
+            ok = warp_wait(&sm.full[b], (c >> 1) & 1) && ok;
+            const T *src = sm.v[b] + 32 * hh * D + j;
+            T2 m = __habs2(T2(src[0], src[D]));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[i] = T2(src[2 * i * D], src[(2 * i + 1) * D]);
+                m = __hmax2(m, __habs2(v[i]));
+            }
+            const float2 mf = to_f32x2(m);
+            sm.vmx[hh][j] = fmaxf(mf.x, mf.y);
             tc16::st_wait();
             tc::fence_before();
+            mbar_arrive(&sm.sput);
         };
-        // W^T = S^T K^T and Y^T = S^T Q^T: the rows of [K; Q] are the 128 columns
-        auto issue_wy = [&](int c) {
+        // The products, by thread 0 once every thread's operands are in place; what fails to be issued is missed by the
+        // waits for it.
+        const uint32_t kq0 = tc::smem_addr(sm.kq), x0 = tc::smem_addr(sm.x), a0 = tc::smem_addr(sm.a);
+        constexpr uint32_t id = tc16::idesc(128, C, false), id_mn = tc16::idesc(128, D, true);
+        auto issue_wy = [&](int c) {   // W^T = S^T K'^T, Y^T = S^T Q'^T
             const int b = c & 1;
-            if (!tc::mbar_wait(&sm.full[b], (c >> 1) & 1, kPolls)) return false;
+            const uint32_t kq = kq0 + b * 2 * kHalf;
+            if (!tc::mbar_wait(&sm.sput, c & 1, kPolls) || !tc::mbar_wait(&sm.full[b], (c >> 1) & 1, kPolls)) return;
             tc::fence_after();
-            const uint32_t kq = kq0 + b * KT * kTerm;
-            for (int p = 0; p < (KT == 1 ? 2 : 3); ++p) {
-                const uint32_t sa = tm + (p == 1 ? TSL : TSH), kb = kq + (p == 2 ? kTerm : 0u);
-                const uint32_t id = tc16::idesc(128, KT == 1 && p == 1 ? C : 2 * C, false);
-                for (int kk = 0; kk < 8; ++kk)
-                    tc16::mma_ts(tm + TWY, sa + 8 * kk, tc16::kmajor(kb + (kk >> 2) * kHalf + (kk & 3) * 32), id, p || kk);
-            }
+#pragma unroll
+            for (int m = 0; m < 16; ++m)
+                tc16::mma_ts(tm + TW, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7),
+                             tc16::kmajor(kq + ((m >> 2) & 1) * kHalf + (m & 3) * 32), id, m);
             tc::commit(&sm.wy);
-            return true;
+#pragma unroll
+            for (int m = 0; m < 8 * Sm::AT; ++m)
+                tc16::mma_ts(tm + TY + C * b, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7),
+                             tc16::kmajor(kq + C * 128 + ((m >> 2) & 1) * kHalf + (m & 3) * 32), id, m);
         };
-        put_state();
-        ok = tc16::group_and(1, NS, ok);
-        if (tid == 0) {
+        auto issue_u = [&](int c) {    // U'^T = R^T X^T, where the last chunk's A U' has been read
+            const int b = c & 1;
+            const uint32_t xb = x0 + b * 2 * C * 128;
+            if (!tc::mbar_wait(&sm.rput, c & 1, kPolls) || !tc::mbar_wait(&sm.ready[b], (c >> 1) & 1, kPolls) ||
+                !(c == 0 || tc::mbar_wait(&sm.out, (c & 1) ^ 1, kPolls)))
+                return;
             tc::fence_after();
-            ok = issue_wy(0);
-        }
+#pragma unroll
+            for (int m = 0; m < 12; ++m)
+                tc16::mma_ts(tm + TU, tm + (m < 8 ? TRH : TRL) + 8 * (m & 3),
+                             tc16::kmajor(xb + (m >= 4 && m < 8 ? C * 128 : 0) + (m & 3) * 32), id, m);
+            tc::commit(&sm.u);
+        };
+        auto issue_dz = [&](int c) {   // the increment of S^T (K's rows along the summed index), (A U')^T
+            const int b = c & 1;
+            const uint32_t kq = kq0 + b * 2 * kHalf, ab = a0 + b * Sm::AT * C * 128;
+            if (!tc::mbar_wait(&sm.uput, c & 1, kPolls)) return;
+            tc::fence_after();
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+                tc16::mma_ts(tm + TD, tm + (m < 4 ? TFH : TFL) + 8 * (m & 3), tc16::desc(kq + (m & 3) * 2048, kHalf, 1024), id_mn, m);
+            tc::commit(&sm.d);
+#pragma unroll
+            for (int m = 0; m < (TWO ? 12 : 4); ++m)
+                tc16::mma_ts(tm + TU, tm + (m >= 4 && m < 8 ? TUL : TUH) + 8 * (m & 3),
+                             tc16::kmajor(ab + (m >= 8 ? C * 128 : 0) + (m & 3) * 32), id, m);
+            tc::commit(&sm.z);
+        };
+        put(0, fmaxf(sm.smx[0][j], sm.smx[1][j]));
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const int b = c & 1, cc = min(C, count - c * C), vb = Sm::VB == 2 ? b : 0;
+        for (int c = 0; c < chunks && ok; ++c) {
+            const int b = c & 1;
             const uint32_t ph = c & 1;
-            // V and the gates are in place where the products are, but this thread has to see them itself
-            ok = tc::mbar_wait(&sm.full[b], (c >> 1) & 1, kPolls) && ok;
-            ok = tc::mbar_wait(&sm.wy, ph, kPolls) && ok;
+            if (tid == 0) issue_wy(c);
+            __syncwarp();
+            // R from W^T and V
+            ok = warp_wait(&sm.sput, ph) && warp_wait(&sm.wy, ph);
+            if (!ok) break;
             tc::fence_after();
-            uint32_t y[32];
+            float sR;
+            const float before = fmaxf(sm.smx[0][j], sm.smx[1][j]);
             {
                 uint32_t w[32], hi[16], lo[16];
-                tc::ld32(quad + TWY + 32 * hh, w);
-                tc::ld32(quad + TWY + C + 32 * hh, y);
-                const T *v = reinterpret_cast<const T *>(sm.v[vb]) + 32 * hh * D + j;
+                tc::ld32(quad + TW + 32 * hh, w);
+                float iR;
+                // |S^T k'| <= 128 * 2 * max |S|
+                scale_for(sm.mb[b] * fmaf(sm.mg[b] * 256.0f, before, fmaxf(sm.vmx[0][j], sm.vmx[1][j])), kTopR, sR, iR);
+                if (hh == 0) {
+                    sm.ss[b][j] = sS;
+                    sm.sr[b][j] = sR;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    float r[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = 2 * i + e;
-                        const float x = fmaf(-sm.gam[b][32 * hh + t], __uint_as_float(w[t]), to_f32(v[t * D]));
-                        r[e] = 32 * hh + t < cc ? x : 0.0f;
-                    }
-                    tc16::split2(r[0], r[1], hi[i], lo[i]);
+                    const float2 g = *reinterpret_cast<const float2 *>(&sm.gk[b][32 * hh + 2 * i]);
+                    const float2 bt = *reinterpret_cast<const float2 *>(&sm.bk[b][32 * hh + 2 * i]);
+                    const float2 y = fma2(g, mul2(pair_of(w, i), both(-sS)), to_f32x2(v[i]));
+                    tc16::split2(mul2(y, mul2(bt, both(iR))), hi[i], lo[i]);
                 }
-                tc16::st16(quad + TR + 16 * hh, hi);
-                tc16::st16(quad + TR + 32 + 16 * hh, lo);
+                tc16::st16(quad + TRH + 16 * hh, hi);
+                tc16::st16(quad + TRL + 16 * hh, lo);
                 tc16::st_wait();
             }
-            if constexpr (KT == 2) mbar_arrive(&sm.v_free);
             tc::fence_before();
-            ok = tc16::group_and(1, NS, ok);
+            mbar_arrive(&sm.rput);
+            if (tid == 0) issue_u(c);
+            __syncwarp();
+            // U' and diag(gamma_C / gamma) U'
+            ok = warp_wait(&sm.u, ph);
             if (!ok) break;
-            if (tid == 0) {   // U^T = R^T T^T
-                ok = tc::mbar_wait(&sm.ready[b], (c >> 1) & 1, kPolls);
-                tc::fence_after();
-                const uint32_t id = tc16::idesc(128, C, false);
-                if (ok) {
-                    for (int p = 0; p < 3; ++p)
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc16::mma_ts(tm + TU, tm + TR + (p == 2 ? 32 : 0) + 8 * kk,
-                                         tc16::kmajor(t0 + b * 2 * C * 128 + (p == 1 ? C * 128 : 0) + kk * 32), id, p || kk);
-                    tc::commit(&sm.u);
-                }
-            }
-            ok = tc::mbar_wait(&sm.u, ph, kPolls) && ok;
             tc::fence_after();
+            float um = 0.0f;
             {
                 uint32_t u[32], hi[16], lo[16];
                 tc::ld32(quad + TU + 32 * hh, u);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 f = *reinterpret_cast<const float2 *>(&sm.f[b][32 * hh + 2 * i]);
-                    tc16::split2(f.x * __uint_as_float(u[2 * i]), f.y * __uint_as_float(u[2 * i + 1]), hi[i], lo[i]);
+                    const float2 x = pair_of(u, i);
+                    um = fmaxf(um, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    tc16::split2(mul2(x, *reinterpret_cast<const float2 *>(&sm.f[b][32 * hh + 2 * i])), hi[i], lo[i]);
                 }
-                tc16::st16(quad + TF + 16 * hh, hi);
-                tc16::st16(quad + TF + 32 + 16 * hh, lo);
+                tc16::st16(quad + TFH + 16 * hh, hi);
+                tc16::st16(quad + TFL + 16 * hh, lo);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) tc16::split2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]), hi[i], lo[i]);
-                tc16::st16(quad + TR + 16 * hh, hi);
-                if constexpr (KT == 2) tc16::st16(quad + TR + 32 + 16 * hh, lo);
+                for (int i = 0; i < 16; ++i) {
+                    if constexpr (TWO) tc16::split2(pair_of(u, i), hi[i], lo[i]);
+                    else hi[i] = tc16::pack2(pair_of(u, i));
+                }
+                tc16::st16(quad + TUH + 16 * hh, hi);
+                if constexpr (TWO) tc16::st16(quad + TUL + 16 * hh, lo);
+                sm.umx[hh][j] = um;
+                if (um > kHalfMax && um <= kFloatMax) atomicOr(a.err, kErrRange);
                 tc16::st_wait();
             }
             tc::fence_before();
-            ok = tc16::group_and(1, NS, ok);
+            mbar_arrive(&sm.uput);
+            if (tid == 0) issue_dz(c);
+            __syncwarp();
+            // S
+            ok = warp_wait(&sm.uput, ph) && warp_wait(&sm.d, ph);
             if (!ok) break;
-            if (tid == 0) {
-                tc::fence_after();
-                // the increment of S^T: (U f)^T K, K's rows along the summed index
-                const uint32_t kq = kq0 + b * KT * kTerm;
-                uint32_t id = tc16::idesc(128, D, true);
-                for (int p = 0; p < KT + 1; ++p)
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc16::mma_ts(tm + TWY, tm + TF + (p == 1 ? 32 : 0) + 8 * kk,
-                                     tc16::desc(kq + (p == 2 ? kTerm : 0u) + kk * 2048, kHalf, 1024), id, p || kk);
-                tc::commit(&sm.d);
-                // (A U)^T
-                id = tc16::idesc(128, C, false);
-                for (int p = 0; p < (KT == 1 ? 1 : 3); ++p)
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc16::mma_ts(tm + TU, tm + TR + (p == 1 ? 32 : 0) + 8 * kk,
-                                     tc16::kmajor(a0 + b * KT * C * 128 + (p == 2 ? C * 128 : 0) + kk * 32), id, p || kk);
-                tc::commit(&sm.z);
-            }
-            ok = tc::mbar_wait(&sm.d, ph, kPolls) && ok;
             tc::fence_after();
-            const float last = sm.gam[b][C - 1];
+            const float last = sm.gl[b];
+            um = fmaxf(sm.umx[0][j], sm.umx[1][j]);
+            float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 uint32_t x[32];
-                tc::ld32(quad + TWY + 64 * hh + 32 * p, x);
+                tc::ld32(quad + TD + 64 * hh + 32 * p, x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) S[32 * p + i] = fmaf(last, S[32 * p + i], __uint_as_float(x[i]));
+                for (int i = 0; i < 16; ++i) {
+                    float2 &y = S[16 * p + i];
+                    y = fma2(pair_of(x, i), both(sR), mul2(y, both(last)));
+                    m0 = fmaxf(m0, fabsf(y.x));
+                    m1 = fmaxf(m1, fabsf(y.y));
+                }
             }
-            if (c + 1 < chunks) put_state();
-            else tc::fence_before();
-            ok = tc16::group_and(1, NS, ok);
-            if (!ok) break;
-            if (tid == 0 && c + 1 < chunks) {
-                tc::fence_after();
-                ok = issue_wy(c + 1);
-            }
-            ok = tc::mbar_wait(&sm.z, ph, kPolls) && ok;
-            tc::fence_after();
-            {
-                uint32_t z[32];
-                tc::ld32(quad + TU + 32 * hh, z);
-                T *o = static_cast<T *>(a.o) + (size_t)(first + c * C + 32 * hh) * a.os + h * D + j;
-#pragma unroll
-                for (int t = 0; t < 32; ++t)
-                    if (32 * hh + t < cc)
-                        o[(size_t)t * a.os] = from_f32<T>(fmaf(sm.gam[b][32 * hh + t], __uint_as_float(y[t]), __uint_as_float(z[t])));
-            }
-            tc::fence_before();
+            sm.smx[hh][j] = fmaxf(m0, m1);
             mbar_arrive(&sm.empty[b]);
+            // U' as an operand stands where S goes
+            ok = warp_wait(&sm.z, ph);
+            if (c + 1 < chunks) put(c + 1, fmaf(last, before, 128.0f * sR * um));   // |K'^T u'| <= 64 * 2 * max |u'|
         }
-        if (tc16::group_and(1, NS, ok)) {
+        if (ok) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) Sg[(size_t)(64 * hh + i) * D + j] = S[i];
-        } else if (tid == 0) {
-            atomicOr(a.err, kErrWait);
+            for (int i = 0; i < 32; ++i) {
+                Sg[(size_t)(64 * hh + 2 * i) * D + j] = S[i].x;
+                Sg[(size_t)(64 * hh + 2 * i + 1) * D + j] = S[i].y;
+            }
         }
     } else {
         // ---- prepare ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         const int p = tid - NS, pw = p >> 5;
-        const uint32_t quad = tm + ((uint32_t)(32 * pw) << 16);
+        const uint32_t quad = tm + ((uint32_t)(32 * (pw & 3)) << 16);
         const T *gq = static_cast<const T *>(a.q) + (size_t)hk * D, *gk = static_cast<const T *>(a.k) + (size_t)hk * D;
         const T *gv = static_cast<const T *>(a.v) + (size_t)h * D;
         bool gates_ok = true;
-        // the rows of a chunk into L2, ahead of their loads
+        float al[2] = {1.0f, 1.0f}, bt[2] = {0.0f, 0.0f};   // warp 7: a chunk's gates, two tokens a lane
+        // the rows of a chunk into L2 ahead of their loads, its gates into registers
         auto prefetch = [&](int c) {
             const int cc = min(C, count - c * C);
-            for (int e = p; e < 3 * cc; e += NP) {
-                const size_t tok = (size_t)(first + c * C + e / 3);
-                const T *src = e % 3 == 0 ? gk + tok * a.ks : e % 3 == 1 ? gq + tok * a.qs : gv + tok * a.vs;
+            const size_t tok0 = (size_t)(first + c * C);
+            if (p < 3 * cc) {
+                const size_t tok = tok0 + p / 3;
+                const T *src = p % 3 == 0 ? gk + tok * a.ks : p % 3 == 1 ? gq + tok * a.qs : gv + tok * a.vs;
                 asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(D * 2) : "memory");
+            }
+            if (pw == 7) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = 2 * lane + e;
+                    al[e] = t < cc ? __ldg(a.alpha + (tok0 + t) * a.H + h) : 1.0f;
+                    bt[e] = t < cc ? __ldg(a.beta + (tok0 + t) * a.H + h) : 0.0f;
+                }
+            }
+        };
+        // O of chunk c: Y^T and (A U')^T to rows of V's buffer, and from there to global memory
+        auto output = [&](int c) {
+            const int b = c & 1, cc = min(C, count - c * C), j = 32 * (pw & 3) + lane, t0 = 32 * (pw >> 2);
+            ok = warp_wait(&sm.uput, c & 1) && warp_wait(&sm.z, c & 1);
+            tc::fence_after();
+            {
+                uint32_t y[32], z[32];
+                tc::ld32(quad + TY + C * b + t0, y);
+                tc::ld32(quad + TU + t0, z);
+                tc::fence_before();
+                mbar_arrive(&sm.out);
+                const float sS = sm.ss[b][j], sR = sm.sr[b][j];
+                T *dst = sm.v[b] + t0 * D + j;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 g = *reinterpret_cast<const float2 *>(&sm.go[b][t0 + 2 * i]);
+                    const float2 q = *reinterpret_cast<const float2 *>(&sm.qs[b][t0 + 2 * i]);
+                    const float2 o = fma2(g, mul2(pair_of(y, i), both(sS)), mul2(q, mul2(pair_of(z, i), both(sR))));
+                    dst[2 * i * D] = from_f32<T>(o.x);
+                    dst[(2 * i + 1) * D] = from_f32<T>(o.y);
+                }
+            }
+            tc::fence_smem_to_async();
+            ok = tc16::group_and(2, NP, ok);
+            if (ok && p < cc) {
+                T *dst = static_cast<T *>(a.o) + (size_t)(first + c * C + p) * a.os + h * D;
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                             "r"(tc::smem_addr(sm.v[b] + p * D)), "r"(D * 2)
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
         };
         prefetch(0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int b = c & 1, cc = min(C, count - c * C), vb = Sm::VB == 2 ? b : 0;
-            ok = tc::mbar_wait(&sm.empty[b], ((c >> 1) & 1) ^ 1, kPolls) && ok;
-            if constexpr (KT == 2) ok = tc::mbar_wait(&sm.v_free, (c & 1) ^ 1, kPolls) && ok;
+            const int b = c & 1, cc = min(C, count - c * C);
+            const size_t tok0 = (size_t)(first + c * C);
+            ok = tc::mbar_wait(&sm.empty[b], ((c >> 1) & 1) ^ 1, kPolls);
+            if (p < C) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the output that stood in V's buffer
             ok = tc16::group_and(2, NP, ok);
             if (!ok) break;
-            if (c + 1 < chunks) prefetch(c + 1);
-            const size_t tok0 = (size_t)(first + c * C);
-            {   // 16 lanes a row of 128 values
-                const int i8 = p & 15;
-                const uint32_t kq = tc::smem_addr(sm.kq[b]) + (i8 >> 3) * kHalf, vs = tc::smem_addr(sm.v[vb]);
-#pragma unroll 4
-                for (int r = p >> 4; r < C; r += NP / 16) {
-                    const bool in = r < cc;
-                    const size_t tok = in ? tok0 + r : tok0;
-                    const T *k = gk + tok * a.ks + i8 * 8, *q = gq + tok * a.qs + i8 * 8, *v = gv + tok * a.vs + i8 * 8;
-                    const uint32_t off = tc16::sw_off(r, (i8 & 7) * 8);   // K and Q rows: 64 rows keep r % 8
-                    copy16(vs + (r * D + i8 * 8) * 2, v, in);
-                    if constexpr (KT == 1) {
-                        copy16(kq + off, k, in);
-                        copy16(kq + C * 128 + off, q, in);
-                    } else {
+            {   // 16 lanes a row of 128 values: rows p / 16 + 16 i
+                const int r0 = p >> 4, i8 = p & 15;
+                uint4 raw_k[4], raw_q[4];
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                            if (in) load_vec<8>(m ? q : k, x);
-                            uint4 hi, lo;
-                            tc16::split2(x[0], x[1], hi.x, lo.x);
-                            tc16::split2(x[2], x[3], hi.y, lo.y);
-                            tc16::split2(x[4], x[5], hi.z, lo.z);
-                            tc16::split2(x[6], x[7], hi.w, lo.w);
-                            uint8_t *dst = sm.kq[b] + (i8 >> 3) * kHalf + m * C * 128 + off;
-                            *reinterpret_cast<uint4 *>(dst) = hi;
-                            *reinterpret_cast<uint4 *>(dst + kTerm) = lo;
-                        }
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + 16 * i;
+                    const bool in = r < cc;
+                    const size_t tok = tok0 + (in ? r : 0);
+                    raw_k[i] = in ? __ldg(reinterpret_cast<const uint4 *>(gk + tok * a.ks) + i8) : make_uint4(0, 0, 0, 0);
+                    raw_q[i] = in ? __ldg(reinterpret_cast<const uint4 *>(gq + tok * a.qs) + i8) : make_uint4(0, 0, 0, 0);
+                    copy16(sm.v[b] + r * D + i8 * 8, gv + tok * a.vs + i8 * 8, in);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 rw = i < 4 ? raw_k[i & 3] : raw_q[i & 3];
+                    const T2 *pr = reinterpret_cast<const T2 *>(&rw);
+                    const int r = r0 + 16 * (i & 3);
+                    T2 m2 = __hmax2(__hmax2(__habs2(pr[0]), __habs2(pr[1])), __hmax2(__habs2(pr[2]), __habs2(pr[3])));
+                    const float2 mf = to_f32x2(m2);
+                    float m = fmaxf(mf.x, mf.y);
+#pragma unroll
+                    for (int w = 8; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+                    const int e = exponent_of(m);
+                    const float2 inv = both(__uint_as_float((uint32_t)(254 - e) << 23));
+                    uint4 out;
+                    out.x = tc16::pack2(mul2(to_f32x2(pr[0]), inv));
+                    out.y = tc16::pack2(mul2(to_f32x2(pr[1]), inv));
+                    out.z = tc16::pack2(mul2(to_f32x2(pr[2]), inv));
+                    out.w = tc16::pack2(mul2(to_f32x2(pr[3]), inv));
+                    // K rows, then Q rows: both start on a group of eight rows
+                    *reinterpret_cast<uint4 *>(sm.kq[b] + (i8 >> 3) * kHalf + (i < 4 ? 0 : C * 128) + tc16::sw_off(r, (i8 & 7) * 8)) = out;
+                    if (i8 == 0) (i < 4 ? sm.ks : sm.qs[b])[r] = __uint_as_float((uint32_t)e << 23);
                 }
             }
-            if (pw == 0) {   // gates: two tokens a lane; log2 of the running products
-                float l2[2], bt[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = 2 * lane + e;
-                    l2[e] = 0.0f;
-                    bt[e] = 0.0f;
-                    if (t < cc) {
-                        const float al = __ldg(a.alpha + (tok0 + t) * a.H + h);
-                        gates_ok = gates_ok && al > 0.0f && al <= 1.0f;
-                        l2[e] = log2f(al);
-                        bt[e] = __ldg(a.beta + (tok0 + t) * a.H + h);
-                    }
-                }
-                float sum = l2[0] + l2[1];
+            const float g0 = al[0], g1 = al[1], b0 = bt[0], b1 = bt[1];
+            if (c + 1 < chunks) prefetch(c + 1);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tc::fence_smem_to_async();
+            tc16::group_and(2, NP, true);
+            if (pw == 7) {   // running products in base 2, and what is formed from them
+                gates_ok = gates_ok && g0 > 0.0f && g0 <= 1.0f && g1 > 0.0f && g1 <= 1.0f;
+                const float l0 = log2f(g0), l1 = log2f(g1);
+                float sum = l0 + l1;
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) {
                     const float y = __shfl_up_sync(0xffffffffu, sum, m);
                     if (lane >= m) sum += y;
                 }
-                const float total = __shfl_sync(0xffffffffu, sum, 31), mid = sum - l2[1];
+                const float total = __shfl_sync(0xffffffffu, sum, 31), mid = sum - l1;
+                const float2 gam = make_float2(exp2f(mid), exp2f(sum)), bb = make_float2(b0, b1);
+                const float2 kk = *reinterpret_cast<const float2 *>(&sm.ks[2 * lane]);
+                const float2 qq = *reinterpret_cast<const float2 *>(&sm.qs[b][2 * lane]);
+                const float2 gkk = mul2(gam, kk), bkk = mul2(bb, kk);
                 *reinterpret_cast<float2 *>(&sm.lg[2 * lane]) = make_float2(mid, sum);
-                *reinterpret_cast<float2 *>(&sm.beta[2 * lane]) = make_float2(bt[0], bt[1]);
-                *reinterpret_cast<float2 *>(&sm.gam[b][2 * lane]) = make_float2(exp2f(mid), exp2f(sum));
+                *reinterpret_cast<float2 *>(&sm.be[2 * lane]) = mul2(bkk, kk);
+                *reinterpret_cast<float2 *>(&sm.gk[b][2 * lane]) = gkk;
+                *reinterpret_cast<float2 *>(&sm.bk[b][2 * lane]) = bkk;
                 *reinterpret_cast<float2 *>(&sm.f[b][2 * lane]) = make_float2(exp2f(total - mid), exp2f(total - sum));
+                *reinterpret_cast<float2 *>(&sm.go[b][2 * lane]) = mul2(gam, qq);
+                float mb = fmaxf(fabsf(bkk.x), fabsf(bkk.y)), mg = fmaxf(fabsf(gkk.x), fabsf(gkk.y));
+#pragma unroll
+                for (int w = 16; w > 0; w >>= 1) {
+                    mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
+                    mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, w));
+                }
+                if (lane == 0) {
+                    sm.gl[b] = exp2f(total);
+                    sm.mb[b] = mb;
+                    sm.mg[b] = mg;
+                }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            tc::fence_smem_to_async();
             mbar_arrive(&sm.full[b]);
-            ok = tc::mbar_wait(&sm.full[b], (c >> 1) & 1, kPolls);
-            if (p == 0 && ok) {   // [K; Q] K^T
+            if (p == 0) {   // [K; Q] K^T
                 tc::fence_after();
                 const uint32_t kq = tc::smem_addr(sm.kq[b]), id = tc16::idesc(128, C, false);
-                for (int m = 0; m < KT * KT; ++m)
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t at = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc16::mma_ss(tm + TG, tc16::kmajor(kq + (m >> 1) * kTerm + at), tc16::kmajor(kq + (m & 1) * kTerm + at), id, m || kk);
-                    }
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t at = tc16::kmajor(kq + (kk >> 2) * kHalf + (kk & 3) * 32);
+                    tc16::mma_ss(tm + TG, at, at, id, kk);
+                }
                 tc::commit(&sm.g);
             }
-            ok = tc::mbar_wait(&sm.g, c & 1, kPolls) && ok;
+            ok = warp_wait(&sm.full[b], (c >> 1) & 1) && warp_wait(&sm.g, c & 1);
             tc::fence_after();
             {
-                const int t = p & 63;
-                const float lt = sm.lg[t], bt = sm.beta[t];
-#pragma unroll 1
-                for (int s0 = 0; s0 < C; s0 += 32) {
-                    uint32_t g[32];
-                    tc::ld32(quad + TG + s0, g);
-                    const bool none = s0 > (t | 31);   // right of the diagonal for the whole warp
-                    if (p < C) {
+                const int t = (32 * pw + lane) & 63, s0 = 32 * (pw >> 2);
+                const float lt = sm.lg[t], bt2 = sm.be[t];
+                uint32_t g[32];
+                tc::ld32(quad + TG + s0, g);
+                float x[32];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float x[4];
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 ls = *reinterpret_cast<const float4 *>(&sm.lg[s0 + e]);
+                    x[e] = ex2(fminf(lt - ls.x, 0.0f)) * __uint_as_float(g[e]);
+                    x[e + 1] = ex2(fminf(lt - ls.y, 0.0f)) * __uint_as_float(g[e + 1]);
+                    x[e + 2] = ex2(fminf(lt - ls.z, 0.0f)) * __uint_as_float(g[e + 2]);
+                    x[e + 3] = ex2(fminf(lt - ls.w, 0.0f)) * __uint_as_float(g[e + 3]);
+                }
+                if ((pw & 3) < 2) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int ss = s0 + e + i;
-                                x[i] = !none && ss < t ? bt * exp2f(lt - sm.lg[ss]) * __uint_as_float(g[e + i]) : 0.0f;
-                            }
-                            *reinterpret_cast<float4 *>(&sm.n[t * SN + s0 + e]) = make_float4(x[0], x[1], x[2], x[3]);
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(&sm.n[t * SN + s0 + e]) =
+                            make_float4(s0 + e < t ? bt2 * x[e] : 0.0f, s0 + e + 1 < t ? bt2 * x[e + 1] : 0.0f,
+                                        s0 + e + 2 < t ? bt2 * x[e + 2] : 0.0f, s0 + e + 3 < t ? bt2 * x[e + 3] : 0.0f);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int ss = s0 + e + 2 * i;
+                            const float2 y = make_float2(ss <= t ? x[e + 2 * i] : 0.0f, ss + 1 <= t ? x[e + 2 * i + 1] : 0.0f);
+                            if constexpr (TWO) tc16::split2(y, hi[i], lo[i]);
+                            else hi[i] = tc16::pack2(y);
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float x[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int ss = s0 + e + i;
-                                x[i] = !none && ss <= t ? exp2f(lt - sm.lg[ss]) * __uint_as_float(g[e + i]) : 0.0f;
-                            }
-                            uint4 hi, lo;
-                            tc16::split2(x[0], x[1], hi.x, lo.x);
-                            tc16::split2(x[2], x[3], hi.y, lo.y);
-                            tc16::split2(x[4], x[5], hi.z, lo.z);
-                            tc16::split2(x[6], x[7], hi.w, lo.w);
-                            uint8_t *dst = sm.a[b] + tc16::sw_off(t, s0 + e);
-                            *reinterpret_cast<uint4 *>(dst) = hi;
-                            if constexpr (KT == 2) *reinterpret_cast<uint4 *>(dst + C * 128) = lo;
-                        }
+                        uint8_t *dst = sm.a[b] + tc16::sw_off(t, s0 + e);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if constexpr (TWO) *reinterpret_cast<uint4 *>(dst + C * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
             }
             tc::fence_before();
             ok = tc16::group_and(2, NP, ok);
             if (!ok) break;
-            // (I + N)^-1: the diagonal blocks of 16 by substitution, a column a lane
-            {
+            // (I + N)^-1 in place: the diagonal blocks of 16 by substitution, a column a lane
+            if (pw < 4) {
                 const int r0 = 16 * pw, col = lane & 15;
                 float x[16];
 #pragma unroll
@@ -429,89 +560,78 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 }
             }
             tc16::group_and(2, NP, true);
-            // pairs of blocks of M rows at r0 (upper) and r0 + M (lower): the block below the diagonal is
-            // -X_lower N X_upper, in N's place; thread: R rows x 4 columns of it.
-            auto join = [&](auto m_, auto r_, int r0, int at) {
-                constexpr int M = decltype(m_)::value, R = decltype(r_)::value;
-                const int row = at / (M / 4) * R, col = at % (M / 4) * 4;
-                float acc[R][4];
+            // pairs of blocks of M rows at r0 (upper) and r0 + M (lower): the block below the diagonal becomes
+            // -X_lower N X_upper; thread: four columns of a row
+            auto join = [&](auto m_, bool mine, int r0, int at) {
+                constexpr int M = decltype(m_)::value;
+                const int row = at / (M / 4), col = at % (M / 4) * 4;
+                float2 acc[2];
                 auto product = [&](const float *l, const float *r) {
+                    acc[0] = acc[1] = make_float2(0.0f, 0.0f);
+                    if (!mine) return;
 #pragma unroll
-                    for (int i = 0; i < R; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-#pragma unroll 4
                     for (int k = 0; k < M; k += 4) {
-                        float4 lv[R];
-#pragma unroll
-                        for (int i = 0; i < R; ++i) lv[i] = *reinterpret_cast<const float4 *>(l + (row + i) * SN + k);
+                        const float4 lv = *reinterpret_cast<const float4 *>(l + row * SN + k);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float4 rv = *reinterpret_cast<const float4 *>(r + (k + e) * SN + col);
-#pragma unroll
-                            for (int i = 0; i < R; ++i) {
-                                const float w = e == 0 ? lv[i].x : e == 1 ? lv[i].y : e == 2 ? lv[i].z : lv[i].w;
-                                acc[i][0] = fmaf(w, rv.x, acc[i][0]);
-                                acc[i][1] = fmaf(w, rv.y, acc[i][1]);
-                                acc[i][2] = fmaf(w, rv.z, acc[i][2]);
-                                acc[i][3] = fmaf(w, rv.w, acc[i][3]);
-                            }
+                            const float2 w = both(e == 0 ? lv.x : e == 1 ? lv.y : e == 2 ? lv.z : lv.w);
+                            acc[0] = fma2(w, make_float2(rv.x, rv.y), acc[0]);
+                            acc[1] = fma2(w, make_float2(rv.z, rv.w), acc[1]);
                         }
                     }
                 };
-                auto put = [&](float sign) {
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-                        *reinterpret_cast<float4 *>(&sm.n[(r0 + M + row + i) * SN + r0 + col]) =
-                            make_float4(sign * acc[i][0], sign * acc[i][1], sign * acc[i][2], sign * acc[i][3]);
+                float *nb = &sm.n[(r0 + M) * SN + r0];
+                auto store = [&](float sign) {
+                    tc16::group_and(2, NP, true);   // every read of the block is done
+                    if (mine)
+                        *reinterpret_cast<float4 *>(nb + row * SN + col) =
+                            make_float4(sign * acc[0].x, sign * acc[0].y, sign * acc[1].x, sign * acc[1].y);
+                    tc16::group_and(2, NP, true);
                 };
-                const float *nb = &sm.n[(r0 + M) * SN + r0];
                 product(nb, &sm.n[r0 * SN + r0]);
-                tc16::group_and(2, NP, true);   // every read of the block is done
-                put(1.0f);
-                tc16::group_and(2, NP, true);
+                store(1.0f);
                 product(&sm.n[(r0 + M) * SN + r0 + M], nb);
-                tc16::group_and(2, NP, true);
-                put(-1.0f);
-                tc16::group_and(2, NP, true);
+                store(-1.0f);
             };
-            join(std::integral_constant<int, 16>(), std::integral_constant<int, 1>(), p < 64 ? 0 : 32, p & 63);
-            join(std::integral_constant<int, 32>(), std::integral_constant<int, 2>(), 0, p);
-            // T = X diag(beta), two terms, zeros right of the diagonal
-            {
+            join(std::integral_constant<int, 16>(), p < 128, p & 64 ? 32 : 0, p & 63);
+            join(std::integral_constant<int, 32>(), true, 0, p);
+            {   // X as operand, zeros right of the diagonal
                 const int t = p & 63;
+                float m = 0.0f;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int s0 = 32 * (p >> 6) + 8 * m;
-                    float x[8];
+                for (int e = 0; e < 2; ++e) {
+                    const int s0 = 16 * (p >> 6) + 8 * e;
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(&sm.n[t * SN + s0 + i]);
-                        const float4 bt = *reinterpret_cast<const float4 *>(&sm.beta[s0 + i]);
-                        x[i] = s0 + i <= t ? y.x * bt.x : 0.0f;
-                        x[i + 1] = s0 + i + 1 <= t ? y.y * bt.y : 0.0f;
-                        x[i + 2] = s0 + i + 2 <= t ? y.z * bt.z : 0.0f;
-                        x[i + 3] = s0 + i + 3 <= t ? y.w * bt.w : 0.0f;
+                    for (int i = 0; i < 4; ++i) {
+                        float2 y = *reinterpret_cast<const float2 *>(&sm.n[t * SN + s0 + 2 * i]);
+                        if (s0 + 2 * i > t) y.x = 0.0f;
+                        if (s0 + 2 * i + 1 > t) y.y = 0.0f;
+                        m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
+                        tc16::split2(y, hi[i], lo[i]);
                     }
-                    uint4 hi, lo;
-                    tc16::split2(x[0], x[1], hi.x, lo.x);
-                    tc16::split2(x[2], x[3], hi.y, lo.y);
-                    tc16::split2(x[4], x[5], hi.z, lo.z);
-                    tc16::split2(x[6], x[7], hi.w, lo.w);
-                    uint8_t *dst = sm.t[b] + tc16::sw_off(t, s0);
-                    *reinterpret_cast<uint4 *>(dst) = hi;
-                    *reinterpret_cast<uint4 *>(dst + C * 128) = lo;
+                    uint8_t *dst = sm.x[b] + tc16::sw_off(t, s0);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(dst + C * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
+                if (m > kHalfMax && m <= kFloatMax) atomicOr(a.err, kErrRange);
             }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.ready[b]);
-            // beta and the gates' logarithms are rewritten by the next chunk: after every thread's reads
-            tc16::group_and(2, NP, true);
+            if (c > 0) {
+                output(c - 1);
+                if (!ok) break;
+            }
         }
+        if (ok) output(chunks - 1);
+        if (p < C) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!gates_ok) atomicOr(a.err, kErrGateRange);
-        if (!ok && p == 0) atomicOr(a.err, kErrWait);
     }
     // A product may still be in flight only after a wait gave up: let it end (bounded) before its memory is given
     // back.  A commit covers what its own thread has issued.
     if (!__syncthreads_and(ok) && (tid == 0 || tid == NS)) {
+        if (tid == 0) atomicOr(a.err, kErrWait);
         uint64_t *bar = &sm.drain[tid == 0 ? 0 : 1];
         tc::commit(bar);
         if (!tc::mbar_wait(bar, 0, kPolls)) atomicOr(a.err, kErrTmemDrain);
@@ -522,22 +642,22 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
     if (warp == 0) tc::dealloc(tm, 512);
 }
 
-template <int KT, class T>
+template <class T>
 cudaError_t launch(const DeltaArgs &a, cudaStream_t st) {
+    static_assert(sizeof(Smem<T>) <= 227 * 1024, "shared memory of a block");
     const long long blocks = (long long)a.n_seq * a.H;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    auto *kern = k_delta_chunk<KT, T>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<KT>));
+    auto *kern = k_delta_chunk<T>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<T>));
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)blocks, NT, sizeof(Smem<KT>), st>>>(a);
+    kern<<<(unsigned)blocks, NT, sizeof(Smem<T>), st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_delta_chunk(int dtype, const DeltaArgs &a, cudaStream_t st) {
-    static_assert(sizeof(Smem<1>) <= 227 * 1024 && sizeof(Smem<2>) <= 227 * 1024, "shared memory of a block");
-    return dtype == 2 ? launch<1, __nv_bfloat16>(a, st) : launch<2, __half>(a, st);
+    return dtype == 2 ? launch<__nv_bfloat16>(a, st) : launch<__half>(a, st);
 }
 
 }  // namespace stepq

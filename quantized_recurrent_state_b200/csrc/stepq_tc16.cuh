@@ -1,5 +1,5 @@
 // Fifth-generation tensor core (tcgen05) building blocks for sm_100a, kind::f16 with
-// bfloat16 operands and fp32 accumulators (tensor memory and barriers: stepq_tc.cuh).
+// fp16 operands and fp32 accumulators (tensor memory and barriers: stepq_tc.cuh).
 //
 // Shared-memory operands use the 128-byte swizzle: rows of 128 bytes (64
 // values), 8-row groups of 1,024 bytes, the 16-byte chunk c of row r at chunk
@@ -9,7 +9,7 @@
 // two consecutive K values in a 32-bit column, row m in lane m.
 #pragma once
 
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "stepq_tc.cuh"
 
@@ -29,9 +29,9 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo, uint32_t 
 }
 __device__ __forceinline__ uint64_t kmajor(uint32_t saddr) { return desc(saddr, 16, 1024); }
 
-// Instruction descriptor: D f32, A and B bf16, A K-major, B K-major or MN-major, M x N.
+// Instruction descriptor: D f32, A and B f16, A K-major, B K-major or MN-major, M x N.
 __host__ __device__ constexpr uint32_t idesc(int m, int n, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
 
@@ -68,15 +68,16 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&v)[32]) {
 #undef STEPQ_W8
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// (x0, x1) as the sum of two bfloat16 pairs: hi the nearest, lo the nearest to the rest (2^-18 of x is left).
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+// (x0, x1) as the sum of two fp16 pairs: hi the nearest, lo the nearest to the rest.
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __float22half2_rn(x);
+    const float2 back = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x.x - back.x, x.y - back.y);
     hi = *reinterpret_cast<const uint32_t *>(&h);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
-__device__ __forceinline__ uint32_t pack2(float x0, float x1) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+__device__ __forceinline__ uint32_t pack2(float2 x) {
+    const __half2 h = __float22half2_rn(x);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
