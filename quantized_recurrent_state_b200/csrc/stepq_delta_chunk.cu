@@ -67,7 +67,7 @@ struct Smem {
     float gl[2], mb[2], mg[2];                 // gamma_C, the largest beta ks, the largest gamma ks
     float smx[2][D], vmx[2][D], umx[2][D];     // largest |S|, |v|, |u'| of a lane, by half
     float ss[2][D], sr[2][D];                  // a lane's scales of the S and R terms
-    alignas(8) uint64_t full[2], ready[2], empty[2], sput, rput, uput, wy, u, d, z, g, out, drain[2];
+    alignas(8) uint64_t full[2], vfull[2], ready[2], empty[2], sput, rput, uput, wy, u, d, z, g, out, drain[2];
     uint32_t taddr;
 };
 
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init_n(&sm.full[b], NP);
+            mbar_init_n(&sm.vfull[b], NP);
             mbar_init_n(&sm.ready[b], NP);
             mbar_init_n(&sm.empty[b], NS);
         }
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 tc16::st16(quad + TSH + 32 * hh + 16 * p, hi);
                 tc16::st16(quad + TSL + 32 * hh + 16 * p, lo);
             }
-            ok = warp_wait(&sm.full[b], (c >> 1) & 1) && ok;
+            ok = warp_wait(&sm.full[b], (c >> 1) & 1) && warp_wait(&sm.vfull[b], (c >> 1) & 1) && ok;
             const T *src = sm.v[b] + 32 * hh * D + j;
             T2 m = __habs2(T2(src[0], src[D]));
 #pragma unroll
@@ -358,10 +359,10 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
         auto prefetch = [&](int c) {
             const int cc = min(C, count - c * C);
             const size_t tok0 = (size_t)(first + c * C);
-            if (p < 3 * cc) {
-                const size_t tok = tok0 + p / 3;
-                const T *src = p % 3 == 0 ? gk + tok * a.ks : p % 3 == 1 ? gq + tok * a.qs : gv + tok * a.vs;
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(D * 2) : "memory");
+            for (int e = p; e < 6 * cc; e += NP) {   // two lines of 128 bytes a row
+                const size_t tok = tok0 + e / 6;
+                const T *src = e % 3 == 0 ? gk + tok * a.ks : e % 3 == 1 ? gq + tok * a.qs : gv + tok * a.vs;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (e % 6 >= 3 ? D / 2 : 0)) : "memory");
             }
             if (pw == 7) {
 #pragma unroll
@@ -394,14 +395,13 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                     dst[(2 * i + 1) * D] = from_f32<T>(o.y);
                 }
             }
-            tc::fence_smem_to_async();
             ok = tc16::group_and(2, NP, ok);
-            if (ok && p < cc) {
-                T *dst = static_cast<T *>(a.o) + (size_t)(first + c * C + p) * a.os + h * D;
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                             "r"(tc::smem_addr(sm.v[b] + p * D)), "r"(D * 2)
-                             : "memory");
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            if (!ok) return;
+            T *dst = static_cast<T *>(a.o) + (size_t)(first + c * C) * a.os + h * D + (p & 15) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (p >> 4) + 16 * i;
+                if (r < cc) *reinterpret_cast<uint4 *>(dst + r * a.os) = *reinterpret_cast<const uint4 *>(sm.v[b] + r * D + (p & 15) * 8);
             }
         };
         prefetch(0);
@@ -410,7 +410,6 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             const int b = c & 1, cc = min(C, count - c * C);
             const size_t tok0 = (size_t)(first + c * C);
             ok = tc::mbar_wait(&sm.empty[b], ((c >> 1) & 1) ^ 1, kPolls);
-            if (p < C) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the output that stood in V's buffer
             ok = tc16::group_and(2, NP, ok);
             if (!ok) break;
             {   // 16 lanes a row of 128 values: rows p / 16 + 16 i
@@ -425,6 +424,8 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                     raw_q[i] = in ? __ldg(reinterpret_cast<const uint4 *>(gq + tok * a.qs) + i8) : make_uint4(0, 0, 0, 0);
                     copy16(sm.v[b] + r * D + i8 * 8, gv + tok * a.vs + i8 * 8, in);
                 }
+                // arrives when this thread's copies have landed
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_addr(&sm.vfull[b])) : "memory");
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint4 rw = i < 4 ? raw_k[i & 3] : raw_q[i & 3];
@@ -449,7 +450,6 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             const float g0 = al[0], g1 = al[1], b0 = bt[0], b1 = bt[1];
             if (c + 1 < chunks) prefetch(c + 1);
-            asm volatile("cp.async.wait_all;" ::: "memory");
             tc::fence_smem_to_async();
             tc16::group_and(2, NP, true);
             if (pw == 7) {   // running products in base 2, and what is formed from them
@@ -561,32 +561,37 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             tc16::group_and(2, NP, true);
             // pairs of blocks of M rows at r0 (upper) and r0 + M (lower): the block below the diagonal becomes
-            // -X_lower N X_upper; thread: four columns of a row
-            auto join = [&](auto m_, bool mine, int r0, int at) {
+            // -X_lower N X_upper; a warp does 16 x 8 of it, operands as two fp16 terms, three products
+            auto join = [&](auto m_, bool mine, int r0, int row, int col) {
                 constexpr int M = decltype(m_)::value;
-                const int row = at / (M / 4), col = at % (M / 4) * 4;
-                float2 acc[2];
+                const int g = lane >> 2, q = 2 * (lane & 3);
+                float acc[4];
                 auto product = [&](const float *l, const float *r) {
-                    acc[0] = acc[1] = make_float2(0.0f, 0.0f);
+                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
                     if (!mine) return;
 #pragma unroll
-                    for (int k = 0; k < M; k += 4) {
-                        const float4 lv = *reinterpret_cast<const float4 *>(l + row * SN + k);
+                    for (int k = 0; k < M; k += 16) {
+                        uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 rv = *reinterpret_cast<const float4 *>(r + (k + e) * SN + col);
-                            const float2 w = both(e == 0 ? lv.x : e == 1 ? lv.y : e == 2 ? lv.z : lv.w);
-                            acc[0] = fma2(w, make_float2(rv.x, rv.y), acc[0]);
-                            acc[1] = fma2(w, make_float2(rv.z, rv.w), acc[1]);
+                        for (int i = 0; i < 4; ++i)
+                            tc16::split2(*reinterpret_cast<const float2 *>(l + (row + g + 8 * (i & 1)) * SN + k + q + 8 * (i >> 1)), ah[i], al[i]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float *y = r + (k + q + 8 * i) * SN + col + g;
+                            tc16::split2(make_float2(y[0], y[SN]), bh[i], bl[i]);
                         }
+                        tc16::mma_sync(acc, ah, bh);
+                        tc16::mma_sync(acc, ah, bl);
+                        tc16::mma_sync(acc, al, bh);
                     }
                 };
                 float *nb = &sm.n[(r0 + M) * SN + r0];
                 auto store = [&](float sign) {
                     tc16::group_and(2, NP, true);   // every read of the block is done
-                    if (mine)
-                        *reinterpret_cast<float4 *>(nb + row * SN + col) =
-                            make_float4(sign * acc[0].x, sign * acc[0].y, sign * acc[1].x, sign * acc[1].y);
+                    if (mine) {
+                        *reinterpret_cast<float2 *>(nb + (row + g) * SN + col + q) = make_float2(sign * acc[0], sign * acc[1]);
+                        *reinterpret_cast<float2 *>(nb + (row + g + 8) * SN + col + q) = make_float2(sign * acc[2], sign * acc[3]);
+                    }
                     tc16::group_and(2, NP, true);
                 };
                 product(nb, &sm.n[r0 * SN + r0]);
@@ -594,8 +599,8 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 product(&sm.n[(r0 + M) * SN + r0 + M], nb);
                 store(-1.0f);
             };
-            join(std::integral_constant<int, 16>(), p < 128, p & 64 ? 32 : 0, p & 63);
-            join(std::integral_constant<int, 32>(), true, 0, p);
+            join(std::integral_constant<int, 16>(), pw < 4, pw & 2 ? 32 : 0, 0, 8 * (pw & 1));
+            join(std::integral_constant<int, 32>(), true, 0, 16 * (pw >> 2), 8 * (pw & 3));
             {   // X as operand, zeros right of the diagonal
                 const int t = p & 63;
                 float m = 0.0f;
@@ -625,7 +630,6 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
         }
         if (ok) output(chunks - 1);
-        if (p < C) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!gates_ok) atomicOr(a.err, kErrGateRange);
     }
     // A product may still be in flight only after a wait gave up: let it end (bounded) before its memory is given

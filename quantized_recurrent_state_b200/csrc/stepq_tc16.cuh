@@ -81,6 +81,13 @@ __device__ __forceinline__ uint32_t pack2(float2 x) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// One warp's 16 x 8 += 16 x 16 times 16 x 8 (the warp-level instruction, for products too small for the others).
+__device__ __forceinline__ void mma_sync(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
 // Barrier `id` of n threads; true where every thread's ok was.
 __device__ __forceinline__ bool group_and(int id, int n, bool ok) {
     uint32_t r;
