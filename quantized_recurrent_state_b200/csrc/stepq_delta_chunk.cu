@@ -21,14 +21,16 @@
 // chain S -> R -> U' -> S is serial, so the block is split by what it waits for:
 //   warps 0-7  (state)   thread = value column j and half of the key rows: S in registers; R, U', S as operands;
 //                        thread 0 issues the products that need them
-//   warps 8-15 (prepare) the next chunk's loads, scales, gates, [K; Q] K^T, X, A; the last chunk's output
+//   warps 8-15 (prepare) two groups of four warps, a group to every other chunk: loads, scales, gates, [K; Q] K^T, X, A,
+//                        and the chunk's output.  What a group prepares is mostly latency (loads, barriers, the
+//                        substitution), so two chunks at a time.
 // The register file is split 168 : 88 between them (2 x 168 + 2 x 88 = 4 x 128 in each quarter of the SM).
 // The value columns j are the lanes of every product (W^T = S^T K'^T and so on), so what a
 // product leaves in a thread's lane is what the thread feeds to the next one.
 //
 // Tensor memory columns: S^T terms 0-127 (hi, lo, two values a column), later diag(gamma_C / gamma) U' (0-63) and U'
-// (64-127); W^T 128-191 and R terms 192-255, later the state's increment; Y^T = S^T Q'^T 256-383, two chunks;
-// U'^T 384-447, later A U'; [K; Q] K^T 448-511.
+// (64-127); W^T 128-191 and R terms 192-255, later the state's increment; Y^T = S^T Q'^T 256-319; U'^T 320-383, later
+// A U'; [K; Q] K^T 384-511, one for each group.
 //
 // Every wait is bounded: a wait that gives up ends its warp's or group's part and sets kErrWait; what waits for that
 // part gives up in turn.
@@ -43,10 +45,10 @@ namespace stepq {
 
 namespace {
 
-constexpr int D = 128, C = 64, NS = 256, NP = 256, NT = NS + NP;
-constexpr uint32_t kPolls = 1u << 22;
+constexpr int D = 128, C = 64, NS = 256, NP = 128, NT = NS + 2 * NP;
+constexpr uint32_t kPolls = 1u << 20;
 constexpr uint32_t TSH = 0, TSL = 64, TFH = 0, TFL = 32, TUH = 64, TUL = 96, TW = 128, TRH = 192, TRL = 224, TD = 128, TY = 256,
-                   TU = 384, TG = 448;
+                   TU = 320, TG = 384;
 constexpr uint32_t kHalf = 128 * 128;   // bytes of 64 columns of [K; Q]
 constexpr int SN = C + 4;               // row stride of the fp32 scratch matrix
 constexpr int kTopS = 13, kTopR = 6;    // the scaled bounds of S and R are 2^kTop
@@ -59,15 +61,16 @@ struct Smem {
     alignas(1024) uint8_t x[2][2 * C * 128];   // X, two terms
     alignas(1024) uint8_t a[2][AT * C * 128];  // A
     alignas(16) T v[2][C * D];                 // V, later the chunk's output
-    alignas(16) float n[C * SN];               // N, its inverse in place
+    alignas(16) float n[2][C * SN];            // by group: N below the diagonal, its inverse in place
     alignas(16) float gk[2][C], bk[2][C];      // gamma ks, beta ks
     alignas(16) float f[2][C];                 // gamma_C / gamma
     alignas(16) float go[2][C], qs[2][C];      // gamma qs, qs
-    alignas(16) float ks[C], lg[C], be[C];     // prepare's own: ks, log2 gamma, beta ks^2
+    alignas(16) float ks[2][C], lg[2][C];      // by group: ks, log2 gamma
+    alignas(16) float be[2][C], e2[2][C];      // beta ks^2; gamma at the end of the block of 16 over gamma
     float gl[2], mb[2], mg[2];                 // gamma_C, the largest beta ks, the largest gamma ks
     float smx[2][D], vmx[2][D], umx[2][D];     // largest |S|, |v|, |u'| of a lane, by half
     float ss[2][D], sr[2][D];                  // a lane's scales of the S and R terms
-    alignas(8) uint64_t full[2], vfull[2], ready[2], empty[2], sput, rput, uput, wy, u, d, z, g, out, drain[2];
+    alignas(8) uint64_t full[2], vfull[2], ready[2], empty[2], sput, rput, uput[2], wy, u, d, z[2], out, g[2], drain[3];
     uint32_t taddr;
 };
 
@@ -142,10 +145,13 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             mbar_init_n(&sm.vfull[b], NP);
             mbar_init_n(&sm.ready[b], NP);
             mbar_init_n(&sm.empty[b], NS);
+            mbar_init_n(&sm.uput[b], NS);
+            mbar_init_n(&sm.z[b], 1);
+            mbar_init_n(&sm.g[b], 1);
         }
-        for (uint64_t *b : {&sm.sput, &sm.rput, &sm.uput}) mbar_init_n(b, NS);
+        for (uint64_t *b : {&sm.sput, &sm.rput}) mbar_init_n(b, NS);
         mbar_init_n(&sm.out, NP);
-        for (uint64_t *b : {&sm.wy, &sm.u, &sm.d, &sm.z, &sm.g, &sm.drain[0], &sm.drain[1]}) mbar_init_n(b, 1);
+        for (uint64_t *b : {&sm.wy, &sm.u, &sm.d, &sm.drain[0], &sm.drain[1], &sm.drain[2]}) mbar_init_n(b, 1);
         fence_mbar_init();
     }
     if (warp == 0) tc::alloc(&sm.taddr, 512);
@@ -198,62 +204,64 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             tc::fence_before();
             mbar_arrive(&sm.sput);
         };
-        // The products, by thread 0 once every thread's operands are in place; what fails to be issued is missed by the
-        // waits for it.
-        const uint32_t kq0 = tc::smem_addr(sm.kq), x0 = tc::smem_addr(sm.x), a0 = tc::smem_addr(sm.a);
+        // The products, by thread 0 once every thread's operands are in place.  A descriptor's address field counts 16 bytes.
+        const uint64_t dk = tc16::kmajor(tc::smem_addr(sm.kq)), dx = tc16::kmajor(tc::smem_addr(sm.x)),
+                       da = tc16::kmajor(tc::smem_addr(sm.a)), dn = tc16::desc(tc::smem_addr(sm.kq), kHalf, 1024);
         constexpr uint32_t id = tc16::idesc(128, C, false), id_mn = tc16::idesc(128, D, true);
-        auto issue_wy = [&](int c) {   // W^T = S^T K'^T, Y^T = S^T Q'^T
+        auto issue_wy = [&](int c) {   // W^T = S^T K'^T; Y^T = S^T Q'^T, where the last chunk's output has been read
             const int b = c & 1;
-            const uint32_t kq = kq0 + b * 2 * kHalf;
-            if (!tc::mbar_wait(&sm.sput, c & 1, kPolls) || !tc::mbar_wait(&sm.full[b], (c >> 1) & 1, kPolls)) return;
+            const uint64_t kq = dk + b * (2 * kHalf >> 4);
+            if (!tc::mbar_wait(&sm.sput, c & 1, kPolls) || !tc::mbar_wait(&sm.full[b], (c >> 1) & 1, kPolls)) return false;
             tc::fence_after();
 #pragma unroll
             for (int m = 0; m < 16; ++m)
-                tc16::mma_ts(tm + TW, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7),
-                             tc16::kmajor(kq + ((m >> 2) & 1) * kHalf + (m & 3) * 32), id, m);
+                tc16::mma_ts(tm + TW, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7), kq + ((((m >> 2) & 1) * kHalf + (m & 3) * 32) >> 4), id, m);
             tc::commit(&sm.wy);
+            if (c > 0 && !tc::mbar_wait(&sm.out, (c & 1) ^ 1, kPolls)) return false;
+            tc::fence_after();
 #pragma unroll
             for (int m = 0; m < 8 * Sm::AT; ++m)
-                tc16::mma_ts(tm + TY + C * b, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7),
-                             tc16::kmajor(kq + C * 128 + ((m >> 2) & 1) * kHalf + (m & 3) * 32), id, m);
+                tc16::mma_ts(tm + TY, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7),
+                             kq + ((C * 128 + ((m >> 2) & 1) * kHalf + (m & 3) * 32) >> 4), id, m);
+            return true;
         };
-        auto issue_u = [&](int c) {    // U'^T = R^T X^T, where the last chunk's A U' has been read
+        auto issue_u = [&](int c) {    // U'^T = R^T X^T
             const int b = c & 1;
-            const uint32_t xb = x0 + b * 2 * C * 128;
-            if (!tc::mbar_wait(&sm.rput, c & 1, kPolls) || !tc::mbar_wait(&sm.ready[b], (c >> 1) & 1, kPolls) ||
-                !(c == 0 || tc::mbar_wait(&sm.out, (c & 1) ^ 1, kPolls)))
-                return;
+            const uint64_t xb = dx + b * (2 * C * 128 >> 4);
+            if (!tc::mbar_wait(&sm.rput, c & 1, kPolls) || !tc::mbar_wait(&sm.ready[b], (c >> 1) & 1, kPolls)) return false;
             tc::fence_after();
 #pragma unroll
             for (int m = 0; m < 12; ++m)
                 tc16::mma_ts(tm + TU, tm + (m < 8 ? TRH : TRL) + 8 * (m & 3),
-                             tc16::kmajor(xb + (m >= 4 && m < 8 ? C * 128 : 0) + (m & 3) * 32), id, m);
+                             xb + (((m >= 4 && m < 8 ? C * 128 : 0) + (m & 3) * 32) >> 4), id, m);
             tc::commit(&sm.u);
+            return true;
         };
         auto issue_dz = [&](int c) {   // the increment of S^T (K's rows along the summed index), (A U')^T
             const int b = c & 1;
-            const uint32_t kq = kq0 + b * 2 * kHalf, ab = a0 + b * Sm::AT * C * 128;
-            if (!tc::mbar_wait(&sm.uput, c & 1, kPolls)) return;
+            const uint64_t kn = dn + b * (2 * kHalf >> 4), ab = da + b * (Sm::AT * C * 128 >> 4);
+            if (!tc::mbar_wait(&sm.uput[b], (c >> 1) & 1, kPolls)) return false;
             tc::fence_after();
 #pragma unroll
             for (int m = 0; m < 8; ++m)
-                tc16::mma_ts(tm + TD, tm + (m < 4 ? TFH : TFL) + 8 * (m & 3), tc16::desc(kq + (m & 3) * 2048, kHalf, 1024), id_mn, m);
+                tc16::mma_ts(tm + TD, tm + (m < 4 ? TFH : TFL) + 8 * (m & 3), kn + ((m & 3) * 2048 >> 4), id_mn, m);
             tc::commit(&sm.d);
 #pragma unroll
             for (int m = 0; m < (TWO ? 12 : 4); ++m)
                 tc16::mma_ts(tm + TU, tm + (m >= 4 && m < 8 ? TUL : TUH) + 8 * (m & 3),
-                             tc16::kmajor(ab + (m >= 8 ? C * 128 : 0) + (m & 3) * 32), id, m);
-            tc::commit(&sm.z);
+                             ab + (((m >= 8 ? C * 128 : 0) + (m & 3) * 32) >> 4), id, m);
+            tc::commit(&sm.z[b]);
+            return true;
         };
         put(0, fmaxf(sm.smx[0][j], sm.smx[1][j]));
 #pragma unroll 1
         for (int c = 0; c < chunks && ok; ++c) {
             const int b = c & 1;
             const uint32_t ph = c & 1;
-            if (tid == 0) issue_wy(c);
-            __syncwarp();
+            if (tid == 0) ok = issue_wy(c);
+            ok = __all_sync(0xffffffffu, ok);
             // R from W^T and V
-            ok = warp_wait(&sm.sput, ph) && warp_wait(&sm.wy, ph);
+            ok = ok && warp_wait(&sm.sput, ph) && warp_wait(&sm.wy, ph);
             if (!ok) break;
             tc::fence_after();
             float sR;
@@ -281,10 +289,10 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             tc::fence_before();
             mbar_arrive(&sm.rput);
-            if (tid == 0) issue_u(c);
-            __syncwarp();
+            if (tid == 0) ok = issue_u(c);
+            ok = __all_sync(0xffffffffu, ok);
             // U' and diag(gamma_C / gamma) U'
-            ok = warp_wait(&sm.u, ph);
+            ok = ok && warp_wait(&sm.u, ph);
             if (!ok) break;
             tc::fence_after();
             float um = 0.0f;
@@ -311,11 +319,11 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 tc16::st_wait();
             }
             tc::fence_before();
-            mbar_arrive(&sm.uput);
-            if (tid == 0) issue_dz(c);
-            __syncwarp();
+            mbar_arrive(&sm.uput[b]);
+            if (tid == 0) ok = issue_dz(c);
+            ok = __all_sync(0xffffffffu, ok);
             // S
-            ok = warp_wait(&sm.uput, ph) && warp_wait(&sm.d, ph);
+            ok = ok && warp_wait(&sm.uput[b], (c >> 1) & 1) && warp_wait(&sm.d, ph);
             if (!ok) break;
             tc::fence_after();
             const float last = sm.gl[b];
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             sm.smx[hh][j] = fmaxf(m0, m1);
             mbar_arrive(&sm.empty[b]);
             // U' as an operand stands where S goes
-            ok = warp_wait(&sm.z, ph);
+            ok = warp_wait(&sm.z[b], (c >> 1) & 1);
             if (c + 1 < chunks) put(c + 1, fmaf(last, before, 128.0f * sR * um));   // |K'^T u'| <= 64 * 2 * max |u'|
         }
         if (ok) {
@@ -349,22 +357,29 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
     } else {
         // ---- prepare ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        const int p = tid - NS, pw = p >> 5;
-        const uint32_t quad = tm + ((uint32_t)(32 * (pw & 3)) << 16);
+        const int gp = (warp - NS / 32) >> 2, p = tid - NS - gp * NP, pw = p >> 5;   // group, thread and warp of the group
+        const int bar = 2 + gp, b = gp;                                              // a group's chunks use its buffers
+        const uint32_t quad = tm + ((uint32_t)(32 * pw) << 16);
+        const int r0 = p >> 4, i8 = p & 15;                                          // 16 lanes to a row: rows r0 + 8 i
         const T *gq = static_cast<const T *>(a.q) + (size_t)hk * D, *gk = static_cast<const T *>(a.k) + (size_t)hk * D;
         const T *gv = static_cast<const T *>(a.v) + (size_t)h * D;
+        float *const n = sm.n[gp], *const ks = sm.ks[gp], *const lg = sm.lg[gp], *const be = sm.be[gp], *const e2 = sm.e2[gp];
         bool gates_ok = true;
-        float al[2] = {1.0f, 1.0f}, bt[2] = {0.0f, 0.0f};   // warp 7: a chunk's gates, two tokens a lane
+        // warp 3: a chunk's gates, two tokens a lane: base-2 logarithms of the running products in the chunk, and from them
+        // gamma, gamma_C / gamma, and gamma at the end of the token's block of 16 over gamma
+        float al[2] = {1.0f, 1.0f}, bt[2] = {0.0f, 0.0f}, lgt[2], total = 0.0f;
+        float2 gam, fin, blk;
         // the rows of a chunk into L2 ahead of their loads, its gates into registers
         auto prefetch = [&](int c) {
             const int cc = min(C, count - c * C);
-            const size_t tok0 = (size_t)(first + c * C);
-            for (int e = p; e < 6 * cc; e += NP) {   // two lines of 128 bytes a row
-                const size_t tok = tok0 + e / 6;
-                const T *src = e % 3 == 0 ? gk + tok * a.ks : e % 3 == 1 ? gq + tok * a.qs : gv + tok * a.vs;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (e % 6 >= 3 ? D / 2 : 0)) : "memory");
+            const size_t tok0 = (size_t)(first + c * C), tok = tok0 + (p >> 1);
+            if ((p >> 1) < cc) {
+                const int half = (p & 1) * (D / 2);   // 128 bytes
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(gk + tok * a.ks + half) : "memory");
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(gq + tok * a.qs + half) : "memory");
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(gv + tok * a.vs + half) : "memory");
             }
-            if (pw == 7) {
+            if (pw == 3) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = 2 * lane + e;
@@ -373,104 +388,122 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 }
             }
         };
-        // O of chunk c: Y^T and (A U')^T to rows of V's buffer, and from there to global memory
-        auto output = [&](int c) {
-            const int b = c & 1, cc = min(C, count - c * C), j = 32 * (pw & 3) + lane, t0 = 32 * (pw >> 2);
-            ok = warp_wait(&sm.uput, c & 1) && warp_wait(&sm.z, c & 1);
-            tc::fence_after();
-            {
-                uint32_t y[32], z[32];
-                tc::ld32(quad + TY + C * b + t0, y);
-                tc::ld32(quad + TU + t0, z);
-                tc::fence_before();
-                mbar_arrive(&sm.out);
-                const float sS = sm.ss[b][j], sR = sm.sr[b][j];
-                T *dst = sm.v[b] + t0 * D + j;
+        auto running = [&]() {
+            gates_ok = gates_ok && al[0] > 0.0f && al[0] <= 1.0f && al[1] > 0.0f && al[1] <= 1.0f;
+            const float l1 = log2f(al[1]);
+            float sum = log2f(al[0]) + l1;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 g = *reinterpret_cast<const float2 *>(&sm.go[b][t0 + 2 * i]);
-                    const float2 q = *reinterpret_cast<const float2 *>(&sm.qs[b][t0 + 2 * i]);
-                    const float2 o = fma2(g, mul2(pair_of(y, i), both(sS)), mul2(q, mul2(pair_of(z, i), both(sR))));
-                    dst[2 * i * D] = from_f32<T>(o.x);
-                    dst[(2 * i + 1) * D] = from_f32<T>(o.y);
-                }
+            for (int m = 1; m < 32; m <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, sum, m);
+                if (lane >= m) sum += y;
             }
-            ok = tc16::group_and(2, NP, ok);
-            if (!ok) return;
-            T *dst = static_cast<T *>(a.o) + (size_t)(first + c * C) * a.os + h * D + (p & 15) * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = (p >> 4) + 16 * i;
-                if (r < cc) *reinterpret_cast<uint4 *>(dst + r * a.os) = *reinterpret_cast<const uint4 *>(sm.v[b] + r * D + (p & 15) * 8);
-            }
+            total = __shfl_sync(0xffffffffu, sum, 31);
+            const float block = __shfl_sync(0xffffffffu, sum, lane | 7);
+            lgt[0] = sum - l1;
+            lgt[1] = sum;
+            gam = make_float2(exp2f(lgt[0]), exp2f(lgt[1]));
+            fin = make_float2(exp2f(total - lgt[0]), exp2f(total - lgt[1]));
+            blk = make_float2(exp2f(block - lgt[0]), exp2f(block - lgt[1]));
         };
-        prefetch(0);
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const int b = c & 1, cc = min(C, count - c * C);
-            const size_t tok0 = (size_t)(first + c * C);
-            ok = tc::mbar_wait(&sm.empty[b], ((c >> 1) & 1) ^ 1, kPolls);
-            ok = tc16::group_and(2, NP, ok);
-            if (!ok) break;
-            {   // 16 lanes a row of 128 values: rows p / 16 + 16 i
-                const int r0 = p >> 4, i8 = p & 15;
-                uint4 raw_k[4], raw_q[4];
+        // K and Q rows as they are into their operand places (16-bit types all), zeros behind the last token; 64 rows keep
+        // a row's place in its group of eight
+        const uint32_t at0 = (i8 >> 3) * kHalf + tc16::sw_off(r0, (i8 & 7) * 8);
+        auto load_kq = [&](int c) {
+            const int cc = min(C, count - c * C);
+            const T *k = gk + (size_t)(first + c * C + r0) * a.ks + i8 * 8, *q = gq + (size_t)(first + c * C + r0) * a.qs + i8 * 8;
+            uint8_t *dst = sm.kq[b] + at0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + 16 * i;
-                    const bool in = r < cc;
-                    const size_t tok = tok0 + (in ? r : 0);
-                    raw_k[i] = in ? __ldg(reinterpret_cast<const uint4 *>(gk + tok * a.ks) + i8) : make_uint4(0, 0, 0, 0);
-                    raw_q[i] = in ? __ldg(reinterpret_cast<const uint4 *>(gq + tok * a.qs) + i8) : make_uint4(0, 0, 0, 0);
-                    copy16(sm.v[b] + r * D + i8 * 8, gv + tok * a.vs + i8 * 8, in);
-                }
-                // arrives when this thread's copies have landed
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_addr(&sm.vfull[b])) : "memory");
+            for (int i = 0; i < 8; ++i) {
+                const bool in = r0 + 8 * i < cc;
+                copy16(dst, in ? k : gk, in);
+                copy16(dst + C * 128, in ? q : gq, in);
+                dst += 8 * 128;
+                k += 8 * a.ks;
+                q += 8 * a.qs;
+            }
+            cp_async_commit();
+        };
+        auto load_v = [&](int c) {
+            const int cc = min(C, count - c * C);
+            const T *v = gv + (size_t)(first + c * C + r0) * a.vs + i8 * 8;
+            T *dst = sm.v[b] + r0 * D + i8 * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = r0 + 8 * i < cc;
+                copy16(dst + 8 * i * D, in ? v : gv, in);
+                v += 8 * a.vs;
+            }
+            // arrives when this thread's copies have landed
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_addr(&sm.vfull[b])) : "memory");
+        };
+        if (gp < chunks) {
+            prefetch(gp);
+            load_kq(gp);
+            load_v(gp);
+            if (pw == 3) running();
+        }
+#pragma unroll 1
+        for (int c = gp; c < chunks; c += 2) {
+            const int cc = min(C, count - c * C);
+            const uint32_t ph2 = (c >> 1) & 1;
+            // this thread's own copies: rows scaled to a largest value in [1, 2), as fp16
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+            for (int i0 = 0; i0 < 16; i0 += 8) {   // eight pieces at a time: rows r0 + 8 i of K, then of Q
+                uint8_t *at = sm.kq[b] + at0 + (i0 ? C * 128 : 0);
+                uint4 rw[8];
+                float m[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) rw[i] = *reinterpret_cast<const uint4 *>(at + i * 8 * 128);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint4 rw = i < 4 ? raw_k[i & 3] : raw_q[i & 3];
-                    const T2 *pr = reinterpret_cast<const T2 *>(&rw);
-                    const int r = r0 + 16 * (i & 3);
-                    T2 m2 = __hmax2(__hmax2(__habs2(pr[0]), __habs2(pr[1])), __hmax2(__habs2(pr[2]), __habs2(pr[3])));
-                    const float2 mf = to_f32x2(m2);
-                    float m = fmaxf(mf.x, mf.y);
+                    const T2 *pr = reinterpret_cast<const T2 *>(&rw[i]);
+                    const float2 mf = to_f32x2(__hmax2(__hmax2(__habs2(pr[0]), __habs2(pr[1])), __hmax2(__habs2(pr[2]), __habs2(pr[3]))));
+                    m[i] = fmaxf(mf.x, mf.y);
+                }
 #pragma unroll
-                    for (int w = 8; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-                    const int e = exponent_of(m);
+                for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], w));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const T2 *pr = reinterpret_cast<const T2 *>(&rw[i]);
+                    const int e = exponent_of(m[i]);
                     const float2 inv = both(__uint_as_float((uint32_t)(254 - e) << 23));
                     uint4 out;
                     out.x = tc16::pack2(mul2(to_f32x2(pr[0]), inv));
                     out.y = tc16::pack2(mul2(to_f32x2(pr[1]), inv));
                     out.z = tc16::pack2(mul2(to_f32x2(pr[2]), inv));
                     out.w = tc16::pack2(mul2(to_f32x2(pr[3]), inv));
-                    // K rows, then Q rows: both start on a group of eight rows
-                    *reinterpret_cast<uint4 *>(sm.kq[b] + (i8 >> 3) * kHalf + (i < 4 ? 0 : C * 128) + tc16::sw_off(r, (i8 & 7) * 8)) = out;
-                    if (i8 == 0) (i < 4 ? sm.ks : sm.qs[b])[r] = __uint_as_float((uint32_t)e << 23);
+                    *reinterpret_cast<uint4 *>(at + i * 8 * 128) = out;
+                    if (i8 == 0) (i0 ? sm.qs[b] : ks)[r0 + 8 * i] = __uint_as_float((uint32_t)e << 23);
                 }
             }
-            const float g0 = al[0], g1 = al[1], b0 = bt[0], b1 = bt[1];
-            if (c + 1 < chunks) prefetch(c + 1);
             tc::fence_smem_to_async();
-            tc16::group_and(2, NP, true);
-            if (pw == 7) {   // running products in base 2, and what is formed from them
-                gates_ok = gates_ok && g0 > 0.0f && g0 <= 1.0f && g1 > 0.0f && g1 <= 1.0f;
-                const float l0 = log2f(g0), l1 = log2f(g1);
-                float sum = l0 + l1;
+            ok = tc::mbar_wait(&sm.empty[b], ph2 ^ 1, kPolls);   // the state is done with the last chunk's gates
+            ok = tc16::group_and(bar, NP, ok);
+            if (!ok) break;
+            if (p == 0) {   // [K; Q] K^T
+                const uint64_t kq = tc16::kmajor(tc::smem_addr(sm.kq[b]));
+                tc::fence_after();
 #pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const float y = __shfl_up_sync(0xffffffffu, sum, m);
-                    if (lane >= m) sum += y;
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t at = kq + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                    tc16::mma_ss(tm + TG + C * gp, at, at, tc16::idesc(128, C, false), kk);
                 }
-                const float total = __shfl_sync(0xffffffffu, sum, 31), mid = sum - l1;
-                const float2 gam = make_float2(exp2f(mid), exp2f(sum)), bb = make_float2(b0, b1);
-                const float2 kk = *reinterpret_cast<const float2 *>(&sm.ks[2 * lane]);
+                tc::commit(&sm.g[gp]);
+            }
+            if (pw == 3) {   // the token's factors
+                const float2 bb = make_float2(bt[0], bt[1]);
+                const float2 kk = *reinterpret_cast<const float2 *>(&ks[2 * lane]);
                 const float2 qq = *reinterpret_cast<const float2 *>(&sm.qs[b][2 * lane]);
                 const float2 gkk = mul2(gam, kk), bkk = mul2(bb, kk);
-                *reinterpret_cast<float2 *>(&sm.lg[2 * lane]) = make_float2(mid, sum);
-                *reinterpret_cast<float2 *>(&sm.be[2 * lane]) = mul2(bkk, kk);
+                *reinterpret_cast<float2 *>(&lg[2 * lane]) = make_float2(lgt[0], lgt[1]);
+                *reinterpret_cast<float2 *>(&be[2 * lane]) = mul2(bkk, kk);
+                *reinterpret_cast<float2 *>(&e2[2 * lane]) = blk;
                 *reinterpret_cast<float2 *>(&sm.gk[b][2 * lane]) = gkk;
                 *reinterpret_cast<float2 *>(&sm.bk[b][2 * lane]) = bkk;
-                *reinterpret_cast<float2 *>(&sm.f[b][2 * lane]) = make_float2(exp2f(total - mid), exp2f(total - sum));
+                *reinterpret_cast<float2 *>(&sm.f[b][2 * lane]) = fin;
                 *reinterpret_cast<float2 *>(&sm.go[b][2 * lane]) = mul2(gam, qq);
                 float mb = fmaxf(fabsf(bkk.x), fabsf(bkk.y)), mg = fmaxf(fabsf(gkk.x), fabsf(gkk.y));
 #pragma unroll
@@ -485,138 +518,154 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 }
             }
             mbar_arrive(&sm.full[b]);
-            if (p == 0) {   // [K; Q] K^T
-                tc::fence_after();
-                const uint32_t kq = tc::smem_addr(sm.kq[b]), id = tc16::idesc(128, C, false);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t at = tc16::kmajor(kq + (kk >> 2) * kHalf + (kk & 3) * 32);
-                    tc16::mma_ss(tm + TG, at, at, id, kk);
-                }
-                tc::commit(&sm.g);
-            }
-            ok = warp_wait(&sm.full[b], (c >> 1) & 1) && warp_wait(&sm.g, c & 1);
+            if (c + 2 < chunks) prefetch(c + 2);
+            ok = warp_wait(&sm.full[b], ph2) && warp_wait(&sm.g[gp], ph2);
             tc::fence_after();
+            // A row of Gamma o [K; Q] K^T a lane.  Right of the diagonal: N is not read there, A is 0.  Columns of an
+            // earlier block of 16: Gamma_ts as gamma_t over gamma at that block's end, times e2_s, each at most 1.
             {
-                const int t = (32 * pw + lane) & 63, s0 = 32 * (pw >> 2);
-                const float lt = sm.lg[t], bt2 = sm.be[t];
-                uint32_t g[32];
-                tc::ld32(quad + TG + s0, g);
-                float x[32];
+                const int t = (32 * pw + lane) & 63;
+                const bool is_n = pw < 2;
+                const float lt = lg[t], row = is_n ? be[t] : 1.0f;
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 ls = *reinterpret_cast<const float4 *>(&sm.lg[s0 + e]);
-                    x[e] = ex2(fminf(lt - ls.x, 0.0f)) * __uint_as_float(g[e]);
-                    x[e + 1] = ex2(fminf(lt - ls.y, 0.0f)) * __uint_as_float(g[e + 1]);
-                    x[e + 2] = ex2(fminf(lt - ls.z, 0.0f)) * __uint_as_float(g[e + 2]);
-                    x[e + 3] = ex2(fminf(lt - ls.w, 0.0f)) * __uint_as_float(g[e + 3]);
-                }
-                if ((pw & 3) < 2) {
+                for (int s0 = 0; s0 < C; s0 += 16) {
+                    if (s0 >= 32 && !(pw & 1)) {   // rows below 32
+                        if (!is_n) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(&sm.n[t * SN + s0 + e]) =
-                            make_float4(s0 + e < t ? bt2 * x[e] : 0.0f, s0 + e + 1 < t ? bt2 * x[e + 1] : 0.0f,
-                                        s0 + e + 2 < t ? bt2 * x[e + 2] : 0.0f, s0 + e + 3 < t ? bt2 * x[e + 3] : 0.0f);
-                } else {
+                            for (int e = 0; e < 16; e += 8)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int ss = s0 + e + 2 * i;
-                            const float2 y = make_float2(ss <= t ? x[e + 2 * i] : 0.0f, ss + 1 <= t ? x[e + 2 * i + 1] : 0.0f);
-                            if constexpr (TWO) tc16::split2(y, hi[i], lo[i]);
-                            else hi[i] = tc16::pack2(y);
+                                for (int m = 0; m < Sm::AT; ++m)
+                                    *reinterpret_cast<uint4 *>(sm.a[b] + m * C * 128 + tc16::sw_off(t, s0 + e)) = make_uint4(0, 0, 0, 0);
                         }
-                        uint8_t *dst = sm.a[b] + tc16::sw_off(t, s0 + e);
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if constexpr (TWO) *reinterpret_cast<uint4 *>(dst + C * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        continue;
+                    }
+                    uint32_t g[16];
+                    tc16::ld16(quad + TG + C * gp + s0, g);
+                    float2 x[8];
+                    if (s0 < 32 && (pw & 1)) {     // an earlier block for every row of the warp
+                        const float2 far = both(row * ex2(lt - lg[s0 + 15]));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            x[i] = mul2(mul2(far, *reinterpret_cast<const float2 *>(&e2[s0 + 2 * i])), pair_of(g, i));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 ls = *reinterpret_cast<const float2 *>(&lg[s0 + 2 * i]);
+                            const float2 y = make_float2(ex2(fminf(lt - ls.x, 0.0f)), ex2(fminf(lt - ls.y, 0.0f)));
+                            x[i] = mul2(mul2(both(row), y), pair_of(g, i));
+                            if (s0 + 2 * i > t) x[i].x = 0.0f;
+                            if (s0 + 2 * i + 1 > t) x[i].y = 0.0f;
+                        }
+                    }
+                    if (is_n) {
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2)
+                            *reinterpret_cast<float4 *>(&n[t * SN + s0 + 2 * i]) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (TWO) tc16::split2(x[4 * e + i], hi[i], lo[i]);
+                                else hi[i] = tc16::pack2(x[4 * e + i]);
+                            }
+                            uint8_t *dst = sm.a[b] + tc16::sw_off(t, s0 + 8 * e);
+                            *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            if constexpr (TWO) *reinterpret_cast<uint4 *>(dst + C * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
                     }
                 }
             }
             tc::fence_before();
-            ok = tc16::group_and(2, NP, ok);
+            ok = tc16::group_and(bar, NP, ok);
             if (!ok) break;
-            // (I + N)^-1 in place: the diagonal blocks of 16 by substitution, a column a lane
-            if (pw < 4) {
-                const int r0 = 16 * pw, col = lane & 15;
+            // (I + N)^-1 in place: the diagonal blocks of 16 by substitution, a warp a block, a column a lane
+            {
+                const int d0 = 16 * pw, col = lane & 15;
                 float x[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     float y0 = r == col ? 1.0f : 0.0f, y1 = 0.0f;
 #pragma unroll
                     for (int m = 0; m + 1 < r; m += 2) {
-                        const float2 nn = *reinterpret_cast<const float2 *>(&sm.n[(r0 + r) * SN + r0 + m]);
+                        const float2 nn = *reinterpret_cast<const float2 *>(&n[(d0 + r) * SN + d0 + m]);
                         y0 = fmaf(-nn.x, x[m], y0);
                         y1 = fmaf(-nn.y, x[m + 1], y1);
                     }
-                    if (r & 1) y0 = fmaf(-sm.n[(r0 + r) * SN + r0 + r - 1], x[r - 1], y0);
+                    if (r & 1) y0 = fmaf(-n[(d0 + r) * SN + d0 + r - 1], x[r - 1], y0);
                     x[r] = y0 + y1;
                 }
                 __syncwarp();
                 if (lane < 16) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) sm.n[(r0 + r) * SN + r0 + col] = x[r];
+                    for (int r = 0; r < 16; ++r) n[(d0 + r) * SN + d0 + col] = x[r];
                 }
             }
-            tc16::group_and(2, NP, true);
-            // pairs of blocks of M rows at r0 (upper) and r0 + M (lower): the block below the diagonal becomes
-            // -X_lower N X_upper; a warp does 16 x 8 of it, operands as two fp16 terms, three products
-            auto join = [&](auto m_, bool mine, int r0, int row, int col) {
-                constexpr int M = decltype(m_)::value;
+            tc16::group_and(bar, NP, true);
+            // pairs of blocks of M rows at u0 (upper) and u0 + M (lower): the block below the diagonal becomes
+            // -X_lower (N X_upper), the product in brackets in the unused top right quarter; a warp does 16 x 8 TILES of it,
+            // operands as two fp16 terms, three products
+            auto join = [&](auto m_, auto tiles_, int u0, int row, int col) {
+                constexpr int M = decltype(m_)::value, TILES = decltype(tiles_)::value;
                 const int g = lane >> 2, q = 2 * (lane & 3);
-                float acc[4];
-                auto product = [&](const float *l, const float *r) {
-                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-                    if (!mine) return;
+                auto product = [&](const float *l, const float *r, float *out, float sign) {
+                    float acc[TILES][4];
+#pragma unroll
+                    for (int y = 0; y < TILES; ++y) acc[y][0] = acc[y][1] = acc[y][2] = acc[y][3] = 0.0f;
 #pragma unroll
                     for (int k = 0; k < M; k += 16) {
-                        uint32_t ah[4], al[4], bh[2], bl[2];
+                        uint32_t ah[4], al_[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            tc16::split2(*reinterpret_cast<const float2 *>(l + (row + g + 8 * (i & 1)) * SN + k + q + 8 * (i >> 1)), ah[i], al[i]);
+                            tc16::split2(*reinterpret_cast<const float2 *>(l + (row + g + 8 * (i & 1)) * SN + k + q + 8 * (i >> 1)), ah[i], al_[i]);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float *y = r + (k + q + 8 * i) * SN + col + g;
-                            tc16::split2(make_float2(y[0], y[SN]), bh[i], bl[i]);
+                        for (int y = 0; y < TILES; ++y) {
+                            uint32_t bh[2], bl[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float *x = r + (k + q + 8 * i) * SN + col + 8 * y + g;
+                                tc16::split2(make_float2(x[0], x[SN]), bh[i], bl[i]);
+                            }
+                            tc16::mma_sync(acc[y], ah, bh);
+                            tc16::mma_sync(acc[y], ah, bl);
+                            tc16::mma_sync(acc[y], al_, bh);
                         }
-                        tc16::mma_sync(acc, ah, bh);
-                        tc16::mma_sync(acc, ah, bl);
-                        tc16::mma_sync(acc, al, bh);
                     }
-                };
-                float *nb = &sm.n[(r0 + M) * SN + r0];
-                auto store = [&](float sign) {
-                    tc16::group_and(2, NP, true);   // every read of the block is done
-                    if (mine) {
-                        *reinterpret_cast<float2 *>(nb + (row + g) * SN + col + q) = make_float2(sign * acc[0], sign * acc[1]);
-                        *reinterpret_cast<float2 *>(nb + (row + g + 8) * SN + col + q) = make_float2(sign * acc[2], sign * acc[3]);
-                    }
-                    tc16::group_and(2, NP, true);
-                };
-                product(nb, &sm.n[r0 * SN + r0]);
-                store(1.0f);
-                product(&sm.n[(r0 + M) * SN + r0 + M], nb);
-                store(-1.0f);
-            };
-            join(std::integral_constant<int, 16>(), pw < 4, pw & 2 ? 32 : 0, 0, 8 * (pw & 1));
-            join(std::integral_constant<int, 32>(), true, 0, 16 * (pw >> 2), 8 * (pw & 3));
-            {   // X as operand, zeros right of the diagonal
-                const int t = p & 63;
-                float m = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int s0 = 16 * (p >> 6) + 8 * e;
+                    for (int y = 0; y < TILES; ++y) {
+                        float *o = out + (row + g) * SN + col + 8 * y + q;
+                        *reinterpret_cast<float2 *>(o) = make_float2(sign * acc[y][0], sign * acc[y][1]);
+                        *reinterpret_cast<float2 *>(o + 8 * SN) = make_float2(sign * acc[y][2], sign * acc[y][3]);
+                    }
+                    tc16::group_and(bar, NP, true);
+                };
+                float *below = n + (u0 + M) * SN + u0, *right = n + u0 / 2 * SN + C / 2;
+                product(below, n + u0 * SN + u0, right, 1.0f);
+                product(n + (u0 + M) * SN + u0 + M, right, below, -1.0f);
+            };
+            join(std::integral_constant<int, 16>(), std::integral_constant<int, 1>(), pw & 2 ? 32 : 0, 0, 8 * (pw & 1));
+            join(std::integral_constant<int, 32>(), std::integral_constant<int, 2>(), 0, 16 * (pw >> 1), 16 * (pw & 1));
+            {   // X as operand, zeros right of the diagonal
+                const int t = p & 63, s0 = 32 * (p >> 6);
+                float m = 0.0f;
+                float4 y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = *reinterpret_cast<const float4 *>(&n[t * SN + s0 + 4 * i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float2 y = *reinterpret_cast<const float2 *>(&sm.n[t * SN + s0 + 2 * i]);
-                        if (s0 + 2 * i > t) y.x = 0.0f;
-                        if (s0 + 2 * i + 1 > t) y.y = 0.0f;
-                        m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
-                        tc16::split2(y, hi[i], lo[i]);
+                        const float4 y4 = y[2 * e + i / 2];
+                        float2 x = i & 1 ? make_float2(y4.z, y4.w) : make_float2(y4.x, y4.y);
+                        const int ss = s0 + 8 * e + 2 * i;
+                        if (ss > t) x.x = 0.0f;
+                        if (ss + 1 > t) x.y = 0.0f;
+                        m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+                        tc16::split2(x, hi[i], lo[i]);
                     }
-                    uint8_t *dst = sm.x[b] + tc16::sw_off(t, s0);
+                    uint8_t *dst = sm.x[b] + tc16::sw_off(t, s0 + 8 * e);
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(dst + C * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
@@ -624,19 +673,67 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.ready[b]);
-            if (c > 0) {
-                output(c - 1);
-                if (!ok) break;
+            if (pw == 3 && c + 2 < chunks) running();
+            // the chunk's last product is done: K, Q, X, A have been read, Y^T and (A U')^T are there
+            ok = warp_wait(&sm.uput[b], ph2) && warp_wait(&sm.z[b], ph2);
+            tc::fence_after();
+            if (ok && c + 2 < chunks) load_kq(c + 2);
+            // O to rows of V's buffer, and from there to global memory
+            {
+                const int j = 32 * pw + lane;
+                const float sS = sm.ss[b][j], sR = sm.sr[b][j];
+#pragma unroll
+                for (int t0 = 0; t0 < C; t0 += 16) {
+                    float4 g[4], q[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        g[i] = *reinterpret_cast<const float4 *>(&sm.go[b][t0 + 4 * i]);
+                        q[i] = *reinterpret_cast<const float4 *>(&sm.qs[b][t0 + 4 * i]);
+                    }
+                    uint32_t y[16], z[16];
+                    tc16::ld16(quad + TY + t0, y);
+                    tc16::ld16(quad + TU + t0, z);
+                    if (t0 + 16 == C) {
+                        tc::fence_before();
+                        mbar_arrive(&sm.out);
+                    }
+                    T *dst = sm.v[b] + t0 * D + j;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 g4 = g[i / 2], q4 = q[i / 2];
+                        const float2 g2 = i & 1 ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y);
+                        const float2 q2 = i & 1 ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
+                        const float2 o = fma2(g2, mul2(pair_of(y, i), both(sS)), mul2(q2, mul2(pair_of(z, i), both(sR))));
+                        dst[2 * i * D] = from_f32<T>(o.x);
+                        dst[(2 * i + 1) * D] = from_f32<T>(o.y);
+                    }
+                }
             }
+            ok = tc16::group_and(bar, NP, ok);
+            if (!ok) break;
+            {
+                T *dst = static_cast<T *>(a.o) + (size_t)(first + c * C) * a.os + h * D + i8 * 8;
+                uint4 y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = *reinterpret_cast<const uint4 *>(sm.v[b] + (r0 + 8 * i) * D + i8 * 8);
+                dst += r0 * a.os;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (r0 + 8 * i < cc) *reinterpret_cast<uint4 *>(dst) = y[i];
+                    dst += 8 * a.os;
+                }
+            }
+            // a thread's copies of V go where it alone has read
+            if (c + 2 < chunks) load_v(c + 2);
         }
-        if (ok) output(chunks - 1);
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (!gates_ok) atomicOr(a.err, kErrGateRange);
     }
     // A product may still be in flight only after a wait gave up: let it end (bounded) before its memory is given
     // back.  A commit covers what its own thread has issued.
-    if (!__syncthreads_and(ok) && (tid == 0 || tid == NS)) {
+    if (!__syncthreads_and(ok) && (tid == 0 || tid == NS || tid == NS + NP)) {
         if (tid == 0) atomicOr(a.err, kErrWait);
-        uint64_t *bar = &sm.drain[tid == 0 ? 0 : 1];
+        uint64_t *bar = &sm.drain[tid == 0 ? 0 : tid == NS ? 1 : 2];
         tc::commit(bar);
         if (!tc::mbar_wait(bar, 0, kPolls)) atomicOr(a.err, kErrTmemDrain);
     }
