@@ -70,7 +70,7 @@ struct Smem {
     float gl[2], mb[2], mg[2];                 // gamma_C, the largest beta ks, the largest gamma ks
     float smx[2][D], vmx[2][D], umx[2][D];     // largest |S|, |v|, |u'| of a lane, by half
     float ss[2][D], sr[2][D];                  // a lane's scales of the S and R terms
-    alignas(8) uint64_t full[2], vfull[2], ready[2], empty[2], sput, rput, uput[2], wy, u, d, z[2], out, g[2], drain[3];
+    alignas(8) uint64_t full[2], vfull[2], ready[2], empty[2], sput, rput, uput[2], w, u, d, z[2], out, g[2], drain[3];
     uint32_t taddr;
 };
 
@@ -115,6 +115,10 @@ template <>
 struct Pair<__nv_bfloat16> {
     using type = __nv_bfloat162;
 };
+__device__ __forceinline__ __half2 lows(__half2 x, __half2 y) { return __lows2half2(x, y); }
+__device__ __forceinline__ __half2 highs(__half2 x, __half2 y) { return __highs2half2(x, y); }
+__device__ __forceinline__ __nv_bfloat162 lows(__nv_bfloat162 x, __nv_bfloat162 y) { return __lows2bfloat162(x, y); }
+__device__ __forceinline__ __nv_bfloat162 highs(__nv_bfloat162 x, __nv_bfloat162 y) { return __highs2bfloat162(x, y); }
 __device__ __forceinline__ float2 to_f32x2(__half2 x) { return __half22float2(x); }
 __device__ __forceinline__ float2 to_f32x2(__nv_bfloat162 x) { return __bfloat1622float2(x); }
 
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
         }
         for (uint64_t *b : {&sm.sput, &sm.rput}) mbar_init_n(b, NS);
         mbar_init_n(&sm.out, NP);
-        for (uint64_t *b : {&sm.wy, &sm.u, &sm.d, &sm.drain[0], &sm.drain[1], &sm.drain[2]}) mbar_init_n(b, 1);
+        for (uint64_t *b : {&sm.w, &sm.u, &sm.d, &sm.drain[0], &sm.drain[1], &sm.drain[2]}) mbar_init_n(b, 1);
         fence_mbar_init();
     }
     if (warp == 0) tc::alloc(&sm.taddr, 512);
@@ -204,64 +208,79 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             tc::fence_before();
             mbar_arrive(&sm.sput);
         };
-        // The products, by thread 0 once every thread's operands are in place.  A descriptor's address field counts 16 bytes.
+        // The products, by warp 0 once every thread's operands are in place: one elected lane, operands from values that the
+        // compiler knows to be the same in all lanes (otherwise each of them is moved to the uniform registers by itself, 110
+        // cycles an instruction).  A descriptor's address field counts 16 bytes.
+        const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
         const uint64_t dk = tc16::kmajor(tc::smem_addr(sm.kq)), dx = tc16::kmajor(tc::smem_addr(sm.x)),
                        da = tc16::kmajor(tc::smem_addr(sm.a)), dn = tc16::desc(tc::smem_addr(sm.kq), kHalf, 1024);
         constexpr uint32_t id = tc16::idesc(128, C, false), id_mn = tc16::idesc(128, D, true);
-        auto issue_wy = [&](int c) {   // W^T = S^T K'^T; Y^T = S^T Q'^T, where the last chunk's output has been read
-            const int b = c & 1;
+        auto issue_w = [&](int b, uint32_t ph, uint32_t ph2) {    // W^T = S^T K'^T
+            if (!warp_wait(&sm.sput, ph) || !warp_wait(&sm.full[b], ph2)) return false;
+            tc::fence_after();
             const uint64_t kq = dk + b * (2 * kHalf >> 4);
-            if (!tc::mbar_wait(&sm.sput, c & 1, kPolls) || !tc::mbar_wait(&sm.full[b], (c >> 1) & 1, kPolls)) return false;
-            tc::fence_after();
+            if (tc16::elect()) {
 #pragma unroll
-            for (int m = 0; m < 16; ++m)
-                tc16::mma_ts(tm + TW, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7), kq + ((((m >> 2) & 1) * kHalf + (m & 3) * 32) >> 4), id, m);
-            tc::commit(&sm.wy);
-            if (c > 0 && !tc::mbar_wait(&sm.out, (c & 1) ^ 1, kPolls)) return false;
-            tc::fence_after();
-#pragma unroll
-            for (int m = 0; m < 8 * Sm::AT; ++m)
-                tc16::mma_ts(tm + TY, tm + (m < 8 ? TSH : TSL) + 8 * (m & 7),
-                             kq + ((C * 128 + ((m >> 2) & 1) * kHalf + (m & 3) * 32) >> 4), id, m);
+                for (int m = 0; m < 16; ++m)
+                    tc16::mma_ts(tmu + TW, tmu + (m < 8 ? TSH : TSL) + 8 * (m & 7), kq + ((((m >> 2) & 1) * kHalf + (m & 3) * 32) >> 4), id, m);
+                tc::commit(&sm.w);
+            }
+            __syncwarp();
             return true;
         };
-        auto issue_u = [&](int c) {    // U'^T = R^T X^T
-            const int b = c & 1;
-            const uint64_t xb = dx + b * (2 * C * 128 >> 4);
-            if (!tc::mbar_wait(&sm.rput, c & 1, kPolls) || !tc::mbar_wait(&sm.ready[b], (c >> 1) & 1, kPolls)) return false;
+        auto issue_yu = [&](int b, uint32_t ph, uint32_t ph2, bool fresh_y) {
+            // Y^T = S^T Q'^T, where the last chunk's output has been read
+            if (!fresh_y && !warp_wait(&sm.out, ph ^ 1)) return false;
             tc::fence_after();
+            const uint64_t q = dk + ((b * 2 * kHalf + C * 128) >> 4), xb = dx + b * (2 * C * 128 >> 4);
+            if (tc16::elect()) {
 #pragma unroll
-            for (int m = 0; m < 12; ++m)
-                tc16::mma_ts(tm + TU, tm + (m < 8 ? TRH : TRL) + 8 * (m & 3),
-                             xb + (((m >= 4 && m < 8 ? C * 128 : 0) + (m & 3) * 32) >> 4), id, m);
-            tc::commit(&sm.u);
+                for (int m = 0; m < 8 * Sm::AT; ++m)
+                    tc16::mma_ts(tmu + TY, tmu + (m < 8 ? TSH : TSL) + 8 * (m & 7), q + ((((m >> 2) & 1) * kHalf + (m & 3) * 32) >> 4), id, m);
+            }
+            __syncwarp();
+            // U'^T = R^T X^T
+            if (!warp_wait(&sm.rput, ph) || !warp_wait(&sm.ready[b], ph2)) return false;
+            tc::fence_after();
+            if (tc16::elect()) {
+#pragma unroll
+                for (int m = 0; m < 12; ++m)
+                    tc16::mma_ts(tmu + TU, tmu + (m < 8 ? TRH : TRL) + 8 * (m & 3),
+                                 xb + (((m >= 4 && m < 8 ? C * 128 : 0) + (m & 3) * 32) >> 4), id, m);
+                tc::commit(&sm.u);
+            }
+            __syncwarp();
             return true;
         };
-        auto issue_dz = [&](int c) {   // the increment of S^T (K's rows along the summed index), (A U')^T
-            const int b = c & 1;
+        auto issue_dz = [&](int b, uint32_t ph2) {
+            if (!warp_wait(&sm.uput[b], ph2)) return false;
+            tc::fence_after();
             const uint64_t kn = dn + b * (2 * kHalf >> 4), ab = da + b * (Sm::AT * C * 128 >> 4);
-            if (!tc::mbar_wait(&sm.uput[b], (c >> 1) & 1, kPolls)) return false;
-            tc::fence_after();
+            if (tc16::elect()) {
+                // the increment of S^T: K's rows along the summed index
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
-                tc16::mma_ts(tm + TD, tm + (m < 4 ? TFH : TFL) + 8 * (m & 3), kn + ((m & 3) * 2048 >> 4), id_mn, m);
-            tc::commit(&sm.d);
+                for (int m = 0; m < 8; ++m)
+                    tc16::mma_ts(tmu + TD, tmu + (m < 4 ? TFH : TFL) + 8 * (m & 3), kn + ((m & 3) * 2048 >> 4), id_mn, m);
+                tc::commit(&sm.d);
+                // (A U')^T
 #pragma unroll
-            for (int m = 0; m < (TWO ? 12 : 4); ++m)
-                tc16::mma_ts(tm + TU, tm + (m >= 4 && m < 8 ? TUL : TUH) + 8 * (m & 3),
-                             ab + (((m >= 8 ? C * 128 : 0) + (m & 3) * 32) >> 4), id, m);
-            tc::commit(&sm.z[b]);
+                for (int m = 0; m < (TWO ? 12 : 4); ++m)
+                    tc16::mma_ts(tmu + TU, tmu + (m >= 4 && m < 8 ? TUL : TUH) + 8 * (m & 3),
+                                 ab + (((m >= 8 ? C * 128 : 0) + (m & 3) * 32) >> 4), id, m);
+                tc::commit(&sm.z[b]);
+            }
+            __syncwarp();
             return true;
         };
-        put(0, fmaxf(sm.smx[0][j], sm.smx[1][j]));
+        float bound = fmaxf(sm.smx[0][j], sm.smx[1][j]);
 #pragma unroll 1
-        for (int c = 0; c < chunks && ok; ++c) {
-            const int b = c & 1;
-            const uint32_t ph = c & 1;
-            if (tid == 0) ok = issue_wy(c);
-            ok = __all_sync(0xffffffffu, ok);
+        for (int c = 0; c < chunks; ++c) {
+            const int b = __shfl_sync(0xffffffffu, c & 1, 0);
+            const uint32_t ph = b, ph2 = (c >> 1) & 1;
+            put(c, bound);
+            if (warp == 0) ok = issue_w(b, ph, ph2) && ok;
             // R from W^T and V
-            ok = ok && warp_wait(&sm.sput, ph) && warp_wait(&sm.wy, ph);
+            ok = ok && warp_wait(&sm.sput, ph) && warp_wait(&sm.w, ph);
             if (!ok) break;
             tc::fence_after();
             float sR;
@@ -289,8 +308,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             tc::fence_before();
             mbar_arrive(&sm.rput);
-            if (tid == 0) ok = issue_u(c);
-            ok = __all_sync(0xffffffffu, ok);
+            if (warp == 0) ok = issue_yu(b, ph, ph2, c == 0) && ok;
             // U' and diag(gamma_C / gamma) U'
             ok = ok && warp_wait(&sm.u, ph);
             if (!ok) break;
@@ -320,10 +338,9 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             tc::fence_before();
             mbar_arrive(&sm.uput[b]);
-            if (tid == 0) ok = issue_dz(c);
-            ok = __all_sync(0xffffffffu, ok);
+            if (warp == 0) ok = issue_dz(b, ph2) && ok;
             // S
-            ok = ok && warp_wait(&sm.uput[b], (c >> 1) & 1) && warp_wait(&sm.d, ph);
+            ok = ok && warp_wait(&sm.uput[b], ph2) && warp_wait(&sm.d, ph);
             if (!ok) break;
             tc::fence_after();
             const float last = sm.gl[b];
@@ -344,8 +361,9 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             sm.smx[hh][j] = fmaxf(m0, m1);
             mbar_arrive(&sm.empty[b]);
             // U' as an operand stands where S goes
-            ok = warp_wait(&sm.z[b], (c >> 1) & 1);
-            if (c + 1 < chunks) put(c + 1, fmaf(last, before, 128.0f * sR * um));   // |K'^T u'| <= 64 * 2 * max |u'|
+            ok = warp_wait(&sm.z[b], ph2);
+            if (!ok) break;
+            bound = fmaf(last, before, 128.0f * sR * um);   // |K'^T u'| <= 64 * 2 * max |u'|
         }
         if (ok) {
 #pragma unroll
@@ -369,22 +387,13 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
         // gamma, gamma_C / gamma, and gamma at the end of the token's block of 16 over gamma
         float al[2] = {1.0f, 1.0f}, bt[2] = {0.0f, 0.0f}, lgt[2], total = 0.0f;
         float2 gam, fin, blk;
-        // the rows of a chunk into L2 ahead of their loads, its gates into registers
-        auto prefetch = [&](int c) {
-            const int cc = min(C, count - c * C);
-            const size_t tok0 = (size_t)(first + c * C), tok = tok0 + (p >> 1);
-            if ((p >> 1) < cc) {
-                const int half = (p & 1) * (D / 2);   // 128 bytes
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(gk + tok * a.ks + half) : "memory");
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(gq + tok * a.qs + half) : "memory");
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(gv + tok * a.vs + half) : "memory");
-            }
+        auto load_gates = [&](int c) {
             if (pw == 3) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int t = 2 * lane + e;
-                    al[e] = t < cc ? __ldg(a.alpha + (tok0 + t) * a.H + h) : 1.0f;
-                    bt[e] = t < cc ? __ldg(a.beta + (tok0 + t) * a.H + h) : 0.0f;
+                    const int t = c * C + 2 * lane + e;
+                    al[e] = t < count ? __ldg(a.alpha + (size_t)(first + t) * a.H + h) : 1.0f;
+                    bt[e] = t < count ? __ldg(a.beta + (size_t)(first + t) * a.H + h) : 0.0f;
                 }
             }
         };
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             const int cc = min(C, count - c * C);
             const T *k = gk + (size_t)(first + c * C + r0) * a.ks + i8 * 8, *q = gq + (size_t)(first + c * C + r0) * a.qs + i8 * 8;
             uint8_t *dst = sm.kq[b] + at0;
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {
                 const bool in = r0 + 8 * i < cc;
                 copy16(dst, in ? k : gk, in);
@@ -427,7 +436,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             const int cc = min(C, count - c * C);
             const T *v = gv + (size_t)(first + c * C + r0) * a.vs + i8 * 8;
             T *dst = sm.v[b] + r0 * D + i8 * 8;
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {
                 const bool in = r0 + 8 * i < cc;
                 copy16(dst + 8 * i * D, in ? v : gv, in);
@@ -436,62 +445,122 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             // arrives when this thread's copies have landed
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_addr(&sm.vfull[b])) : "memory");
         };
-        if (gp < chunks) {
-            prefetch(gp);
-            load_kq(gp);
-            load_v(gp);
-            if (pw == 3) running();
-        }
+        load_gates(gp);
 #pragma unroll 1
-        for (int c = gp; c < chunks; c += 2) {
-            const int cc = min(C, count - c * C);
+        for (int c = gp; c < chunks + 2; c += 2) {
+            const int done = c - 2;              // the group's last chunk, whose output comes before the next one's loads
+            const bool more = c < chunks;
             const uint32_t ph2 = (c >> 1) & 1;
+            if (pw == 3 && more) running();
+            if (done >= 0) {
+                // its last product is done: K, Q, X, A have been read, Y^T and (A U')^T are there
+                ok = warp_wait(&sm.uput[b], ph2 ^ 1) && warp_wait(&sm.z[b], ph2 ^ 1);
+                tc::fence_after();
+            }
+            if (ok && more) load_kq(c);
+            if (done >= 0) {
+                const int cc = min(C, count - done * C);
+                // O to rows of V's buffer, and from there to global memory
+                {
+                    const int j = 32 * pw + lane;
+                    const float sS = sm.ss[b][j], sR = sm.sr[b][j];
+#pragma unroll 1
+                    for (int t0 = 0; t0 < C; t0 += 16) {
+                        float4 g[4], q[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            g[i] = *reinterpret_cast<const float4 *>(&sm.go[b][t0 + 4 * i]);
+                            q[i] = *reinterpret_cast<const float4 *>(&sm.qs[b][t0 + 4 * i]);
+                        }
+                        uint32_t y[16], z[16];
+                        tc16::ld16x2(quad + TY + t0, y, quad + TU + t0, z);
+                        if (t0 + 16 == C) {
+                            tc::fence_before();
+                            mbar_arrive(&sm.out);
+                        }
+                        T *dst = sm.v[b] + t0 * D + j;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 g4 = g[i / 2], q4 = q[i / 2];
+                            const float2 g2 = i & 1 ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y);
+                            const float2 q2 = i & 1 ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
+                            const float2 o = fma2(g2, mul2(pair_of(y, i), both(sS)), mul2(q2, mul2(pair_of(z, i), both(sR))));
+                            dst[2 * i * D] = from_f32<T>(o.x);
+                            dst[(2 * i + 1) * D] = from_f32<T>(o.y);
+                        }
+                    }
+                }
+                ok = tc16::group_and(bar, NP, ok);
+                if (!ok) break;
+                {
+                    T *dst = static_cast<T *>(a.o) + (size_t)(first + done * C) * a.os + h * D + i8 * 8;
+                    uint4 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = *reinterpret_cast<const uint4 *>(sm.v[b] + (r0 + 8 * i) * D + i8 * 8);
+                    dst += r0 * a.os;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (r0 + 8 * i < cc) *reinterpret_cast<uint4 *>(dst) = y[i];
+                        dst += 8 * a.os;
+                    }
+                }
+            }
+            if (!more) break;
+            load_v(c);                           // a thread's copies of V go where it alone has read the output
             // this thread's own copies: rows scaled to a largest value in [1, 2), as fp16
             asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-            for (int i0 = 0; i0 < 16; i0 += 8) {   // eight pieces at a time: rows r0 + 8 i of K, then of Q
-                uint8_t *at = sm.kq[b] + at0 + (i0 ? C * 128 : 0);
+#pragma unroll 1
+            for (int i0 = 0; i0 < 8; i0 += 4) {   // pieces of four rows r0 + 8 i of K and of Q at a time
+                uint8_t *at = sm.kq[b] + at0 + i0 * 8 * 128;
                 uint4 rw[8];
-                float m[8];
+                T2 m[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) rw[i] = *reinterpret_cast<const uint4 *>(at + i * 8 * 128);
+                for (int i = 0; i < 8; ++i) rw[i] = *reinterpret_cast<const uint4 *>(at + (i & 1) * C * 128 + (i >> 1) * 8 * 128);
+                auto most = [](const uint4 &x) {
+                    const T2 *pr = reinterpret_cast<const T2 *>(&x);
+                    return __hmax2(__hmax2(__habs2(pr[0]), __habs2(pr[1])), __hmax2(__habs2(pr[2]), __habs2(pr[3])));
+                };
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const T2 *pr = reinterpret_cast<const T2 *>(&rw[i]);
-                    const float2 mf = to_f32x2(__hmax2(__hmax2(__habs2(pr[0]), __habs2(pr[1])), __hmax2(__habs2(pr[2]), __habs2(pr[3]))));
-                    m[i] = fmaxf(mf.x, mf.y);
+                for (int i = 0; i < 4; ++i) {     // (of K, of Q)
+                    const T2 k = most(rw[2 * i]), q = most(rw[2 * i + 1]);
+                    m[i] = __hmax2(lows(k, q), highs(k, q));
                 }
 #pragma unroll
                 for (int w = 8; w > 0; w >>= 1)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], w));
+                    for (int i = 0; i < 4; ++i) m[i] = __hmax2(m[i], __shfl_xor_sync(0xffffffffu, m[i], w));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const T2 *pr = reinterpret_cast<const T2 *>(&rw[i]);
-                    const int e = exponent_of(m[i]);
+                    const float2 mf = to_f32x2(m[i >> 1]);
+                    const int e = exponent_of(i & 1 ? mf.y : mf.x);
                     const float2 inv = both(__uint_as_float((uint32_t)(254 - e) << 23));
                     uint4 out;
                     out.x = tc16::pack2(mul2(to_f32x2(pr[0]), inv));
                     out.y = tc16::pack2(mul2(to_f32x2(pr[1]), inv));
                     out.z = tc16::pack2(mul2(to_f32x2(pr[2]), inv));
                     out.w = tc16::pack2(mul2(to_f32x2(pr[3]), inv));
-                    *reinterpret_cast<uint4 *>(at + i * 8 * 128) = out;
-                    if (i8 == 0) (i0 ? sm.qs[b] : ks)[r0 + 8 * i] = __uint_as_float((uint32_t)e << 23);
+                    *reinterpret_cast<uint4 *>(at + (i & 1) * C * 128 + (i >> 1) * 8 * 128) = out;
+                    if (i8 == 0) (i & 1 ? sm.qs[b] : ks)[r0 + 8 * (i0 + (i >> 1))] = __uint_as_float((uint32_t)e << 23);
                 }
             }
             tc::fence_smem_to_async();
             ok = tc::mbar_wait(&sm.empty[b], ph2 ^ 1, kPolls);   // the state is done with the last chunk's gates
             ok = tc16::group_and(bar, NP, ok);
             if (!ok) break;
-            if (p == 0) {   // [K; Q] K^T
-                const uint64_t kq = tc16::kmajor(tc::smem_addr(sm.kq[b]));
+            if (pw == 0) {   // [K; Q] K^T
+                const uint64_t kq = tc16::kmajor(tc::smem_addr(sm.kq)) + __shfl_sync(0xffffffffu, b, 0) * (2 * kHalf >> 4);
+                const uint32_t dst = __shfl_sync(0xffffffffu, tm + TG + C * gp, 0);
                 tc::fence_after();
+                if (tc16::elect()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t at = kq + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                    tc16::mma_ss(tm + TG + C * gp, at, at, tc16::idesc(128, C, false), kk);
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint64_t at = kq + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                        tc16::mma_ss(dst, at, at, tc16::idesc(128, C, false), kk);
+                    }
+                    tc::commit(&sm.g[gp]);
                 }
-                tc::commit(&sm.g[gp]);
+                __syncwarp();
             }
             if (pw == 3) {   // the token's factors
                 const float2 bb = make_float2(bt[0], bt[1]);
@@ -518,7 +587,16 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 }
             }
             mbar_arrive(&sm.full[b]);
-            if (c + 2 < chunks) prefetch(c + 2);
+            if (c + 2 < chunks) {   // the next chunk's gates into registers, its rows into L2
+                load_gates(c + 2);
+                const int t = (c + 2) * C + (p >> 1), half = (p & 1) * (D / 2);
+                if (t < count) {
+                    const size_t tok = (size_t)(first + t);
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(gk + tok * a.ks + half) : "memory");
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(gq + tok * a.qs + half) : "memory");
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(gv + tok * a.vs + half) : "memory");
+                }
+            }
             ok = warp_wait(&sm.full[b], ph2) && warp_wait(&sm.g[gp], ph2);
             tc::fence_after();
             // A row of Gamma o [K; Q] K^T a lane.  Right of the diagonal: N is not read there, A is 0.  Columns of an
@@ -527,43 +605,43 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 const int t = (32 * pw + lane) & 63;
                 const bool is_n = pw < 2;
                 const float lt = lg[t], row = is_n ? be[t] : 1.0f;
-#pragma unroll
-                for (int s0 = 0; s0 < C; s0 += 16) {
-                    if (s0 >= 32 && !(pw & 1)) {   // rows below 32
+#pragma unroll 1
+                for (int s0 = 0; s0 < C; s0 += 32) {
+                    if (s0 > 0 && !(pw & 1)) {     // right of the diagonal for every row of the warp
                         if (!is_n) {
 #pragma unroll
-                            for (int e = 0; e < 16; e += 8)
+                            for (int e = 0; e < 32; e += 8)
 #pragma unroll
                                 for (int m = 0; m < Sm::AT; ++m)
                                     *reinterpret_cast<uint4 *>(sm.a[b] + m * C * 128 + tc16::sw_off(t, s0 + e)) = make_uint4(0, 0, 0, 0);
                         }
                         continue;
                     }
-                    uint32_t g[16];
-                    tc16::ld16(quad + TG + C * gp + s0, g);
-                    float2 x[8];
-                    if (s0 < 32 && (pw & 1)) {     // an earlier block for every row of the warp
-                        const float2 far = both(row * ex2(lt - lg[s0 + 15]));
+                    uint32_t g[32];
+                    tc::ld32(quad + TG + C * gp + s0, g);
+                    float2 x[16];
+                    if (s0 == 0 && (pw & 1)) {     // earlier blocks for every row of the warp
+                        const float2 far[2] = {both(row * ex2(lt - lg[15])), both(row * ex2(lt - lg[31]))};
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            x[i] = mul2(mul2(far, *reinterpret_cast<const float2 *>(&e2[s0 + 2 * i])), pair_of(g, i));
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = mul2(mul2(far[i >> 3], *reinterpret_cast<const float2 *>(&e2[2 * i])), pair_of(g, i));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             const float2 ls = *reinterpret_cast<const float2 *>(&lg[s0 + 2 * i]);
-                            const float2 y = make_float2(ex2(fminf(lt - ls.x, 0.0f)), ex2(fminf(lt - ls.y, 0.0f)));
-                            x[i] = mul2(mul2(both(row), y), pair_of(g, i));
+                            const float2 y = make_float2(ex2(lt - ls.x), ex2(lt - ls.y));   // right of the diagonal: anything
+                            x[i] = mul2(is_n ? mul2(both(row), y) : y, pair_of(g, i));
                             if (s0 + 2 * i > t) x[i].x = 0.0f;
                             if (s0 + 2 * i + 1 > t) x[i].y = 0.0f;
                         }
                     }
                     if (is_n) {
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2)
+                        for (int i = 0; i < 16; i += 2)
                             *reinterpret_cast<float4 *>(&n[t * SN + s0 + 2 * i]) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int e = 0; e < 4; ++e) {
                             uint32_t hi[4], lo[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -673,70 +751,19 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.ready[b]);
-            if (pw == 3 && c + 2 < chunks) running();
-            // the chunk's last product is done: K, Q, X, A have been read, Y^T and (A U')^T are there
-            ok = warp_wait(&sm.uput[b], ph2) && warp_wait(&sm.z[b], ph2);
-            tc::fence_after();
-            if (ok && c + 2 < chunks) load_kq(c + 2);
-            // O to rows of V's buffer, and from there to global memory
-            {
-                const int j = 32 * pw + lane;
-                const float sS = sm.ss[b][j], sR = sm.sr[b][j];
-#pragma unroll
-                for (int t0 = 0; t0 < C; t0 += 16) {
-                    float4 g[4], q[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        g[i] = *reinterpret_cast<const float4 *>(&sm.go[b][t0 + 4 * i]);
-                        q[i] = *reinterpret_cast<const float4 *>(&sm.qs[b][t0 + 4 * i]);
-                    }
-                    uint32_t y[16], z[16];
-                    tc16::ld16(quad + TY + t0, y);
-                    tc16::ld16(quad + TU + t0, z);
-                    if (t0 + 16 == C) {
-                        tc::fence_before();
-                        mbar_arrive(&sm.out);
-                    }
-                    T *dst = sm.v[b] + t0 * D + j;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 g4 = g[i / 2], q4 = q[i / 2];
-                        const float2 g2 = i & 1 ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y);
-                        const float2 q2 = i & 1 ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
-                        const float2 o = fma2(g2, mul2(pair_of(y, i), both(sS)), mul2(q2, mul2(pair_of(z, i), both(sR))));
-                        dst[2 * i * D] = from_f32<T>(o.x);
-                        dst[(2 * i + 1) * D] = from_f32<T>(o.y);
-                    }
-                }
-            }
-            ok = tc16::group_and(bar, NP, ok);
-            if (!ok) break;
-            {
-                T *dst = static_cast<T *>(a.o) + (size_t)(first + c * C) * a.os + h * D + i8 * 8;
-                uint4 y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = *reinterpret_cast<const uint4 *>(sm.v[b] + (r0 + 8 * i) * D + i8 * 8);
-                dst += r0 * a.os;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (r0 + 8 * i < cc) *reinterpret_cast<uint4 *>(dst) = y[i];
-                    dst += 8 * a.os;
-                }
-            }
-            // a thread's copies of V go where it alone has read
-            if (c + 2 < chunks) load_v(c + 2);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (!gates_ok) atomicOr(a.err, kErrGateRange);
     }
     // A product may still be in flight only after a wait gave up: let it end (bounded) before its memory is given
     // back.  A commit covers what its own thread has issued.
-    if (!__syncthreads_and(ok) && (tid == 0 || tid == NS || tid == NS + NP)) {
-        if (tid == 0) atomicOr(a.err, kErrWait);
-        uint64_t *bar = &sm.drain[tid == 0 ? 0 : tid == NS ? 1 : 2];
+    if (!__syncthreads_and(ok) && (warp & 3) == 0 && (warp == 0 || warp >= NS / 32) && tc16::elect()) {
+        if (warp == 0) atomicOr(a.err, kErrWait);
+        uint64_t *bar = &sm.drain[warp == 0 ? 0 : warp == NS / 32 ? 1 : 2];
         tc::commit(bar);
         if (!tc::mbar_wait(bar, 0, kPolls)) atomicOr(a.err, kErrTmemDrain);
     }
+    __syncwarp();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
