@@ -759,17 +759,19 @@ extern "C" int stepq_ctx_create(const stepq_plan *plan, void *main_stream, void 
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    cudaDeviceProp prop;
-    e = cudaGetDeviceProperties(&prop, dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDeviceProperties");
-    if (prop.major < 10) return fail(STEPQ_ECUDA, "ctx_create: device %d is sm_%d%d; this library is built for sm_100a", dev, prop.major, prop.minor);
+    int major = 0, minor = 0, sms = 0;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return cuda_fail(e, "cudaDeviceGetAttribute");
+    if (major < 10) return fail(STEPQ_ECUDA, "ctx_create: device %d is sm_%d%d; this library is built for sm_100a", dev, major, minor);
     if (plan->mode == 1 && plan->D != 128)
         return fail(STEPQ_EINVAL, "ctx_create: per-key-row plans run on the device at d = 128 only (d = %d)", plan->D);
     stepq_ctx *c = new (std::nothrow) stepq_ctx;
     if (!c) return fail(STEPQ_ENOMEM, "ctx_create: out of memory");
     c->plan = plan;
     c->device = dev;
-    c->n_sms = prop.multiProcessorCount;
+    c->n_sms = sms;
     c->n_slots = n_slots;
     c->chunk = chunk_layers > 0 ? chunk_layers : 4;
     c->main = static_cast<cudaStream_t>(main_stream);

@@ -26,18 +26,19 @@ extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, in
     if (page_tokens < 16 || page_tokens > 65536 || page_tokens % 16)
         return fail(STEPQ_EINVAL, "kv_create: page_tokens %d (a multiple of 16, at most 65536)", page_tokens);
     if (n_pages < 1) return fail(STEPQ_EINVAL, "kv_create: n_pages %d", n_pages);
-    int dev = 0;
-    cudaDeviceProp prop;
+    int dev = 0, major = 0, minor = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if ((e = cudaGetDeviceProperties(&prop, dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDeviceProperties");
-    if (prop.major < 10)
-        return fail(STEPQ_ECUDA, "kv_create: device %d is sm_%d%d; this library is built for sm_100a", dev, prop.major, prop.minor);
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return cuda_fail(e, "cudaDeviceGetAttribute");
+    if (major < 10) return fail(STEPQ_ECUDA, "kv_create: device %d is sm_%d%d; this library is built for sm_100a", dev, major, minor);
     stepq_kv *kv = new (std::nothrow) stepq_kv;
     if (!kv) return fail(STEPQ_ENOMEM, "kv_create: out of memory");
     kv->g = {bits, n_heads, d, page_tokens, n_pages, nullptr};
     kv->device = dev;
-    kv->n_sms = prop.multiProcessorCount;
+    kv->n_sms = sms;
     e = cudaMalloc(&kv->g.err, sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(kv->g.err, 0, sizeof(int));
     if (e != cudaSuccess) {

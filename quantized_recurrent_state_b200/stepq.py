@@ -152,44 +152,59 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _dtype_codes():
-    import torch
-    return {torch.float32: FP32, torch.float16: FP16, torch.bfloat16: BF16}
+_codes = {}
 
 
-def _want(ok, msg):
-    if not ok:
-        raise StepqError(EINVAL, msg)
+def _dtype_code(t, name):
+    """The STEPQ_* code of a tensor's type."""
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: FP32, torch.float16: FP16, torch.bfloat16: BF16})
+    code = _codes.get(t.dtype)
+    if code is None:
+        _refuse(f"{name} is {t.dtype}: float32, float16 or bfloat16")
+    return code
 
 
-def _on(t, device, name):
-    _want(t.is_cuda and t.device.index == device, f"{name} is on {t.device}, not on cuda:{device}")
+# Checks of the tensors given to the calls below.  They run on every call, so messages are formed only where one fails.
+
+def _refuse(msg):
+    raise StepqError(EINVAL, msg)
 
 
 def _dense(t, device, dtype, numel, name):
     """A contiguous device tensor of `numel` elements: its address."""
-    _on(t, device, name)
-    _want(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
-    _want(t.is_contiguous(), f"{name} is not contiguous")
-    _want(t.numel() == numel, f"{name} has {t.numel()} elements, not {numel}")
+    if t.get_device() != device:
+        _refuse(f"{name} is on {t.device}, not on cuda:{device}")
+    if t.dtype is not dtype:
+        _refuse(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_contiguous():
+        _refuse(f"{name} is not contiguous")
+    if t.numel() != numel:
+        _refuse(f"{name} has {t.numel()} elements, not {numel}")
     return t.data_ptr()
 
 
 def _row_stride(t, lead, heads, d, name):
     """Stride in elements of the rows of t [*lead, heads, d], which have to lie evenly spaced."""
-    _want(tuple(t.shape) == (*lead, heads, d), f"{name} has the shape {tuple(t.shape)}, not {(*lead, heads, d)}")
+    if t.shape != (*lead, heads, d):
+        _refuse(f"{name} has the shape {tuple(t.shape)}, not {(*lead, heads, d)}")
     st = t.stride()
-    _want((d == 1 or st[-1] == 1) and (heads == 1 or st[-2] == d), f"{name}: a row's heads are not contiguous")
-    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1:
-        _want(st[0] == lead[1] * st[1], f"{name}: the rows are not evenly spaced")
+    if st[-1] != 1 or (heads > 1 and st[-2] != d):
+        _refuse(f"{name}: a row's heads are not contiguous")
+    if len(lead) == 2 and lead[1] > 1:
+        if lead[0] > 1 and st[0] != lead[1] * st[1]:
+            _refuse(f"{name}: the rows are not evenly spaced")
         return st[1]
-    return next((s for n, s in zip(lead, st) if n > 1), heads * d)
+    return st[0] if lead[0] > 1 else heads * d
 
 
 def _rows(t, device, dtype, lead, heads, d, name):
     """Device token rows [*lead, heads, d]: (address, stride in elements)."""
-    _on(t, device, name)
-    _want(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != device:
+        _refuse(f"{name} is on {t.device}, not on cuda:{device}")
+    if t.dtype is not dtype:
+        _refuse(f"{name} is {t.dtype}, not {dtype}")
     return t.data_ptr(), _row_stride(t, lead, heads, d, name)
 
 
@@ -337,56 +352,57 @@ class Context:
     def _delta(self, S, slots, n_seq, lead, q, k, v, alpha, beta, o):
         """Checked arguments shared by delta_step and delta_prefill: (S, slots, Tokens)."""
         import torch
-        p, dev = self.plan, self.device
-        code = _dtype_codes().get(q.dtype)
-        _want(code is not None, f"q is {q.dtype}: float32, float16 or bfloat16 tokens")
-        _want(q.dim() == len(lead) + 2, f"q has {q.dim()} dimensions")
+        p, dev, dt = self.plan, self.device, q.dtype
+        code, h, d = _dtype_code(q, "q"), p.n_heads, p.d
         hk, n_tok = q.shape[-2], lead[0] * (lead[1] if len(lead) > 1 else 1)
-        t = Tokens(dtype=code, n_qk_heads=hk)
-        t.q, t.q_stride = _rows(q, dev, q.dtype, lead, hk, p.d, "q")
-        t.k, t.k_stride = _rows(k, dev, q.dtype, lead, hk, p.d, "k")
-        t.v, t.v_stride = _rows(v, dev, q.dtype, lead, p.n_heads, p.d, "v")
-        t.o, t.o_stride = _rows(o, dev, q.dtype, lead, p.n_heads, p.d, "o")
-        t.alpha = _dense(alpha, dev, torch.float32, n_tok * p.n_heads * (p.d if p.mode else 1), "alpha")
-        t.beta = _dense(beta, dev, torch.float32, n_tok * p.n_heads, "beta")
-        per = p.n_heads * p.d * p.d
+        qp, qs = _rows(q, dev, dt, lead, hk, d, "q")
+        kp, ks = _rows(k, dev, dt, lead, hk, d, "k")
+        vp, vs = _rows(v, dev, dt, lead, h, d, "v")
+        op, os_ = _rows(o, dev, dt, lead, h, d, "o")
+        f32 = torch.float32
+        t = Tokens(code, hk, qp, kp, vp, _dense(alpha, dev, f32, n_tok * h * (d if p.mode else 1), "alpha"),
+                   _dense(beta, dev, f32, n_tok * h, "beta"), op, qs, ks, vs, os_)
         if slots is None:
-            return _dense(S, dev, torch.float32, n_seq * per, "S"), None, t
-        return (_dense(S, dev, torch.float32, self.n_slots * p.n_layers * per, "S"),
+            return _dense(S, dev, f32, n_seq * h * d * d, "S"), None, t
+        return (_dense(S, dev, f32, self.n_slots * p.n_layers * h * d * d, "S"),
                 _dense(slots, dev, torch.int32, n_seq, "slots"), t)
 
     def _ordered(self, call, *args):
         """call(*args) on main, after the caller's current stream and before what it enqueues next."""
         import torch
-        cur, l = torch.cuda.current_stream(self.device).cuda_stream, lib()
+        cur = torch.cuda.current_stream(self.device).cuda_stream
         if cur == self.main.cuda_stream:
             return _check(call(self._h, *args))
-        _check(l.stepq_ctx_wait_stream(self._h, cur))
+        _check(_lib.stepq_ctx_wait_stream(self._h, cur))
         _check(call(self._h, *args))
-        return _check(l.stepq_stream_wait_ctx(self._h, cur))
+        return _check(_lib.stepq_stream_wait_ctx(self._h, cur))
 
     def delta_step(self, S, slots, q, k, v, alpha, beta, o, layer: int = 0):
         """The gated delta rule for the next token(s) of every request: q, k [n_seq, n_tok, n_qk_heads, d],
         v, o [n_seq, n_tok, n_heads, d] (float32, float16 or bfloat16; rows may be slices of wider ones),
         alpha, beta as in stepq.h; S the fp32 pool (slots given) or [n_seq, n_heads, d, d], updated."""
-        _want(q.dim() == 4, f"q has {q.dim()} dimensions, not 4")
+        if q.dim() != 4:
+            _refuse(f"q has {q.dim()} dimensions, not 4")
         n, n_tok = q.shape[0], q.shape[1]
         S, slots, t = self._delta(S, slots, n, (n, n_tok), q, k, v, alpha, beta, o)
-        return self._ordered(lib().stepq_delta_step, layer, S, slots, n, n_tok, ctypes.byref(t))
+        return self._ordered(_lib.stepq_delta_step, layer, S, slots, n, n_tok, t)
 
     def delta_prefill(self, S, slots, cu_seqlens, q, k, v, alpha, beta, o, layer: int = 0, fresh=None):
         """The gated delta rule over a ragged batch: sequence s has the rows [cu_seqlens[s], cu_seqlens[s + 1])
         of q, k [n_tokens, n_qk_heads, d] and v, o [n_tokens, n_heads, d]; fresh [n_seq] uint8 or bool marks those
         that start from a zero state."""
         import torch
+        if q.dim() != 3:
+            _refuse(f"q has {q.dim()} dimensions, not 3")
         n = cu_seqlens.numel() - 1
-        _want(n >= 0, "cu_seqlens is empty")
+        if n < 0:
+            _refuse("cu_seqlens is empty")
         cu = _dense(cu_seqlens, self.device, torch.int32, n + 1, "cu_seqlens")
         if fresh is not None:
             fresh = _dense(fresh, self.device, torch.bool if fresh.dtype == torch.bool else torch.uint8, n, "fresh")
         tokens = q.shape[0]
         S, slots, t = self._delta(S, slots, n, (tokens,), q, k, v, alpha, beta, o)
-        return self._ordered(lib().stepq_delta_prefill, layer, S, slots, fresh, n, cu, tokens, ctypes.byref(t))
+        return self._ordered(_lib.stepq_delta_prefill, layer, S, slots, fresh, n, cu, tokens, t)
 
     def set_step_kernel(self, kernel: int):
         return _check(lib().stepq_ctx_set_step_kernel(self._h, kernel))
@@ -470,7 +486,8 @@ class KVCache:
 
     def _table(self, page_table, lens):
         import torch
-        _want(page_table.dim() == 2, f"page_table has {page_table.dim()} dimensions, not 2")
+        if page_table.dim() != 2:
+            _refuse(f"page_table has {page_table.dim()} dimensions, not 2")
         n, most = page_table.shape
         return (n, _dense(page_table, self.device, torch.int32, n * most, "page_table"), most,
                 _dense(lens, self.device, torch.int32, n, "lens"))
@@ -478,53 +495,52 @@ class KVCache:
     def append(self, cache, k, v, places):
         """Quantise the rows k, v [n_tokens, n_heads, d] into the cache at places [n_tokens] (int64)."""
         import torch
-        code, n = _dtype_codes().get(k.dtype), k.shape[0]
-        _want(code is not None, f"k is {k.dtype}: float32, float16 or bfloat16")
-        kp, ks = _rows(k, self.device, k.dtype, (n,), self.n_heads, self.d, "k")
-        vp, vs = _rows(v, self.device, k.dtype, (n,), self.n_heads, self.d, "v")
-        places = _dense(places, self.device, torch.int64, n, "places")
-        return _check(lib().stepq_kv_append(self._h, self._cache(cache), code, n, kp, vp, ks, vs, places, self._stream()))
+        code, dev, dt, lead = _dtype_code(k, "k"), self.device, k.dtype, k.shape[:1]
+        kp, ks = _rows(k, dev, dt, lead, self.n_heads, self.d, "k")
+        vp, vs = _rows(v, dev, dt, lead, self.n_heads, self.d, "v")
+        places = _dense(places, dev, torch.int64, lead[0], "places")
+        return _check(_lib.stepq_kv_append(self._h, self._cache(cache), code, lead[0], kp, vp, ks, vs, places, self._stream()))
 
     def read(self, cache, page_table, lens, cu_seqlens, k, v):
         """Read the sequences back into the rows k, v [n_rows, n_heads, d], sequence s from row cu_seqlens[s] on."""
         import torch
-        code, rows = _dtype_codes().get(k.dtype), k.shape[0]
-        _want(code is not None, f"k is {k.dtype}: float32, float16 or bfloat16")
+        code, dev, dt, lead = _dtype_code(k, "k"), self.device, k.dtype, k.shape[:1]
         n, table, most, lens = self._table(page_table, lens)
-        _on(cu_seqlens, self.device, "cu_seqlens")
-        _want(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= n,
-              f"cu_seqlens: {n} contiguous int32 row numbers (or {n + 1})")
-        kp, ks = _rows(k, self.device, k.dtype, (rows,), self.n_heads, self.d, "k")
-        vp, vs = _rows(v, self.device, k.dtype, (rows,), self.n_heads, self.d, "v")
-        return _check(lib().stepq_kv_read(self._h, self._cache(cache), n, table, most, lens, cu_seqlens.data_ptr(), rows, code,
-                                          kp, vp, ks, vs, self._stream()))
+        if (cu_seqlens.get_device() != dev or cu_seqlens.dtype is not torch.int32 or not cu_seqlens.is_contiguous()
+                or cu_seqlens.numel() < n):
+            _refuse(f"cu_seqlens: {n} (or {n + 1}) contiguous int32 row numbers on cuda:{dev}")
+        kp, ks = _rows(k, dev, dt, lead, self.n_heads, self.d, "k")
+        vp, vs = _rows(v, dev, dt, lead, self.n_heads, self.d, "v")
+        return _check(_lib.stepq_kv_read(self._h, self._cache(cache), n, table, most, lens, cu_seqlens.data_ptr(), lead[0],
+                                         code, kp, vp, ks, vs, self._stream()))
 
     def attend(self, cache, q, page_table, lens, scale, o, workspace, lse=None):
         """Attention of the newest tokens q [n_seq, n_tok, n_q_heads, d] over their sequences; o likewise, lse
-        [n_seq, n_tok, n_q_heads] float32 or None."""
+        [n_seq, n_tok, n_q_heads] float32 or None; workspace of attend_workspace_bytes bytes, for one call at a time."""
         import torch
-        _want(q.dim() == 4, f"q has {q.dim()} dimensions, not 4")
-        code, (n, n_tok, hq, _) = _dtype_codes().get(q.dtype), q.shape
-        _want(code is not None, f"q is {q.dtype}: float32, float16 or bfloat16")
+        if q.dim() != 4:
+            _refuse(f"q has {q.dim()} dimensions, not 4")
+        code, dev, dt, (n, n_tok, hq, _) = _dtype_code(q, "q"), self.device, q.dtype, q.shape
         rows, table, most, lens = self._table(page_table, lens)
-        _want(rows == n, f"page_table has {rows} rows for {n} sequences")
-        qp, qs = _rows(q, self.device, q.dtype, (n, n_tok), hq, self.d, "q")
-        op, os_ = _rows(o, self.device, q.dtype, (n, n_tok), hq, self.d, "o")
+        if rows != n:
+            _refuse(f"page_table has {rows} rows for {n} sequences")
+        qp, qs = _rows(q, dev, dt, (n, n_tok), hq, self.d, "q")
+        op, os_ = _rows(o, dev, dt, (n, n_tok), hq, self.d, "o")
         if lse is not None:
-            lse = _dense(lse, self.device, torch.float32, n * n_tok * hq, "lse")
-        _on(workspace, self.device, "workspace")
+            lse = _dense(lse, dev, torch.float32, n * n_tok * hq, "lse")
         need = self.attend_workspace_bytes(n, n_tok, hq, most)
-        _want(workspace.is_contiguous() and workspace.numel() * workspace.element_size() >= need,
-              f"workspace: {need} contiguous bytes")
-        return _check(lib().stepq_kv_attend(self._h, self._cache(cache), n, table, most, lens, code, n_tok, hq, qp, qs,
-                                            scale, op, os_, lse, workspace.data_ptr(), self._stream()))
+        if (workspace.get_device() != dev or not workspace.is_contiguous()
+                or workspace.numel() * workspace.element_size() < need):
+            _refuse(f"workspace: {need} contiguous bytes on cuda:{dev}")
+        return _check(_lib.stepq_kv_attend(self._h, self._cache(cache), n, table, most, lens, code, n_tok, hq, qp, qs, scale,
+                                           op, os_, lse, workspace.data_ptr(), self._stream()))
 
     def attend_workspace_bytes(self, n_seq: int, n_tok: int, n_q_heads: int, max_pages: int) -> int:
-        return int(lib().stepq_kv_attend_workspace_bytes(self._h, n_seq, n_tok, n_q_heads, max_pages))
+        return int(_lib.stepq_kv_attend_workspace_bytes(self._h, n_seq, n_tok, n_q_heads, max_pages))
 
     def check(self):
         """Wait for the caller's current stream; raises if a call found a place, page or length out of range."""
-        return _check(lib().stepq_kv_check(self._h, self._stream()))
+        return _check(_lib.stepq_kv_check(self._h, self._stream()))
 
     def close(self):
         if getattr(self, "_h", None):
