@@ -56,6 +56,7 @@ struct KvAttendArgs {
     float *lse;
     float *part;            // split results: [unit][split][row][d + 2] (d sums, reference, total)
     int n_splits, row_tiles;
+    uint64_t div_page;      // div_magic(page_tokens)
 };
 
 // dtype 0 fp32, 1 fp16, 2 bf16

@@ -4,6 +4,7 @@
 #include <new>
 
 #include "../../include/stepq.h"
+#include "stepq_dev.cuh"
 #include "stepq_host.h"
 #include "stepq_kv.cuh"
 
@@ -144,7 +145,8 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
     const stepq::KvSplit k = stepq::kv_split(kv->g, n_seq, n_tok, n_q_heads, max_pages, kv->n_sms);
     const stepq::KvAttendArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, n_seq, max_pages, n_tok,
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
-                                static_cast<float *>(workspace), k.n_splits, k.row_tiles};
+                                static_cast<float *>(workspace), k.n_splits, k.row_tiles,
+                                stepq::div_magic((uint32_t)kv->g.page_tokens)};
     const cudaError_t e = stepq::launch_kv_attend(a, k.nr, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_attend launch");
 }

@@ -12,9 +12,12 @@
 //                  by two 8 x 8 transposes
 // The index summed over may be permuted at will, so a lane's codes need not be
 // neighbours in the fragment's order: a lane takes contiguous bytes, q is stored to
-// match.  Codes become fp16 exactly (1024 + u has the code in its low bits;
-// one subtraction, or for the high nibbles one fma, leaves z).  The row scales stay
-// outside the products: r_k multiplies the score, r_v the weight.
+// match.  A code becomes fp16 by a mask: 1024 + u has the code in its low bits (1024 + 16 u in the next four).  For the
+// keys that is all: the scores are off by a constant of the query row, 1152 sum q for 8 bits and, with q / 16 stored for 4
+// bits, 72 sum q, which is taken off the fp32 score (the constant is 9 to 18 times the codes' own size, so the sum loses
+// four of its 24 bits; fp32 queries subtract it from each code instead).  The values' sums run over the whole
+// length and could not bear it: one subtraction, or for the high nibbles one fma, leaves z.  The row scales stay outside
+// the products: r_k multiplies the score, r_v the weight.
 //
 // The weight p r_v has to fit fp16, whatever r_v is, so the running reference of a row
 // is the largest s + log2 r_v instead of the largest s (lr below).  It moves only
@@ -22,8 +25,10 @@
 // three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry 2^-12 of
 // themselves as rounding error; fp32 outputs take them (and q) as sums of two fp16 values.
 //
-// A warp works on its own tiles of 16 tokens, the block's warps in turn, and keeps
-// its own reference, total and sums; they are joined once at the end, in warp order.  A
+// A warp works on its own tiles of 16 tokens, the block's warps in turn.  The registers of a tile's keys are loaded again
+// for the next tile as soon as the scores are formed, those of the values after the sums, so loads are always in flight and no
+// second set of registers is needed.  A warp keeps its own reference, total and sums; they are joined once at the end, in warp
+// order.  A
 // sequence is cut into n_splits parts when the batch does not fill the SMs; a second
 // kernel joins them in order, so results do not depend on timing.
 #include <float.h>
@@ -31,6 +36,7 @@
 #include <type_traits>
 
 #include "stepq_delta.cuh"
+#include "stepq_dev.cuh"
 #include "stepq_kv.cuh"
 
 namespace stepq {
@@ -39,6 +45,7 @@ namespace {
 
 constexpr int kWarps = 4, kTile = 16;
 constexpr float kSlack = 8.0f;           // log2 of the largest weight
+constexpr float kNone = -1e30f;          // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -49,6 +56,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
@@ -95,7 +107,7 @@ struct Geo {
         if constexpr (BITS == 8) {
             ks = idx / 4; reg = idx / 2 % 2; half = idx % 2;
         } else {
-            ks = idx / 8 * 2 + idx % 4 / 2; reg = idx % 2; half = idx / 4 % 2;
+            ks = idx / 8 * 2 + idx % 4 / 2; reg = idx % 2; half = idx / 4 % 2;   // codes m and m + 4 of a word are a pair
         }
         plane_words = KS * NR * 32 * 2;
         return ((((ks * NR + r / 8) * 32 + (r % 8) * 4 + c) * 2) + reg) * 2 + half;
@@ -108,19 +120,14 @@ struct Geo {
     }
 };
 
-template <int BITS, int D>
-struct Tile {                                            // one lane's codes and scales of 16 tokens
-    uint32_t k[2][D * BITS / 128], v[4][D * BITS / 256];
-    float rk[2], rv[2];
-};
-
 template <int BITS, int D, int NR, int TERMS>
 __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
     using G = Geo<BITS, D, NR>;
     extern __shared__ __align__(16) uint8_t smem[];
     __half *qf = reinterpret_cast<__half *>(smem);                              // [TERMS][KS][NR][32][2] half pairs
     float *qe = reinterpret_cast<float *>(smem + TERMS * G::KS * NR * 256);     // [R] score factor of the row
-    float *join = qe + G::R;                                                    // [kWarps][R][D + 2]
+    float *qc = qe + G::R;                                                      // [R] what the codes' offset adds to the score
+    float *join = qc + G::R;                                                    // [kWarps][R][D + 2]
     const KvGeo &g = a.g;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lc = lane & 3;
     const int group = a.Hq / g.H, rows = a.n_tok * group;
@@ -171,29 +178,39 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         const int e1 = ex / 2, e2 = ex - e1;
         const float f1 = ldexpf(1.0f, -e1), f2 = ldexpf(1.0f, -e2);
         int plane;
+        float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
-            const float y = x[e] * f1 * f2;
+            float y = x[e] * f1 * f2;
+            if (TERMS == 1 && BITS == 4) y *= 0.0625f;
             const int at = G::q_at(e * 32 + lane, r, plane);
             const __half hi = __float2half_rn(y);
             qf[at] = hi;
+            sum += __half2float(hi);
             if constexpr (TERMS == 2) qf[2 * plane + at] = __float2half_rn(y - __half2float(hi));
         }
-        if (lane == 0) qe[r] = ldexpf(a.scale * kLog2e, ex);
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        if (lane == 0) {
+            qe[r] = ldexpf(a.scale * kLog2e, ex);
+            qc[r] = TERMS == 2 ? 0.0f : -1152.0f * sum;   // 1024 + 128; for 4 bits 1024 + 16 * 8 of q / 16
+        }
     }
     __syncthreads();
 
-    float ref[2 * NR], total[2 * NR], lift[2 * NR];
+    float ref[2 * NR], total[2 * NR], lift[2 * NR], offset[2 * NR];
     int limit[2 * NR];                                   // first token that the row does not see
     float acc[G::KS][NR][4];
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
         const int r = 8 * (j / 2) + 2 * lc + j % 2;
-        ref[j] = -INFINITY;
+        ref[j] = kNone;
         total[j] = 0.0f;
         lift[j] = qe[r];
+        offset[j] = qc[r];
         limit[j] = r < nrow ? len - a.n_tok + 1 + (r0 + r) / group : 0;   // a row without a query sees nothing
     }
+    const int clear = len - a.n_tok + 1 + r0 / group;    // tokens below it are seen by every row
 #pragma unroll
     for (int mt = 0; mt < G::KS; ++mt)
 #pragma unroll
@@ -202,29 +219,43 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
     const int32_t *table = a.table + (int64_t)s * a.max_pages;
     auto page_of = [&](int t) -> int {
         if (t >= end) return 0;
-        const int page = __ldg(table + t / g.page_tokens);
+        const int page = __ldg(table + fast_div((uint32_t)t, a.div_page));
         if (page >= 0 && page < g.n_pages) return page;
         if (lane == 0) atomicOr(g.err, kErrKvPlace);
         return 0;
     };
-    // the tile that starts at token t (t + 15 is in the same page: pages and tiles are whole sixteens)
-    auto fetch = [&](Tile<BITS, D> &x, int page, int t) {
-        const int at = t % g.page_tokens;
-        const uint8_t *kb = a.cache + g.codes_at(page, h, 0) + (int64_t)at * G::RB;
-        const uint8_t *vb = kb + (int64_t)g.page_tokens * G::RB;
-        const float *sc = reinterpret_cast<const float *>(a.cache + g.scales_at(page, h, 0)) + at;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) G::K::template load<4>(kb + (lg + 8 * i) * G::RB, lc, x.k[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) G::V::template load<8>(vb + (2 * lc + (i & 1) + 8 * (i >> 1)) * G::RB, lg, x.v[i]);
+    // The tile that starts at token t lies in one page (pages and tiles are whole sixteens).
+    uint32_t kw[2][G::K::W], vw[4][G::V::W];
+    float rk[2], rv[2], rk2[2], rv2[2];
+    const uint8_t *kb = nullptr;                         // the tile's first key row
+    const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
+    const int64_t page_bytes = g.page_bytes(), v_off = (int64_t)g.page_tokens * G::RB;
+    auto fetch_k = [&](int page, int t) {
+        const int at = t - (int)fast_div((uint32_t)t, a.div_page) * g.page_tokens;
+        const uint8_t *base = head + page * page_bytes;
+        kb = base + at * G::RB;
+        const float *sc = reinterpret_cast<const float *>(base + 2 * v_off) + at + lg;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            x.rk[i] = __ldg(sc + lg + 8 * i);
-            x.rv[i] = __ldg(sc + g.page_tokens + lg + 8 * i);
+            G::K::template load<4>(kb + (lg + 8 * i) * G::RB, lc, kw[i]);
+            rk2[i] = __ldg(sc + 8 * i);
+            rv2[i] = __ldg(sc + g.page_tokens + 8 * i);
         }
     };
+    auto fetch_v = [&]() {
+        const uint8_t *vb = kb + v_off + 2 * lc * G::RB;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) G::V::template load<8>(vb + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
+    };
 
-    auto work = [&](const Tile<BITS, D> &x, int t0) {
+    int t0 = begin + warp * kTile;
+    int page = page_of(t0 + kStep);
+    if (t0 < end) {
+        fetch_k(page_of(t0), t0);
+        fetch_v();
+    }
+#pragma unroll 1
+    for (; t0 < end; t0 += kStep) {
         // scores of 16 tokens (rows lg, lg + 8 of the tile) by R query rows
         float sc[NR][4];
 #pragma unroll
@@ -245,8 +276,12 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 uint32_t f[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    f[i] = minus(__byte_perm(x.k[i][w], 0x64646464u, 0x4140), 0x64806480u);
-                    f[2 + i] = minus(__byte_perm(x.k[i][w], 0x64646464u, 0x4342), 0x64806480u);
+                    f[i] = __byte_perm(kw[i][w], 0x64646464u, 0x4140);
+                    f[2 + i] = __byte_perm(kw[i][w], 0x64646464u, 0x4342);
+                    if constexpr (TERMS == 2) {
+                        f[i] = minus(f[i], 0x64806480u);
+                        f[2 + i] = minus(f[2 + i], 0x64806480u);
+                    }
                 }
                 score(w, f);
             } else {
@@ -254,28 +289,47 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint32_t y = x.k[i][w] >> (8 * m);
-                        f[m][i] = minus((y & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        f[m][2 + i] = bits_of(__hfma2(half2_of((y & 0x00f000f0u) | 0x64006400u), half2_of(0x2c002c00u),
-                                                      half2_of(0xd480d480u)));   // (1024 + 16 u) / 16 - 72
+                    for (int m = 0; m < 4; ++m) {        // codes m and m + 4 of the word
+                        const uint32_t y = m == 0 ? kw[i][w] << 4 : kw[i][w] >> (4 * (m - 1));
+                        f[m / 2][2 * (m % 2) + i] = (y & 0x00f000f0u) | 0x64006400u;
+                        if constexpr (TERMS == 2)        // (1024 + 16 u) / 16 - 72
+                            f[m / 2][2 * (m % 2) + i] = bits_of(__hfma2(half2_of(f[m / 2][2 * (m % 2) + i]), half2_of(0x2c002c00u),
+                                                                        half2_of(0xd480d480u)));
                     }
                 score(2 * w, f[0]);
                 score(2 * w + 1, f[1]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            rk[i] = rk2[i];
+            rv[i] = rv2[i];
+        }
+        const bool more = t0 + kStep < end;
+        if (more) {
+            const int now = page;
+            page = page_of(t0 + 2 * kStep);
+            fetch_k(now, t0 + kStep);
+        }
         // weights
-        const float lr[2] = {fmaxf(__log2f(x.rv[0]), -60.0f), fmaxf(__log2f(x.rv[1]), -60.0f)};
+        const float lr[2] = {fmaxf(__log2f(rv[0]), -60.0f), fmaxf(__log2f(rv[1]), -60.0f)};
         bool far = false;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 2 * nr + (e & 1), i = e >> 1;
-                const float y = sc[nr][e] * x.rk[i] * lift[j];
-                sc[nr][e] = t0 + lg + 8 * i < limit[j] ? y : -INFINITY;
-                far = far || sc[nr][e] + lr[i] > ref[j] + kSlack;
-            }
+            for (int e = 0; e < 4; ++e) sc[nr][e] = (sc[nr][e] + offset[2 * nr + (e & 1)]) * (rk[e >> 1] * lift[2 * nr + (e & 1)]);
+        const bool masked = t0 + kTile > clear;
+        if (masked) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t0 + lg + 8 * (e >> 1) >= limit[2 * nr + (e & 1)]) sc[nr][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) far = far || sc[nr][e] + lr[e >> 1] > ref[2 * nr + (e & 1)] + kSlack;
         if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
             for (int j = 0; j < 2 * NR; ++j) {
@@ -283,8 +337,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                const float to = fmaxf(m, ref[j]);
-                const float f = to > ref[j] ? exp2f(ref[j] - to) : 1.0f;
+                const float to = fmaxf(m, ref[j]), f = ex2(ref[j] - to);
                 ref[j] = to;
                 total[j] *= f;
 #pragma unroll
@@ -302,11 +355,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 float wgt[2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const int j = 2 * nr + b;
-                    const float y = sc[nr][2 * i + b];
-                    const float p = exp2f(y - (ref[j] == -INFINITY ? 0.0f : ref[j]));
-                    total[j] += p;
-                    wgt[b] = y == -INFINITY ? 0.0f : p * x.rv[i];    // nothing of a masked row, whatever its scale
+                    const float y = sc[nr][2 * i + b], p = ex2(y - ref[2 * nr + b]);
+                    total[2 * nr + b] += p;
+                    wgt[b] = p * rv[i];
+                    if (masked && y == -INFINITY) wgt[b] = 0.0f;     // nothing of a masked row, whatever its scale
                 }
                 const __half2 hi = __floats2half2_rn(wgt[0], wgt[1]);
                 pb[0][nr][i] = transpose8(bits_of(hi));
@@ -328,8 +380,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 uint32_t f[2][4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t lo = __byte_perm(x.v[2 * i][w], x.v[2 * i + 1][w], 0x5140);
-                    const uint32_t hi = __byte_perm(x.v[2 * i][w], x.v[2 * i + 1][w], 0x7362);
+                    const uint32_t lo = __byte_perm(vw[2 * i][w], vw[2 * i + 1][w], 0x5140);
+                    const uint32_t hi = __byte_perm(vw[2 * i][w], vw[2 * i + 1][w], 0x7362);
                     f[0][2 * i] = minus(__byte_perm(lo, 0x64646464u, 0x4140), 0x64806480u);
                     f[0][2 * i + 1] = minus(__byte_perm(lo, 0x64646464u, 0x4342), 0x64806480u);
                     f[1][2 * i] = minus(__byte_perm(hi, 0x64646464u, 0x4140), 0x64806480u);
@@ -343,7 +395,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                     uint32_t f[2][4];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t y = __byte_perm(x.v[2 * i][w], x.v[2 * i + 1][w], half ? 0x7632 : 0x5410);
+                        const uint32_t y = __byte_perm(vw[2 * i][w], vw[2 * i + 1][w], half ? 0x7632 : 0x5410);
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             const uint32_t z = y >> (8 * m);
@@ -357,23 +409,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 }
             }
         }
-    };
-
-    {
-        Tile<BITS, D> x;
-        int t = begin + warp * kTile;
-        int page = page_of(t), page2 = page_of(t + kStep);
-        if (t < end) fetch(x, page, t);
-#pragma unroll 1
-        for (; t < end; t += kStep) {
-            Tile<BITS, D> y;
-            const int t2 = t + kStep;
-            page = page2;
-            page2 = page_of(t2 + kStep);
-            if (t2 < end) fetch(y, page, t2);
-            work(x, t);
-            x = y;
-        }
+        if (more) fetch_v();
     }
 
     // join the warps, in order
@@ -397,15 +433,13 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
     __syncthreads();
     for (int r = warp; r < nrow; r += kWarps) {
         const float *in = join + r * (D + 2);
-        float m = -INFINITY, l = 0.0f, f[kWarps];
+        float m = kNone, l = 0.0f, f[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, in[w * G::R * (D + 2) + D]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float y = in[w * G::R * (D + 2) + D];
-            f[w] = y == -INFINITY ? 0.0f : exp2f(y - m);
-            // a warp that saw only NaN rows keeps the reference -infinity and a NaN total
-            l += y == -INFINITY ? in[w * G::R * (D + 2) + D + 1] : f[w] * in[w * G::R * (D + 2) + D + 1];
+            f[w] = ex2(in[w * G::R * (D + 2) + D] - m);
+            l += f[w] * in[w * G::R * (D + 2) + D + 1];
         }
         const int i = (r0 + r) / group, hq = h * group + (r0 + r) % group;
         const int64_t tok = (int64_t)s * a.n_tok + i;
@@ -413,10 +447,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         for (int c = lane; c < D; c += 32) {
             float y = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float z = in[w * G::R * (D + 2) + c];
-                y += f[w] == 0.0f ? 0.0f : f[w] * z;
-            }
+            for (int w = 0; w < kWarps; ++w) y += f[w] * in[w * G::R * (D + 2) + c];
             if (part) {
                 part[c] = y;
                 continue;
@@ -432,21 +463,21 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 part[D] = m;
                 part[D + 1] = l;
             } else if (a.lse) {
-                a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m * kLn2 + logf(l));
+                a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
             }
         }
     }
 }
 
-// Joins the parts of a row, in order: a warp per row.
-__global__ void __launch_bounds__(128) k_kv_join(KvAttendArgs a, int R) {
+// Joins the parts of a row: a block of four warps per row, a quarter of the parts each, in order.
+constexpr int kJoin = 128;
+__global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
+    __shared__ float sum[4][256 + 1];
     const KvGeo &g = a.g;
-    const int lane = threadIdx.x & 31, D = g.d;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = g.d;
     const int group = a.Hq / g.H, rows = a.n_tok * group;
-    if (row >= (int64_t)a.n_seq * g.H * rows) return;
-    const int rr = (int)(row % rows);
-    const int64_t sh = row / rows;
+    const int rr = (int)(blockIdx.x % rows);
+    const int64_t sh = blockIdx.x / rows;
     const int h = (int)(sh % g.H), s = (int)(sh / g.H);
     const int len = a.lens[s];
     if (len < 0 || len > (int64_t)a.max_pages * g.page_tokens) return;
@@ -455,35 +486,38 @@ __global__ void __launch_bounds__(128) k_kv_join(KvAttendArgs a, int R) {
     const int parts = len == 0 ? 1 : (int)(((int64_t)len + per - 1) / per);
     const float *in = a.part + ((sh * a.row_tiles + rr / R) * a.n_splits * R + rr % R) * (D + 2);
     const int64_t step = (int64_t)R * (D + 2);
-    float m = -INFINITY;
+    float m = kNone;
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, in[p * step + D]);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
     float l = 0.0f;
     float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < parts; ++p) {
+    const int quarter = (parts + 3) / 4, p1 = min(parts, (warp + 1) * quarter);
+#pragma unroll 4
+    for (int p = warp * quarter; p < p1; ++p) {
         const float *x = in + p * step;
-        const float e = x[D];
-        const float f = e == -INFINITY ? 0.0f : exp2f(e - m);
-        l += e == -INFINITY ? x[D + 1] : f * x[D + 1];
-        if (f != 0.0f)
+        const float f = ex2(x[D] - m);
+        l += f * x[D + 1];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c * 32 < D) y[c] += f * x[c * 32 + lane];
+        for (int c = 0; c < 8; ++c)
+            if (c * 32 < D) y[c] += f * x[c * 32 + lane];
     }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (c * 32 < D) sum[warp][c * 32 + lane] = y[c];
+    if (lane == 0) sum[warp][256] = l;
+    __syncthreads();
+    l = (sum[0][256] + sum[1][256]) + (sum[2][256] + sum[3][256]);
     const int64_t tok = (int64_t)s * a.n_tok + rr / group;
     const int hq = h * group + rr % group;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        if (c * 32 >= D) continue;
-        const float z = l == 0.0f ? 0.0f : y[c] / l;
-        const int64_t at = tok * a.os + (int64_t)hq * D + c * 32 + lane;
+    for (int c = threadIdx.x; c < D; c += kJoin) {
+        const float z = l == 0.0f ? 0.0f : ((sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c])) / l;
+        const int64_t at = tok * a.os + (int64_t)hq * D + c;
         if (a.dtype == 0) static_cast<float *>(a.o)[at] = z;
         else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(z);
         else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(z);
     }
-    if (lane == 0 && a.lse)
-        a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m * kLn2 + logf(l));
+    if (threadIdx.x == 0 && a.lse) a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 template <int BITS, int D, int NR, int TERMS>
@@ -491,7 +525,7 @@ cudaError_t launch_one(const KvAttendArgs &a, cudaStream_t st) {
     using G = Geo<BITS, D, NR>;
     const int64_t blocks = (int64_t)a.n_seq * a.g.H * a.row_tiles * a.n_splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)TERMS * G::KS * NR * 256 + G::R * 4 + (size_t)kWarps * G::R * (D + 2) * 4;
+    const size_t smem = (size_t)TERMS * G::KS * NR * 256 + G::R * 8 + (size_t)kWarps * G::R * (D + 2) * 4;
     auto *kern = k_kv_attend<BITS, D, NR, TERMS>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -501,7 +535,8 @@ cudaError_t launch_one(const KvAttendArgs &a, cudaStream_t st) {
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.n_splits > 1) {
         const int64_t rows = (int64_t)a.n_seq * a.n_tok * a.Hq;
-        k_kv_join<<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, G::R);
+        if (rows > 0x7fffffff) return cudaErrorInvalidValue;
+        k_kv_join<<<(unsigned)rows, kJoin, 0, st>>>(a, G::R);
         e = cudaGetLastError();
     }
     return e;
@@ -522,7 +557,10 @@ KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, in
     k.row_tiles = (int)((rows + 8 * k.nr - 1) / (8 * k.nr));
     // about eight blocks for every SM, but no part shorter than four steps of a block
     const int64_t units = (int64_t)n_seq * g.H * k.row_tiles, steps = (int64_t)max_pages * g.page_tokens / (kWarps * kTile);
-    int64_t n = units > 0 ? (8 * (int64_t)n_sms + units - 1) / units : 1;
+#ifndef KV_BLOCKS
+#define KV_BLOCKS 8
+#endif
+    int64_t n = units > 0 ? (KV_BLOCKS * (int64_t)n_sms + units - 1) / units : 1;
     if (n > (steps + 3) / 4) n = (steps + 3) / 4;
     k.n_splits = n < 1 ? 1 : (int)n;
     return k;
