@@ -354,8 +354,8 @@ int stepq_stream_wait_ctx(stepq_ctx *ctx, void *stream);
  * sequence's length is never used. */
 typedef struct stepq_kv stepq_kv; /* opaque: geometry, device, 4-byte error word */
 
-/* bits 4 or 8; d 64, 128 or 256; page_tokens a multiple of 16, at most 65536.  Bound to the
- * current device. */
+/* bits 4 or 8; d 64, 128 or 256; page_tokens a multiple of 16, at most 65536; a page below 2 GiB.
+ * Bound to the current device. */
 int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, int n_pages, stepq_kv **out);
 void stepq_kv_free(stepq_kv *kv);
 /* Bytes of the cache buffer (the caller's, 128-byte aligned). */

@@ -56,7 +56,8 @@ struct KvAttendArgs {
     float *lse;
     float *part;            // split results: [unit][split][row][d + 2] (d sums, reference, total)
     int n_splits, row_tiles;
-    uint64_t div_page;      // div_magic(page_tokens)
+    uint32_t div_mul;       // t / page_tokens = umulhi(t, div_mul) >> div_shift for t < 2^30
+    int div_shift;
 };
 
 // dtype 0 fp32, 1 fp16, 2 bf16

@@ -4,7 +4,6 @@
 #include <new>
 
 #include "../../include/stepq.h"
-#include "stepq_dev.cuh"
 #include "stepq_host.h"
 #include "stepq_kv.cuh"
 
@@ -17,6 +16,9 @@ using stepq::NvtxRange;
 struct stepq_kv {
     stepq::KvGeo g{};
     int device = 0, n_sms = 0;
+    // ceil(2^(30 + l) / page_tokens), l = ceil(log2 page_tokens) >= 4: exact quotients of numbers below 2^30
+    uint32_t div_mul = 0;
+    int div_shift = 0;
 };
 
 extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, int n_pages, stepq_kv **out) {
@@ -27,6 +29,8 @@ extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, in
     if (page_tokens < 16 || page_tokens > 65536 || page_tokens % 16)
         return fail(STEPQ_EINVAL, "kv_create: page_tokens %d (a multiple of 16, at most 65536)", page_tokens);
     if (n_pages < 1) return fail(STEPQ_EINVAL, "kv_create: n_pages %d", n_pages);
+    const stepq::KvGeo g{bits, n_heads, d, page_tokens, n_pages, nullptr};
+    if (g.page_bytes() > 0x7fffffff) return fail(STEPQ_EINVAL, "kv_create: a page of %lld bytes", (long long)g.page_bytes());
     int dev = 0, major = 0, minor = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -37,7 +41,11 @@ extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, in
     if (major < 10) return fail(STEPQ_ECUDA, "kv_create: device %d is sm_%d%d; this library is built for sm_100a", dev, major, minor);
     stepq_kv *kv = new (std::nothrow) stepq_kv;
     if (!kv) return fail(STEPQ_ENOMEM, "kv_create: out of memory");
-    kv->g = {bits, n_heads, d, page_tokens, n_pages, nullptr};
+    kv->g = g;
+    int l = 4;
+    while ((1 << l) < page_tokens) ++l;
+    kv->div_mul = (uint32_t)(((1ull << (30 + l)) + page_tokens - 1) / page_tokens);
+    kv->div_shift = l - 2;
     kv->device = dev;
     kv->n_sms = sms;
     e = cudaMalloc(&kv->g.err, sizeof(int));
@@ -146,7 +154,7 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
     const stepq::KvAttendArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, n_seq, max_pages, n_tok,
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
                                 static_cast<float *>(workspace), k.n_splits, k.row_tiles,
-                                stepq::div_magic((uint32_t)kv->g.page_tokens)};
+                                kv->div_mul, kv->div_shift};
     const cudaError_t e = stepq::launch_kv_attend(a, k.nr, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_attend launch");
 }

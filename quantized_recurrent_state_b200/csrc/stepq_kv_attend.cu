@@ -63,6 +63,17 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// (x & mask) | magic in one instruction: both constants in registers (two immediates would take two)
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t mask, uint32_t magic) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(magic));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
 __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
 // (1024 + u) pairs -> u - zero
@@ -204,7 +215,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
         const int r = 8 * (j / 2) + 2 * lc + j % 2;
-        ref[j] = kNone;
+        ref[j] = 0.0f;                                   // set by the first tile
         total[j] = 0.0f;
         lift[j] = qe[r];
         offset[j] = qc[r];
@@ -217,41 +228,50 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         for (int nr = 0; nr < NR; ++nr) acc[mt][nr][0] = acc[mt][nr][1] = acc[mt][nr][2] = acc[mt][nr][3] = 0.0f;
 
     const int32_t *table = a.table + (int64_t)s * a.max_pages;
-    auto page_of = [&](int t) -> int {
-        if (t >= end) return 0;
-        const int page = __ldg(table + fast_div((uint32_t)t, a.div_page));
-        if (page >= 0 && page < g.n_pages) return page;
-        if (lane == 0) atomicOr(g.err, kErrKvPlace);
-        return 0;
+    bool bad_page = false;
+    // page and row in it of the tile that starts at token t; it lies in one page (pages and tiles are whole sixteens)
+    struct Place {
+        int page, row;
     };
-    // The tile that starts at token t lies in one page (pages and tiles are whole sixteens).
+    auto place_of = [&](int t) {
+        Place p{0, 0};
+        if (t < end) {
+            const int i = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift);
+            p.page = __ldg(table + i);
+            p.row = t - i * g.page_tokens;
+        }
+        return p;
+    };
     uint32_t kw[2][G::K::W], vw[4][G::V::W];
     float rk[2], rv[2], rk2[2], rv2[2];
-    const uint8_t *kb = nullptr;                         // the tile's first key row
+    const uint8_t *vb = nullptr;
+    const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
     const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
-    const int64_t page_bytes = g.page_bytes(), v_off = (int64_t)g.page_tokens * G::RB;
-    auto fetch_k = [&](int page, int t) {
-        const int at = t - (int)fast_div((uint32_t)t, a.div_page) * g.page_tokens;
-        const uint8_t *base = head + page * page_bytes;
-        kb = base + at * G::RB;
-        const float *sc = reinterpret_cast<const float *>(base + 2 * v_off) + at + lg;
+    const uint32_t k_lane = lg * G::RB, v_lane = v_off + 2 * lc * G::RB;
+    auto fetch_k = [&](const Place &p) {
+        const bool in = (uint32_t)p.page < (uint32_t)g.n_pages;
+        bad_page = bad_page || !in;
+        const uint8_t *base = head + (uint64_t)(in ? (uint32_t)p.page : 0u) * page_bytes;
+        const uint8_t *row = base + (uint32_t)(p.row * G::RB);
+        const float *sc = reinterpret_cast<const float *>(base + 2 * v_off + 4 * (p.row + lg));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            G::K::template load<4>(kb + (lg + 8 * i) * G::RB, lc, kw[i]);
+            G::K::template load<4>(row + k_lane + 8 * i * G::RB, lc, kw[i]);
             rk2[i] = __ldg(sc + 8 * i);
             rv2[i] = __ldg(sc + g.page_tokens + 8 * i);
         }
+        vb = row + v_lane;
     };
     auto fetch_v = [&]() {
-        const uint8_t *vb = kb + v_off + 2 * lc * G::RB;
 #pragma unroll
         for (int i = 0; i < 4; ++i) G::V::template load<8>(vb + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
     };
+    const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
 
     int t0 = begin + warp * kTile;
-    int page = page_of(t0 + kStep);
+    Place next = place_of(t0 + kStep);
     if (t0 < end) {
-        fetch_k(page_of(t0), t0);
+        fetch_k(place_of(t0));
         fetch_v();
     }
 #pragma unroll 1
@@ -291,7 +311,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {        // codes m and m + 4 of the word
                         const uint32_t y = m == 0 ? kw[i][w] << 4 : kw[i][w] >> (4 * (m - 1));
-                        f[m / 2][2 * (m % 2) + i] = (y & 0x00f000f0u) | 0x64006400u;
+                        f[m / 2][2 * (m % 2) + i] = pick(y, hi_mask, magic);
                         if constexpr (TERMS == 2)        // (1024 + 16 u) / 16 - 72
                             f[m / 2][2 * (m % 2) + i] = bits_of(__hfma2(half2_of(f[m / 2][2 * (m % 2) + i]), half2_of(0x2c002c00u),
                                                                         half2_of(0xd480d480u)));
@@ -307,17 +327,23 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         }
         const bool more = t0 + kStep < end;
         if (more) {
-            const int now = page;
-            page = page_of(t0 + 2 * kStep);
-            fetch_k(now, t0 + kStep);
+            const Place now = next;
+            next = place_of(t0 + 2 * kStep);
+            fetch_k(now);
         }
         // weights
-        const float lr[2] = {fmaxf(__log2f(rv[0]), -60.0f), fmaxf(__log2f(rv[1]), -60.0f)};
+        // log2 of the weights against the reference: the score less it; log2 r_v on top of that may not pass the slack
+        const float lr[2] = {fmaxf(lg2(rv[0]), -60.0f), fmaxf(lg2(rv[1]), -60.0f)};
+        const float room[2] = {kSlack - lr[0], kSlack - lr[1]};
         bool far = false;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nr][e] = (sc[nr][e] + offset[2 * nr + (e & 1)]) * (rk[e >> 1] * lift[2 * nr + (e & 1)]);
+            for (int e = 0; e < 4; ++e) {
+                const int j = 2 * nr + (e & 1);
+                const float f = rk[e >> 1] * lift[j];
+                sc[nr][e] = fmaf(sc[nr][e], f, fmaf(offset[j], f, -ref[j]));
+            }
         const bool masked = t0 + kTile > clear;
         if (masked) {
 #pragma unroll
@@ -329,16 +355,21 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) far = far || sc[nr][e] + lr[e >> 1] > ref[2 * nr + (e & 1)] + kSlack;
-        if (__any_sync(0xffffffffu, far)) {
+            for (int e = 0; e < 4; ++e) far = far || sc[nr][e] > room[e >> 1];
+        const bool first = t0 < begin + kStep;
+        if (first || __any_sync(0xffffffffu, far)) {
 #pragma unroll
             for (int j = 0; j < 2 * NR; ++j) {
                 float m = fmaxf(sc[j / 2][j & 1] + lr[0], sc[j / 2][2 + (j & 1)] + lr[1]);
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                const float to = fmaxf(m, ref[j]), f = ex2(ref[j] - to);
-                ref[j] = to;
+                // by how much the reference moves: down only while there are no sums (a row that sees nothing in its first
+                // tile sees nothing at all)
+                const float by = first ? (m == -INFINITY ? 0.0f : m) : fmaxf(m, 0.0f), f = first ? 1.0f : ex2(-by);
+                ref[j] += by;
+                sc[j / 2][j & 1] -= by;
+                sc[j / 2][2 + (j & 1)] -= by;
                 total[j] *= f;
 #pragma unroll
                 for (int mt = 0; mt < G::KS; ++mt) {
@@ -355,7 +386,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 float wgt[2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float y = sc[nr][2 * i + b], p = ex2(y - ref[2 * nr + b]);
+                    const float y = sc[nr][2 * i + b], p = ex2(y);
                     total[2 * nr + b] += p;
                     wgt[b] = p * rv[i];
                     if (masked && y == -INFINITY) wgt[b] = 0.0f;     // nothing of a masked row, whatever its scale
@@ -399,9 +430,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             const uint32_t z = y >> (8 * m);
-                            f[m][2 * i] = minus((z & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                            f[m][2 * i + 1] = bits_of(__hfma2(half2_of((z & 0x00f000f0u) | 0x64006400u),
-                                                              half2_of(0x2c002c00u), half2_of(0xd480d480u)));
+                            f[m][2 * i] = minus(pick(z, lo_mask, magic), 0x64086408u);
+                            f[m][2 * i + 1] = bits_of(__hfma2(half2_of(pick(z, hi_mask, magic)), half2_of(0x2c002c00u),
+                                                              half2_of(0xd480d480u)));
                         }
                     }
                     add(4 * w + 2 * half, f[0]);
@@ -412,6 +443,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         if (more) fetch_v();
     }
 
+    if (bad_page && lane == 0) atomicOr(g.err, kErrKvPlace);
+
     // join the warps, in order
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
@@ -421,7 +454,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         const int r = 8 * (j / 2) + 2 * lc + j % 2;
         float *out = join + (warp * G::R + r) * (D + 2);
         if (lg == 0) {
-            out[D] = ref[j];
+            out[D] = total[j] == 0.0f ? kNone : ref[j];
             out[D + 1] = total[j];
         }
 #pragma unroll
