@@ -54,7 +54,8 @@ struct KvAttendArgs {
     int64_t qs, os;
     float scale;
     float *lse;
-    float *part;            // split results: [unit][split][row][d + 2] (d sums, reference, total)
+    float *part;            // split results: sums [unit][split][row][d]
+    float2 *meta;           // and [unit][row][split] (reference, total)
     int n_splits, row_tiles;
     uint32_t div_mul;       // t / page_tokens = umulhi(t, div_mul) >> div_shift for t < 2^30
     int div_shift;

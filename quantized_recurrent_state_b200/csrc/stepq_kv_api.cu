@@ -127,7 +127,7 @@ extern "C" size_t stepq_kv_attend_workspace_bytes(const stepq_kv *kv, int n_seq,
     if (!kv || n_seq < 0 || n_tok < 1 || n_q_heads < 1 || n_q_heads % kv->g.H || max_pages < 1) return 0;
     const stepq::KvSplit k = stepq::kv_split(kv->g, n_seq, n_tok, n_q_heads, max_pages, kv->n_sms);
     if (k.n_splits == 1) return 16;
-    return (size_t)n_seq * kv->g.H * k.row_tiles * k.n_splits * 8 * k.nr * (kv->g.d + 2) * sizeof(float);
+    return (size_t)n_seq * kv->g.H * k.row_tiles * k.n_splits * 8 * k.nr * (kv->g.d + 2) * sizeof(float);   // sums, (reference, total)
 }
 
 extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const int32_t *page_table, int max_pages,
@@ -151,9 +151,11 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
     const stepq::DeviceScope dev(kv->device);
     if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
     const stepq::KvSplit k = stepq::kv_split(kv->g, n_seq, n_tok, n_q_heads, max_pages, kv->n_sms);
+    float *const part = static_cast<float *>(workspace);
+    const size_t rows = (size_t)n_seq * kv->g.H * k.row_tiles * k.n_splits * 8 * k.nr;
     const stepq::KvAttendArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, n_seq, max_pages, n_tok,
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
-                                static_cast<float *>(workspace), k.n_splits, k.row_tiles,
+                                part, reinterpret_cast<float2 *>(part + rows * kv->g.d), k.n_splits, k.row_tiles,
                                 kv->div_mul, kv->div_shift};
     const cudaError_t e = stepq::launch_kv_attend(a, k.nr, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_attend launch");

@@ -43,7 +43,7 @@ namespace stepq {
 
 namespace {
 
-constexpr int kWarps = 4, kTile = 16;
+constexpr int kWarps = 4, kTile = 16, kMaxSplits = 1024;
 constexpr float kSlack = 8.0f;           // log2 of the largest weight
 constexpr float kNone = -1e30f;          // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -163,6 +163,54 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
     const int begin = (int)min((int64_t)len, (int64_t)split * per), end = (int)min((int64_t)len, (int64_t)begin + per);
     if (a.n_splits > 1 && split > 0 && begin >= len) return;                    // the joining kernel knows it is empty
 
+    const int32_t *table = a.table + (int64_t)s * a.max_pages;
+    bool bad_page = false;
+    // page and row in it of the tile that starts at token t; it lies in one page (pages and tiles are whole sixteens)
+    struct Place {
+        int page, row;
+    };
+    auto place_of = [&](int t) {
+        Place p{0, 0};
+        if (t < end) {
+            const int i = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift);
+            p.page = __ldg(table + i);
+            p.row = t - i * g.page_tokens;
+        }
+        return p;
+    };
+    uint32_t kw[2][G::K::W], vw[4][G::V::W];
+    float rk[2], rv[2], rk2[2], rv2[2];
+    const uint8_t *vb = nullptr;
+    const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
+    const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
+    const uint32_t k_lane = lg * G::RB, v_lane = v_off + 2 * lc * G::RB;
+    auto fetch_k = [&](const Place &p) {
+        const bool in = (uint32_t)p.page < (uint32_t)g.n_pages;
+        bad_page = bad_page || !in;
+        const uint8_t *base = head + (uint64_t)(in ? (uint32_t)p.page : 0u) * page_bytes;
+        const uint8_t *row = base + (uint32_t)(p.row * G::RB);
+        const float *sc = reinterpret_cast<const float *>(base + 2 * v_off + 4 * (p.row + lg));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            G::K::template load<4>(row + k_lane + 8 * i * G::RB, lc, kw[i]);
+            rk2[i] = __ldg(sc + 8 * i);
+            rv2[i] = __ldg(sc + g.page_tokens + 8 * i);
+        }
+        vb = row + v_lane;
+    };
+    auto fetch_v = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) G::V::template load<8>(vb + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
+    };
+    const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
+
+    int t0 = begin + warp * kTile;
+    Place next = place_of(t0 + kStep);
+    if (t0 < end) {
+        fetch_k(place_of(t0));
+        fetch_v();
+    }
+
     // q rows as fp16 fragments, scaled by a power of two to below 1
     for (int r = warp; r < G::R; r += kWarps) {
         float x[D / 32], m = 0.0f;
@@ -227,53 +275,6 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) acc[mt][nr][0] = acc[mt][nr][1] = acc[mt][nr][2] = acc[mt][nr][3] = 0.0f;
 
-    const int32_t *table = a.table + (int64_t)s * a.max_pages;
-    bool bad_page = false;
-    // page and row in it of the tile that starts at token t; it lies in one page (pages and tiles are whole sixteens)
-    struct Place {
-        int page, row;
-    };
-    auto place_of = [&](int t) {
-        Place p{0, 0};
-        if (t < end) {
-            const int i = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift);
-            p.page = __ldg(table + i);
-            p.row = t - i * g.page_tokens;
-        }
-        return p;
-    };
-    uint32_t kw[2][G::K::W], vw[4][G::V::W];
-    float rk[2], rv[2], rk2[2], rv2[2];
-    const uint8_t *vb = nullptr;
-    const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
-    const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
-    const uint32_t k_lane = lg * G::RB, v_lane = v_off + 2 * lc * G::RB;
-    auto fetch_k = [&](const Place &p) {
-        const bool in = (uint32_t)p.page < (uint32_t)g.n_pages;
-        bad_page = bad_page || !in;
-        const uint8_t *base = head + (uint64_t)(in ? (uint32_t)p.page : 0u) * page_bytes;
-        const uint8_t *row = base + (uint32_t)(p.row * G::RB);
-        const float *sc = reinterpret_cast<const float *>(base + 2 * v_off + 4 * (p.row + lg));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            G::K::template load<4>(row + k_lane + 8 * i * G::RB, lc, kw[i]);
-            rk2[i] = __ldg(sc + 8 * i);
-            rv2[i] = __ldg(sc + g.page_tokens + 8 * i);
-        }
-        vb = row + v_lane;
-    };
-    auto fetch_v = [&]() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) G::V::template load<8>(vb + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
-    };
-    const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
-
-    int t0 = begin + warp * kTile;
-    Place next = place_of(t0 + kStep);
-    if (t0 < end) {
-        fetch_k(place_of(t0));
-        fetch_v();
-    }
 #pragma unroll 1
     for (; t0 < end; t0 += kStep) {
         // scores of 16 tokens (rows lg, lg + 8 of the tile) by R query rows
@@ -445,7 +446,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 
     if (bad_page && lane == 0) atomicOr(g.err, kErrKvPlace);
 
-    // join the warps, in order
+    // join the warps, in order; the kernel that joins the parts may get ready meanwhile
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
         total[j] += __shfl_xor_sync(0xffffffffu, total[j], 4);
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         }
         const int i = (r0 + r) / group, hq = h * group + (r0 + r) % group;
         const int64_t tok = (int64_t)s * a.n_tok + i;
-        float *part = a.n_splits > 1 ? a.part + ((unit * a.n_splits + split) * G::R + r) * (D + 2) : nullptr;
+        float *part = a.n_splits > 1 ? a.part + ((unit * a.n_splits + split) * G::R + r) * D : nullptr;
         for (int c = lane; c < D; c += 32) {
             float y = 0.0f;
 #pragma unroll
@@ -493,8 +495,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         }
         if (lane == 0) {
             if (part) {
-                part[D] = m;
-                part[D + 1] = l;
+                a.meta[(unit * G::R + r) * a.n_splits + split] = make_float2(m, l);
             } else if (a.lse) {
                 a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
             }
@@ -502,12 +503,16 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
     }
 }
 
-// Joins the parts of a row: a block of four warps per row, a quarter of the parts each, in order.
-constexpr int kJoin = 128;
+// Joins the parts of a row: a block a row.  Factors of all parts first, then groups of D / 4 threads take every
+// (4 kJoin / D)-th part, and the groups' sums are added in order.
+constexpr int kJoin = 256;
+template <int D>
 __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
-    __shared__ float sum[4][256 + 1];
+    constexpr int L = D / 4, GROUPS = kJoin / L;
+    __shared__ float f[kMaxSplits], red[2][kJoin / 32];
+    __shared__ __align__(16) float sum[GROUPS][D];
     const KvGeo &g = a.g;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = g.d;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = a.Hq / g.H, rows = a.n_tok * group;
     const int rr = (int)(blockIdx.x % rows);
     const int64_t sh = blockIdx.x / rows;
@@ -517,40 +522,57 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     constexpr int kStep = kWarps * kTile;
     const int per = (int)(((int64_t)len + (int64_t)a.n_splits * kStep - 1) / ((int64_t)a.n_splits * kStep)) * kStep;
     const int parts = len == 0 ? 1 : (int)(((int64_t)len + per - 1) / per);
-    const float *in = a.part + ((sh * a.row_tiles + rr / R) * a.n_splits * R + rr % R) * (D + 2);
-    const int64_t step = (int64_t)R * (D + 2);
+    const int64_t unit = sh * a.row_tiles + rr / R;
+    const float2 *meta = a.meta + (unit * R + rr % R) * a.n_splits;
+    const float *in = a.part + (unit * a.n_splits * R + rr % R) * D;
+    const int64_t step = (int64_t)R * D;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float m = kNone;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, in[p * step + D]);
+    for (int p = tid; p < parts; p += kJoin) m = fmaxf(m, meta[p].x);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    float l = 0.0f;
-    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const int quarter = (parts + 3) / 4, p1 = min(parts, (warp + 1) * quarter);
-#pragma unroll 4
-    for (int p = warp * quarter; p < p1; ++p) {
-        const float *x = in + p * step;
-        const float f = ex2(x[D] - m);
-        l += f * x[D + 1];
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (c * 32 < D) y[c] += f * x[c * 32 + lane];
+    for (int w = 0; w < kJoin / 32; ++w) m = fmaxf(m, red[0][w]);
+    float l = 0.0f;
+    for (int p = tid; p < parts; p += kJoin) {
+        const float2 x = meta[p];
+        f[p] = ex2(x.x - m);
+        l += f[p] * x.y;
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (c * 32 < D) sum[warp][c * 32 + lane] = y[c];
-    if (lane == 0) sum[warp][256] = l;
+    for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    if (lane == 0) red[1][warp] = l;
     __syncthreads();
-    l = (sum[0][256] + sum[1][256]) + (sum[2][256] + sum[3][256]);
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoin / 32; ++w) l += red[1][w];
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = tid / L; p < parts; p += GROUPS) {
+        const float4 x = *reinterpret_cast<const float4 *>(in + p * step + tid % L * 4);
+        const float w = f[p];
+        y.x += w * x.x;
+        y.y += w * x.y;
+        y.z += w * x.z;
+        y.w += w * x.w;
+    }
+    *reinterpret_cast<float4 *>(&sum[tid / L][tid % L * 4]) = y;
+    __syncthreads();
     const int64_t tok = (int64_t)s * a.n_tok + rr / group;
     const int hq = h * group + rr % group;
-    for (int c = threadIdx.x; c < D; c += kJoin) {
-        const float z = l == 0.0f ? 0.0f : ((sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c])) / l;
-        const int64_t at = tok * a.os + (int64_t)hq * D + c;
+    if (tid < D) {
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < GROUPS; ++w) z += sum[w][tid];
+        z = l == 0.0f ? 0.0f : z / l;
+        const int64_t at = tok * a.os + (int64_t)hq * D + tid;
         if (a.dtype == 0) static_cast<float *>(a.o)[at] = z;
         else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(z);
         else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(z);
     }
-    if (threadIdx.x == 0 && a.lse) a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+    if (tid == 0 && a.lse) a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 template <int BITS, int D, int NR, int TERMS>
@@ -569,8 +591,17 @@ cudaError_t launch_one(const KvAttendArgs &a, cudaStream_t st) {
     if (e == cudaSuccess && a.n_splits > 1) {
         const int64_t rows = (int64_t)a.n_seq * a.n_tok * a.Hq;
         if (rows > 0x7fffffff) return cudaErrorInvalidValue;
-        k_kv_join<<<(unsigned)rows, kJoin, 0, st>>>(a, G::R);
-        e = cudaGetLastError();
+        // launched while the parts are still being made: it waits for them itself
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)rows);
+        cfg.blockDim = dim3(kJoin);
+        cfg.stream = st;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, k_kv_join<D>, a, G::R);
     }
     return e;
 }
@@ -595,6 +626,7 @@ KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, in
 #endif
     int64_t n = units > 0 ? (KV_BLOCKS * (int64_t)n_sms + units - 1) / units : 1;
     if (n > (steps + 3) / 4) n = (steps + 3) / 4;
+    if (n > kMaxSplits) n = kMaxSplits;
     k.n_splits = n < 1 ? 1 : (int)n;
     return k;
 }
