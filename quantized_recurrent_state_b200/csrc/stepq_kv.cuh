@@ -9,6 +9,7 @@ namespace stepq {
 
 constexpr int kErrKvPlace = 1;  // device error word: a place, page or output row out of range
 constexpr int kErrKvLen = 2;    // a length above max_pages * page_tokens
+constexpr int kErrKvWait = 4;   // a wait for a copy gave up
 
 struct KvGeo {
     int bits, H, d, page_tokens, n_pages;
@@ -59,6 +60,7 @@ struct KvAttendArgs {
     int n_splits, row_tiles;
     uint32_t div_mul;       // t / page_tokens = umulhi(t, div_mul) >> div_shift for t < 2^30
     int div_shift;
+    int seg;                // tokens of a copy: divides a page and a stage of 64, at least 16
 };
 
 // dtype 0 fp32, 1 fp16, 2 bf16

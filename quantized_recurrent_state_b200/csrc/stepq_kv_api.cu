@@ -156,7 +156,8 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
     const stepq::KvAttendArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, n_seq, max_pages, n_tok,
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
                                 part, reinterpret_cast<float2 *>(part + rows * kv->g.d), k.n_splits, k.row_tiles,
-                                kv->div_mul, kv->div_shift};
+                                kv->div_mul, kv->div_shift,
+                                kv->g.page_tokens % 64 == 0 ? 64 : kv->g.page_tokens % 32 == 0 ? 32 : 16};
     const cudaError_t e = stepq::launch_kv_attend(a, k.nr, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_attend launch");
 }
@@ -172,7 +173,8 @@ extern "C" int stepq_kv_check(stepq_kv *kv, void *stream) {
     if (e != cudaSuccess) return cuda_fail(e, "kv_check");
     if (!word) return STEPQ_OK;
     cudaMemset(kv->g.err, 0, sizeof(int));
-    return fail(STEPQ_EDEVICE, "device error word 0x%x (%s%s)", word,
+    return fail(STEPQ_EDEVICE, "device error word 0x%x (%s%s%s)", word,
                 (word & stepq::kErrKvPlace) ? "place, page or output row out of range " : "",
-                (word & stepq::kErrKvLen) ? "length above the page table's " : "");
+                (word & stepq::kErrKvLen) ? "length above the page table's " : "",
+                (word & stepq::kErrKvWait) ? "copy wait gave up " : "");
 }

@@ -25,10 +25,9 @@
 // three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry 2^-12 of
 // themselves as rounding error; fp32 outputs take them (and q) as sums of two fp16 values.
 //
-// A warp works on its own tiles of 16 tokens, the block's warps in turn.  The registers of a tile's keys are loaded again
-// for the next tile as soon as the scores are formed, those of the values after the sums, so loads are always in flight and no
-// second set of registers is needed.  A warp keeps its own reference, total and sums; they are joined once at the end, in warp
-// order.  A
+// The cache comes in by bulk copies of whole rows of a page into a ring of stages of 64 tokens, issued by a fifth warp, so
+// that 40 to 60 KB a block are in flight whatever the registers hold.  A warp works on its own 16 tokens of every stage
+// and keeps its own reference, total and sums; they are joined once at the end, in warp order.  A
 // sequence is cut into n_splits parts when the batch does not fill the SMs; a second
 // kernel joins them in order, so results do not depend on timing.
 #include <float.h>
@@ -44,6 +43,8 @@ namespace stepq {
 namespace {
 
 constexpr int kWarps = 4, kTile = 16, kMaxSplits = 1024;
+constexpr int kStep = kWarps * kTile;    // tokens of a stage
+constexpr uint32_t kPolls = 1u << 22;
 constexpr float kSlack = 8.0f;           // log2 of the largest weight
 constexpr float kNone = -1e30f;          // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -90,13 +91,13 @@ struct Piece {
         for (int n = 0; n < N; ++n) {
             const uint8_t *p = row + (n * LANES + i) * V;
             if constexpr (V == 16) {
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p));
+                const uint4 y = *reinterpret_cast<const uint4 *>(p);
                 w[4 * n] = y.x; w[4 * n + 1] = y.y; w[4 * n + 2] = y.z; w[4 * n + 3] = y.w;
             } else if constexpr (V == 8) {
-                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(p));
+                const uint2 y = *reinterpret_cast<const uint2 *>(p);
                 w[0] = y.x; w[1] = y.y;
             } else {
-                w[0] = __ldg(reinterpret_cast<const unsigned int *>(p));
+                w[0] = *reinterpret_cast<const uint32_t *>(p);
             }
         }
     }
@@ -110,6 +111,10 @@ struct Geo {
     static constexpr int CW = 32 / BITS;                 // codes in a word
     static constexpr int KS = D / 16;                    // K steps of the scores, and 16-column tiles of the sums
     static constexpr int R = 8 * NR;                     // rows of a block
+    static constexpr int STAGE = kStep * (2 * RB + 8);   // bytes of a stage: K codes, V codes, K scales, V scales
+    static constexpr int STAGES = STAGE > 20480 ? 3 : STAGE > 10240 ? 4 : 6;
+    static constexpr int JOIN = kWarps * R * (D + 2) * 4;
+    static constexpr int RING = ((STAGES * STAGE > JOIN ? STAGES * STAGE : JOIN) + 127) / 128 * 128;
     // place of q element dd in the fragments: step, register, half, lane quarter
     static __device__ __forceinline__ int q_at(int dd, int r, int &plane_words) {
         constexpr int CV = K::V * CW / 4;                // codes of a piece
@@ -131,14 +136,27 @@ struct Geo {
     }
 };
 
+// Tokens of a part, the same for every sequence so that blocks take equally long: the longest length in n_splits
+// parts, in whole steps of a block.  (The lengths are on the device; max_pages may be far above them.)
+__device__ __forceinline__ int part_tokens(const KvAttendArgs &a, int lane) {
+    int most = 1;
+    for (int i = lane; i < a.n_seq; i += 32) most = max(most, a.lens[i]);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, w));
+    most = (int)min((int64_t)most, (int64_t)a.max_pages * a.g.page_tokens);
+    return (most + a.n_splits * kStep - 1) / (a.n_splits * kStep) * kStep;
+}
+
 template <int BITS, int D, int NR, int TERMS>
-__global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
+__global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) {
     using G = Geo<BITS, D, NR>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __half *qf = reinterpret_cast<__half *>(smem);                              // [TERMS][KS][NR][32][2] half pairs
-    float *qe = reinterpret_cast<float *>(smem + TERMS * G::KS * NR * 256);     // [R] score factor of the row
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *const ring = smem;                                                 // [STAGES] stages
+    float *join = reinterpret_cast<float *>(smem);                              // [kWarps][R][D + 2], after the last stage
+    __half *qf = reinterpret_cast<__half *>(smem + G::RING);                    // [TERMS][KS][NR][32][2] half pairs
+    float *qe = reinterpret_cast<float *>(smem + G::RING + TERMS * G::KS * NR * 256);   // [R] score factor of the row
     float *qc = qe + G::R;                                                      // [R] what the codes' offset adds to the score
-    float *join = qc + G::R;                                                    // [kWarps][R][D + 2]
+    __shared__ uint64_t full[G::STAGES], empty[G::STAGES];
     const KvGeo &g = a.g;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lc = lane & 3;
     const int group = a.Hq / g.H, rows = a.n_tok * group;
@@ -157,58 +175,65 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         if (threadIdx.x == 0) atomicOr(g.err, kErrKvLen);
         return;
     }
-    // this block's tokens: a part of the length in whole steps of the block
-    constexpr int kStep = kWarps * kTile;
-    const int per = (int)(((int64_t)len + (int64_t)a.n_splits * kStep - 1) / ((int64_t)a.n_splits * kStep)) * kStep;
+    // this block's tokens: a part of the length
+    const int per = part_tokens(a, lane);
     const int begin = (int)min((int64_t)len, (int64_t)split * per), end = (int)min((int64_t)len, (int64_t)begin + per);
     if (a.n_splits > 1 && split > 0 && begin >= len) return;                    // the joining kernel knows it is empty
 
-    const int32_t *table = a.table + (int64_t)s * a.max_pages;
-    bool bad_page = false;
-    // page and row in it of the tile that starts at token t; it lies in one page (pages and tiles are whole sixteens)
-    struct Place {
-        int page, row;
-    };
-    auto place_of = [&](int t) {
-        Place p{0, 0};
-        if (t < end) {
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < G::STAGES; ++b) {
+            mbar_init(&full[b], 1);
+            mbar_init(&empty[b], kWarps);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (warp == kWarps) {
+        // ---- copies ---- a lane takes a.seg tokens of a stage, which lie in one page: seg divides pages and stages
+        const int32_t *table = a.table + (int64_t)s * a.max_pages;
+        const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
+        const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
+        const uint32_t codes = (uint32_t)(a.seg * G::RB), scales = (uint32_t)(a.seg * 4);
+        const int at = lane * a.seg;
+        bool bad_page = false;
+        auto lookup = [&](int t, int &row) {
             const int i = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift);
-            p.page = __ldg(table + i);
-            p.row = t - i * g.page_tokens;
+            row = t - i * g.page_tokens;
+            return __ldg(table + i);
+        };
+        int row = 0, page = at < kStep && begin + at < end ? lookup(begin + at, row) : 0;
+        int b = 0;
+        uint32_t round = 0;
+        for (int t0 = begin; t0 < end; t0 += kStep) {
+            const bool mine = at < kStep && t0 + at < end;
+            const int now = page, now_row = row;
+            if (at < kStep && t0 + kStep + at < end) page = lookup(t0 + kStep + at, row);   // ahead of its use
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[b], (round & 1) ^ 1, kPolls))) {
+                if (lane == 0) atomicOr(g.err, kErrKvWait);
+                break;
+            }
+            const uint32_t lanes = __popc(__ballot_sync(0xffffffffu, mine));
+            if (lane == 0) mbar_arrive_expect(&full[b], lanes * 2 * (codes + scales));
+            __syncwarp();
+            if (mine) {
+                const bool in = (uint32_t)now < (uint32_t)g.n_pages;
+                bad_page = bad_page || !in;
+                const uint8_t *base = head + (uint64_t)(in ? (uint32_t)now : 0u) * page_bytes;
+                const uint8_t *src = base + (uint32_t)(now_row * G::RB), *sc = base + 2 * v_off + 4 * now_row;
+                uint8_t *dst = ring + b * G::STAGE;
+                bulk_g2s(dst + at * G::RB, src, codes, &full[b]);
+                bulk_g2s(dst + (kStep + at) * G::RB, src + v_off, codes, &full[b]);
+                bulk_g2s(dst + 2 * kStep * G::RB + 4 * at, sc, scales, &full[b]);
+                bulk_g2s(dst + 2 * kStep * G::RB + 4 * (kStep + at), sc + 4 * g.page_tokens, scales, &full[b]);
+            }
+            if (++b == G::STAGES) {
+                b = 0;
+                ++round;
+            }
         }
-        return p;
-    };
-    uint32_t kw[2][G::K::W], vw[4][G::V::W];
-    float rk[2], rv[2], rk2[2], rv2[2];
-    const uint8_t *vb = nullptr;
-    const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
-    const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
-    const uint32_t k_lane = lg * G::RB, v_lane = v_off + 2 * lc * G::RB;
-    auto fetch_k = [&](const Place &p) {
-        const bool in = (uint32_t)p.page < (uint32_t)g.n_pages;
-        bad_page = bad_page || !in;
-        const uint8_t *base = head + (uint64_t)(in ? (uint32_t)p.page : 0u) * page_bytes;
-        const uint8_t *row = base + (uint32_t)(p.row * G::RB);
-        const float *sc = reinterpret_cast<const float *>(base + 2 * v_off + 4 * (p.row + lg));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            G::K::template load<4>(row + k_lane + 8 * i * G::RB, lc, kw[i]);
-            rk2[i] = __ldg(sc + 8 * i);
-            rv2[i] = __ldg(sc + g.page_tokens + 8 * i);
-        }
-        vb = row + v_lane;
-    };
-    auto fetch_v = [&]() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) G::V::template load<8>(vb + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
-    };
-    const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
-
-    int t0 = begin + warp * kTile;
-    Place next = place_of(t0 + kStep);
-    if (t0 < end) {
-        fetch_k(place_of(t0));
-        fetch_v();
+        if (bad_page) atomicOr(g.err, kErrKvPlace);
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        return;
     }
 
     // q rows as fp16 fragments, scaled by a power of two to below 1
@@ -255,7 +280,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
             qc[r] = TERMS == 2 ? 0.0f : -1152.0f * sum;   // 1024 + 128; for 4 bits 1024 + 16 * 8 of q / 16
         }
     }
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 
     float ref[2 * NR], total[2 * NR], lift[2 * NR], offset[2 * NR];
     int limit[2 * NR];                                   // first token that the row does not see
@@ -275,8 +300,33 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) acc[mt][nr][0] = acc[mt][nr][1] = acc[mt][nr][2] = acc[mt][nr][3] = 0.0f;
 
+    const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
+    bool ok = true, first = true;
+    int b = 0;
+    uint32_t round = 0;
 #pragma unroll 1
-    for (; t0 < end; t0 += kStep) {
+    for (int t0 = begin + warp * kTile; t0 - warp * kTile < end; t0 += kStep) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[b], round & 1, kPolls));
+        if (!ok) break;
+        const uint8_t *const stage = ring + b * G::STAGE;
+        uint64_t *const done = &empty[b];
+        if (++b == G::STAGES) {
+            b = 0;
+            ++round;
+        }
+        if (t0 >= end) continue;                         // the last stage, and the last this warp waits for
+        uint32_t kw[2][G::K::W], vw[4][G::V::W];
+        float rk[2], rv[2];
+        {
+            const uint8_t *kr = stage + (warp * kTile + lg) * G::RB;
+            const float *sc = reinterpret_cast<const float *>(stage + 2 * kStep * G::RB) + warp * kTile + lg;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                G::K::template load<4>(kr + 8 * i * G::RB, lc, kw[i]);
+                rk[i] = sc[8 * i];
+                rv[i] = sc[kStep + 8 * i];
+            }
+        }
         // scores of 16 tokens (rows lg, lg + 8 of the tile) by R query rows
         float sc[NR][4];
 #pragma unroll
@@ -321,18 +371,13 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 score(2 * w + 1, f[1]);
             }
         }
+        {
+            const uint8_t *vr = stage + (kStep + warp * kTile + 2 * lc) * G::RB;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            rk[i] = rk2[i];
-            rv[i] = rv2[i];
+            for (int i = 0; i < 4; ++i) G::V::template load<8>(vr + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
         }
-        const bool more = t0 + kStep < end;
-        if (more) {
-            const Place now = next;
-            next = place_of(t0 + 2 * kStep);
-            fetch_k(now);
-        }
-        // weights
+        __syncwarp();
+        if (lane == 0) mbar_arrive(done);
         // log2 of the weights against the reference: the score less it; log2 r_v on top of that may not pass the slack
         const float lr[2] = {fmaxf(lg2(rv[0]), -60.0f), fmaxf(lg2(rv[1]), -60.0f)};
         const float room[2] = {kSlack - lr[0], kSlack - lr[1]};
@@ -357,7 +402,6 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 4; ++e) far = far || sc[nr][e] > room[e >> 1];
-        const bool first = t0 < begin + kStep;
         if (first || __any_sync(0xffffffffu, far)) {
 #pragma unroll
             for (int j = 0; j < 2 * NR; ++j) {
@@ -441,13 +485,13 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
                 }
             }
         }
-        if (more) fetch_v();
+        first = false;
     }
+    if (!ok && lane == 0) atomicOr(g.err, kErrKvWait);
 
-    if (bad_page && lane == 0) atomicOr(g.err, kErrKvPlace);
-
-    // join the warps, in order; the kernel that joins the parts may get ready meanwhile
+    // join the warps, in order, where the stages were; the kernel that joins the parts may get ready meanwhile
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
         total[j] += __shfl_xor_sync(0xffffffffu, total[j], 4);
@@ -465,7 +509,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_attend(KvAttendArgs a) {
             out[G::col_of(mt, 1, lg)] = acc[mt][j / 2][2 + (j & 1)];
         }
     }
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
     for (int r = warp; r < nrow; r += kWarps) {
         const float *in = join + r * (D + 2);
         float m = kNone, l = 0.0f, f[kWarps];
@@ -519,8 +563,7 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     const int h = (int)(sh % g.H), s = (int)(sh / g.H);
     const int len = a.lens[s];
     if (len < 0 || len > (int64_t)a.max_pages * g.page_tokens) return;
-    constexpr int kStep = kWarps * kTile;
-    const int per = (int)(((int64_t)len + (int64_t)a.n_splits * kStep - 1) / ((int64_t)a.n_splits * kStep)) * kStep;
+    const int per = part_tokens(a, lane);
     const int parts = len == 0 ? 1 : (int)(((int64_t)len + per - 1) / per);
     const int64_t unit = sh * a.row_tiles + rr / R;
     const float2 *meta = a.meta + (unit * R + rr % R) * a.n_splits;
@@ -580,13 +623,13 @@ cudaError_t launch_one(const KvAttendArgs &a, cudaStream_t st) {
     using G = Geo<BITS, D, NR>;
     const int64_t blocks = (int64_t)a.n_seq * a.g.H * a.row_tiles * a.n_splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)TERMS * G::KS * NR * 256 + G::R * 8 + (size_t)kWarps * G::R * (D + 2) * 4;
+    const size_t smem = (size_t)G::RING + TERMS * G::KS * NR * 256 + G::R * 8;
     auto *kern = k_kv_attend<BITS, D, NR, TERMS>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    kern<<<(unsigned)blocks, 32 * kWarps, smem, st>>>(a);
+    kern<<<(unsigned)blocks, 32 * kWarps + 32, smem, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.n_splits > 1) {
         const int64_t rows = (int64_t)a.n_seq * a.n_tok * a.Hq;
