@@ -111,7 +111,7 @@ struct Geo {
     static constexpr int CW = 32 / BITS;                 // codes in a word
     static constexpr int KS = D / 16;                    // K steps of the scores, and 16-column tiles of the sums
     static constexpr int R = 8 * NR;                     // rows of a block
-    static constexpr int STAGE = kStep * (2 * RB + 8);   // bytes of a stage: K codes, V codes, K scales, V scales
+    static constexpr int STAGE = kStep * (2 * RB + 8);   // bytes of a stage: segments as in a page, K codes, V codes, scales
     static constexpr int STAGES = STAGE > 20480 ? 3 : STAGE > 10240 ? 4 : 6;
     static constexpr int JOIN = kWarps * R * (D + 2) * 4;
     static constexpr int RING = ((STAGES * STAGE > JOIN ? STAGES * STAGE : JOIN) + 127) / 128 * 128;
@@ -136,15 +136,24 @@ struct Geo {
     }
 };
 
-// Tokens of a part, the same for every sequence so that blocks take equally long: the longest length in n_splits
-// parts, in whole steps of a block.  (The lengths are on the device; max_pages may be far above them.)
+// Tokens of a part, the same for every sequence so that blocks take equally long: all tokens over a.n_parts parts, but
+// no more than n_splits parts of the longest sequence; whole stages, at least four.  The lengths are on the device
+// (max_pages may be far above them), so this is found here.
 __device__ __forceinline__ int part_tokens(const KvAttendArgs &a, int lane) {
     int most = 1;
-    for (int i = lane; i < a.n_seq; i += 32) most = max(most, a.lens[i]);
+    long long total = 0;
+    for (int i = lane; i < a.n_seq; i += 32) {
+        const int len = (int)min((int64_t)max(a.lens[i], 0), (int64_t)a.max_pages * a.g.page_tokens);
+        most = max(most, len);
+        total += len;
+    }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, w));
-    most = (int)min((int64_t)most, (int64_t)a.max_pages * a.g.page_tokens);
-    return (most + a.n_splits * kStep - 1) / (a.n_splits * kStep) * kStep;
+    for (int w = 16; w > 0; w >>= 1) {
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, w));
+        total += __shfl_xor_sync(0xffffffffu, total, w);
+    }
+    const int per = max(max((int)((total + a.n_parts - 1) / a.n_parts), (most + a.n_splits - 1) / a.n_splits), 4 * kStep);
+    return (per + kStep - 1) / kStep * kStep;
 }
 
 template <int BITS, int D, int NR, int TERMS>
@@ -189,7 +198,8 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
     }
     __syncthreads();
     if (warp == kWarps) {
-        // ---- copies ---- a lane takes a.seg tokens of a stage, which lie in one page: seg divides pages and stages
+        // ---- copies ---- a lane takes a.seg tokens of a stage, which lie in one page: seg divides pages and stages.  One
+        // copy where that is the page (its rows and scales are neighbours), four otherwise.
         const int32_t *table = a.table + (int64_t)s * a.max_pages;
         const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
         const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
@@ -220,11 +230,15 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
                 bad_page = bad_page || !in;
                 const uint8_t *base = head + (uint64_t)(in ? (uint32_t)now : 0u) * page_bytes;
                 const uint8_t *src = base + (uint32_t)(now_row * G::RB), *sc = base + 2 * v_off + 4 * now_row;
-                uint8_t *dst = ring + b * G::STAGE;
-                bulk_g2s(dst + at * G::RB, src, codes, &full[b]);
-                bulk_g2s(dst + (kStep + at) * G::RB, src + v_off, codes, &full[b]);
-                bulk_g2s(dst + 2 * kStep * G::RB + 4 * at, sc, scales, &full[b]);
-                bulk_g2s(dst + 2 * kStep * G::RB + 4 * (kStep + at), sc + 4 * g.page_tokens, scales, &full[b]);
+                uint8_t *dst = ring + b * G::STAGE + lane * 2 * (codes + scales);   // as in a page of seg tokens
+                if (a.seg == g.page_tokens) {
+                    bulk_g2s(dst, base, 2 * (codes + scales), &full[b]);
+                } else {
+                    bulk_g2s(dst, src, codes, &full[b]);
+                    bulk_g2s(dst + codes, src + v_off, codes, &full[b]);
+                    bulk_g2s(dst + 2 * codes, sc, scales, &full[b]);
+                    bulk_g2s(dst + 2 * codes + scales, sc + 4 * g.page_tokens, scales, &full[b]);
+                }
             }
             if (++b == G::STAGES) {
                 b = 0;
@@ -301,6 +315,10 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         for (int nr = 0; nr < NR; ++nr) acc[mt][nr][0] = acc[mt][nr][1] = acc[mt][nr][2] = acc[mt][nr][3] = 0.0f;
 
     const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
+    // where this lane's rows and scales stand in a stage
+    const int seg_at = warp * kTile / a.seg * a.seg * (2 * G::RB + 8), seg_row = warp * kTile % a.seg;
+    const int k_at = seg_at + (seg_row + lg) * G::RB, v_at = seg_at + (a.seg + seg_row + 2 * lc) * G::RB;
+    const int s_at = seg_at + 2 * a.seg * G::RB + 4 * (seg_row + lg);
     bool ok = true, first = true;
     int b = 0;
     uint32_t round = 0;
@@ -318,13 +336,13 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         uint32_t kw[2][G::K::W], vw[4][G::V::W];
         float rk[2], rv[2];
         {
-            const uint8_t *kr = stage + (warp * kTile + lg) * G::RB;
-            const float *sc = reinterpret_cast<const float *>(stage + 2 * kStep * G::RB) + warp * kTile + lg;
+            const uint8_t *kr = stage + k_at;
+            const float *sc = reinterpret_cast<const float *>(stage + s_at);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 G::K::template load<4>(kr + 8 * i * G::RB, lc, kw[i]);
                 rk[i] = sc[8 * i];
-                rv[i] = sc[kStep + 8 * i];
+                rv[i] = sc[a.seg + 8 * i];
             }
         }
         // scores of 16 tokens (rows lg, lg + 8 of the tile) by R query rows
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
             }
         }
         {
-            const uint8_t *vr = stage + (kStep + warp * kTile + 2 * lc) * G::RB;
+            const uint8_t *vr = stage + v_at;
 #pragma unroll
             for (int i = 0; i < 4; ++i) G::V::template load<8>(vr + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
         }
@@ -662,13 +680,22 @@ KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, in
     const int64_t rows = (int64_t)n_tok * (Hq / g.H);
     k.nr = rows <= 8 ? 1 : 2;
     k.row_tiles = (int)((rows + 8 * k.nr - 1) / (8 * k.nr));
-    // about eight blocks for every SM, but no part shorter than four steps of a block
-    const int64_t units = (int64_t)n_seq * g.H * k.row_tiles, steps = (int64_t)max_pages * g.page_tokens / (kWarps * kTile);
-#ifndef KV_BLOCKS
-#define KV_BLOCKS 8
-#endif
-    int64_t n = units > 0 ? (KV_BLOCKS * (int64_t)n_sms + units - 1) / units : 1;
-    if (n > (steps + 3) / 4) n = (steps + 3) / 4;
+    // Blocks that an SM holds: by shared memory (Geo::RING) for one tile of rows, by registers for two.
+    const int by_ring = g.bits * g.d == 8 * 256 ? 2 : g.bits * g.d == 8 * 128 ? 3 : 4;
+    const int by_regs = k.nr == 1 ? 4 : g.d == 256 ? 1 : g.d == 128 ? 2 : 3;
+    const int64_t resident = (int64_t)n_sms * (by_ring < by_regs ? by_ring : by_regs);
+    // Few sequences: all parts at once, a little below what fits (16 requests of 2 heads over up to 20,000 tokens: 46 us, 54
+    // to 62 us with up to twice as many parts).  Many: four times as many, so that uneven ends even out (70 requests of 8 heads
+    // over up to 8,192 tokens: 134 us, 141 us with half as many).
+    const int64_t units = (int64_t)n_seq * g.H * k.row_tiles, per_seq = (int64_t)g.H * k.row_tiles;
+    const int64_t blocks = units * 4 > resident ? 4 * resident : resident;
+    int64_t parts = blocks / per_seq;
+    if (n_seq > 1 && parts > 2 * n_seq) parts -= n_seq;       // each sequence may have one part more
+    k.n_parts = (int)(parts < 1 ? 1 : parts > 0x7fffffff ? 0x7fffffff : parts);
+    // the grid has room for a sequence of twice the average length, or more of them where the parts are few
+    const int64_t stages = (int64_t)max_pages * g.page_tokens / kStep;
+    int64_t n = n_seq == 1 ? k.n_parts : units > 0 ? (2 * blocks + units - 1) / units : 1;
+    if (n > (stages + 3) / 4) n = (stages + 3) / 4;
     if (n > kMaxSplits) n = kMaxSplits;
     k.n_splits = n < 1 ? 1 : (int)n;
     return k;
