@@ -58,6 +58,7 @@ struct KvAttendArgs {
     float *part;            // split results: sums [unit][split][row][d]
     float2 *meta;           // and [unit][row][split] (reference, total)
     int n_splits, n_parts, row_tiles;
+    bool many;
     uint32_t div_mul;       // t / page_tokens = umulhi(t, div_mul) >> div_shift for t < 2^30
     int div_shift;
     int seg;                // tokens of a copy: divides a page and a stage of 64, at least 16
@@ -71,6 +72,7 @@ cudaError_t launch_kv_read(int dtype, const KvReadArgs &a, cudaStream_t st);
 // tile, NR tiles to a block; the length into n_splits parts.
 struct KvSplit {
     int nr, row_tiles, n_splits, n_parts;   // n_parts: aimed at, over all sequences
+    bool many;                              // more parts than are resident at once
 };
 KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, int n_sms);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, int nr, cudaStream_t st);

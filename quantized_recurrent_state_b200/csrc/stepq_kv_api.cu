@@ -155,7 +155,7 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
     const size_t rows = (size_t)n_seq * kv->g.H * k.row_tiles * k.n_splits * 8 * k.nr;
     const stepq::KvAttendArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, n_seq, max_pages, n_tok,
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
-                                part, reinterpret_cast<float2 *>(part + rows * kv->g.d), k.n_splits, k.n_parts, k.row_tiles,
+                                part, reinterpret_cast<float2 *>(part + rows * kv->g.d), k.n_splits, k.n_parts, k.row_tiles, k.many,
                                 kv->div_mul, kv->div_shift,
                                 kv->g.page_tokens % 64 == 0 ? 64 : kv->g.page_tokens % 32 == 0 ? 32 : 16};
     const cudaError_t e = stepq::launch_kv_attend(a, k.nr, static_cast<cudaStream_t>(stream));

@@ -136,9 +136,11 @@ struct Geo {
     }
 };
 
-// Tokens of a part, the same for every sequence so that blocks take equally long: all tokens over a.n_parts parts, but
-// no more than n_splits parts of the longest sequence; whole stages, at least four.  The lengths are on the device
-// (max_pages may be far above them), so this is found here.
+// Tokens of a part, the same for every sequence so that blocks take equally long: all tokens over a.n_parts parts (kWaves
+// times as many where the batch is large and parts stay above kPart bytes: what a block costs beside its tokens is a few
+// microseconds), but no more than n_splits parts of the longest sequence; whole stages, at least four.  The lengths are on
+// the device (max_pages may be far above them), so this is found here.
+constexpr int kWaves = 4, kPart = 256 * 1024;
 __device__ __forceinline__ int part_tokens(const KvAttendArgs &a, int lane) {
     int most = 1;
     long long total = 0;
@@ -152,7 +154,9 @@ __device__ __forceinline__ int part_tokens(const KvAttendArgs &a, int lane) {
         most = max(most, __shfl_xor_sync(0xffffffffu, most, w));
         total += __shfl_xor_sync(0xffffffffu, total, w);
     }
-    const int per = max(max((int)((total + a.n_parts - 1) / a.n_parts), (most + a.n_splits - 1) / a.n_splits), 4 * kStep);
+    int per = (int)((total + a.n_parts - 1) / a.n_parts);
+    if (a.many) per = max((per + kWaves - 1) / kWaves, min(per, kPart / (2 * a.g.row_bytes() + 8)));
+    per = max(max(per, (most + a.n_splits - 1) / a.n_splits), 4 * kStep);
     return (per + kStep - 1) / kStep * kStep;
 }
 
@@ -187,7 +191,8 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
     // this block's tokens: a part of the length
     const int per = part_tokens(a, lane);
     const int begin = (int)min((int64_t)len, (int64_t)split * per), end = (int)min((int64_t)len, (int64_t)begin + per);
-    if (a.n_splits > 1 && split > 0 && begin >= len) return;                    // the joining kernel knows it is empty
+    if (split > 0 && begin >= len) return;                                      // the joining kernel knows it is empty
+    const bool whole = per >= len;                                              // one part: nothing to join
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < G::STAGES; ++b) {
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         }
         const int i = (r0 + r) / group, hq = h * group + (r0 + r) % group;
         const int64_t tok = (int64_t)s * a.n_tok + i;
-        float *part = a.n_splits > 1 ? a.part + ((unit * a.n_splits + split) * G::R + r) * D : nullptr;
+        float *part = !whole ? a.part + ((unit * a.n_splits + split) * G::R + r) * D : nullptr;
         for (int c = lane; c < D; c += 32) {
             float y = 0.0f;
 #pragma unroll
@@ -582,7 +587,8 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     const int len = a.lens[s];
     if (len < 0 || len > (int64_t)a.max_pages * g.page_tokens) return;
     const int per = part_tokens(a, lane);
-    const int parts = len == 0 ? 1 : (int)(((int64_t)len + per - 1) / per);
+    if (per >= len) return;                              // written by the part itself
+    const int parts = (int)(((int64_t)len + per - 1) / per);
     const int64_t unit = sh * a.row_tiles + rr / R;
     const float2 *meta = a.meta + (unit * R + rr % R) * a.n_splits;
     const float *in = a.part + (unit * a.n_splits * R + rr % R) * D;
@@ -688,8 +694,9 @@ KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, in
     // to 62 us with up to twice as many parts).  Many: four times as many, so that uneven ends even out (70 requests of 8 heads
     // over up to 8,192 tokens: 134 us, 141 us with half as many).
     const int64_t units = (int64_t)n_seq * g.H * k.row_tiles, per_seq = (int64_t)g.H * k.row_tiles;
-    const int64_t blocks = units * 4 > resident ? 4 * resident : resident;
-    int64_t parts = blocks / per_seq;
+    k.many = units * 4 > resident;
+    const int64_t blocks = k.many ? kWaves * resident : resident;
+    int64_t parts = resident / per_seq;
     if (n_seq > 1 && parts > 2 * n_seq) parts -= n_seq;       // each sequence may have one part more
     k.n_parts = (int)(parts < 1 ? 1 : parts > 0x7fffffff ? 0x7fffffff : parts);
     // the grid has room for a sequence of twice the average length, or more of them where the parts are few
