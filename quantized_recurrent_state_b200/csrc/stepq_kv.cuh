@@ -55,10 +55,9 @@ struct KvAttendArgs {
     int64_t qs, os;
     float scale;
     float *lse;
-    float *part;            // split results: sums [unit][split][row][d]
-    float2 *meta;           // and [unit][row][split] (reference, total)
-    int n_splits, n_parts, row_tiles;
-    bool many;
+    float *part;            // pieces of units: sums [block][2][row][d]
+    float2 *meta;           // and (reference, total) [block][2][row]
+    int blocks, row_tiles;
     uint32_t div_mul;       // t / page_tokens = umulhi(t, div_mul) >> div_shift for t < 2^30
     int div_shift;
     int seg;                // tokens of a copy: divides a page and a stage of 64, at least 16
@@ -68,13 +67,15 @@ struct KvAttendArgs {
 cudaError_t launch_kv_append(int dtype, const KvAppendArgs &a, cudaStream_t st);
 cudaError_t launch_kv_read(int dtype, const KvReadArgs &a, cudaStream_t st);
 
-// How a call is cut up: rows of query heads and tokens that share a cache head, eight to an MMA column
-// tile, NR tiles to a block; the length into n_splits parts.
+// How a call is cut up: rows of query heads and tokens that share a cache head, eight to an MMA column tile, nr (1 or 2)
+// tiles to a unit of work.
 struct KvSplit {
-    int nr, row_tiles, n_splits, n_parts;   // n_parts: aimed at, over all sequences
-    bool many;                              // more parts than are resident at once
+    int nr, row_tiles;
 };
-KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, int n_sms);
+KvSplit kv_split(const KvGeo &g, int n_tok, int Hq);
+// Blocks that the current device holds at once, [nr - 1][0: 16-bit queries, 1: fp32], and the kernels' shared memory set; once
+// per cache.
+cudaError_t kv_prepare(const KvGeo &g, int n_sms, int (*blocks)[2]);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, int nr, cudaStream_t st);
 
 }  // namespace stepq

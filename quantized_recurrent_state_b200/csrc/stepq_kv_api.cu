@@ -15,10 +15,11 @@ using stepq::NvtxRange;
 
 struct stepq_kv {
     stepq::KvGeo g{};
-    int device = 0, n_sms = 0;
+    int device = 0;
     // ceil(2^(30 + l) / page_tokens), l = ceil(log2 page_tokens) >= 4: exact quotients of numbers below 2^30
     uint32_t div_mul = 0;
     int div_shift = 0;
+    int blocks[2][2] = {};  // of an attend call, by tiles of rows and terms of q
 };
 
 extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, int n_pages, stepq_kv **out) {
@@ -47,7 +48,10 @@ extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, in
     kv->div_mul = (uint32_t)(((1ull << (30 + l)) + page_tokens - 1) / page_tokens);
     kv->div_shift = l - 2;
     kv->device = dev;
-    kv->n_sms = sms;
+    if ((e = stepq::kv_prepare(g, sms, kv->blocks)) != cudaSuccess) {
+        delete kv;
+        return cuda_fail(e, "kv_create: kernel setup");
+    }
     e = cudaMalloc(&kv->g.err, sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(kv->g.err, 0, sizeof(int));
     if (e != cudaSuccess) {
@@ -125,9 +129,10 @@ extern "C" int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const i
 
 extern "C" size_t stepq_kv_attend_workspace_bytes(const stepq_kv *kv, int n_seq, int n_tok, int n_q_heads, int max_pages) {
     if (!kv || n_seq < 0 || n_tok < 1 || n_q_heads < 1 || n_q_heads % kv->g.H || max_pages < 1) return 0;
-    const stepq::KvSplit k = stepq::kv_split(kv->g, n_seq, n_tok, n_q_heads, max_pages, kv->n_sms);
-    if (k.n_splits == 1) return 16;
-    return (size_t)n_seq * kv->g.H * k.row_tiles * k.n_splits * 8 * k.nr * (kv->g.d + 2) * sizeof(float);   // sums, (reference, total)
+    // two pieces a block: sums, (reference, total)
+    const int nr = stepq::kv_split(kv->g, n_tok, n_q_heads).nr;
+    const int blocks = kv->blocks[nr - 1][0] > kv->blocks[nr - 1][1] ? kv->blocks[nr - 1][0] : kv->blocks[nr - 1][1];
+    return (size_t)blocks * 2 * 8 * nr * (kv->g.d + 2) * sizeof(float);
 }
 
 extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const int32_t *page_table, int max_pages,
@@ -150,13 +155,13 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
     if (lse && (rc = check_ptr(lse, 4, "lse"))) return rc;
     const stepq::DeviceScope dev(kv->device);
     if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
-    const stepq::KvSplit k = stepq::kv_split(kv->g, n_seq, n_tok, n_q_heads, max_pages, kv->n_sms);
+    const stepq::KvSplit k = stepq::kv_split(kv->g, n_tok, n_q_heads);
+    const int blocks = kv->blocks[k.nr - 1][dtype == STEPQ_FP32 ? 1 : 0];
     float *const part = static_cast<float *>(workspace);
-    const size_t rows = (size_t)n_seq * kv->g.H * k.row_tiles * k.n_splits * 8 * k.nr;
     const stepq::KvAttendArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, n_seq, max_pages, n_tok,
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
-                                part, reinterpret_cast<float2 *>(part + rows * kv->g.d), k.n_splits, k.n_parts, k.row_tiles, k.many,
-                                kv->div_mul, kv->div_shift,
+                                part, reinterpret_cast<float2 *>(part + (size_t)blocks * 2 * 8 * k.nr * kv->g.d),
+                                blocks, k.row_tiles, kv->div_mul, kv->div_shift,
                                 kv->g.page_tokens % 64 == 0 ? 64 : kv->g.page_tokens % 32 == 0 ? 32 : 16};
     const cudaError_t e = stepq::launch_kv_attend(a, k.nr, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_attend launch");

@@ -25,11 +25,14 @@
 // three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry 2^-12 of
 // themselves as rounding error; fp32 outputs take them (and q) as sums of two fp16 values.
 //
-// The cache comes in by bulk copies of whole rows of a page into a ring of stages of 64 tokens, issued by a fifth warp, so
-// that 40 to 60 KB a block are in flight whatever the registers hold.  A warp works on its own 16 tokens of every stage
-// and keeps its own reference, total and sums; they are joined once at the end, in warp order.  A
-// sequence is cut into n_splits parts when the batch does not fill the SMs; a second
-// kernel joins them in order, so results do not depend on timing.
+// Work is cut evenly: all stages of 64 tokens of all (sequence, cache head, tile of rows) units lie in one line, and block i of
+// as many as the GPU holds at once takes the i-th piece of it, whatever the lengths are (they are on the device, and each
+// block finds its place by a scan of them).  A unit that ends up in several blocks leaves their sums, references and totals in
+// the workspace, two places a block; a second kernel joins them in order, so results do not depend on timing.
+//
+// The cache comes in by bulk copies of whole rows of a page into a ring of stages, issued by a fifth warp that runs ahead
+// across units.  Each of the other four warps works on its own 16 tokens of every stage with its own reference, total and sums,
+// joined in a fixed order at the end of a unit.
 #include <float.h>
 
 #include <type_traits>
@@ -42,7 +45,7 @@ namespace stepq {
 
 namespace {
 
-constexpr int kWarps = 4, kTile = 16, kMaxSplits = 1024;
+constexpr int kWarps = 4, kTile = 16, kMaxBlocks = 1024;
 constexpr int kStep = kWarps * kTile;    // tokens of a stage
 constexpr uint32_t kPolls = 1u << 22;
 constexpr float kSlack = 8.0f;           // log2 of the largest weight
@@ -112,9 +115,10 @@ struct Geo {
     static constexpr int KS = D / 16;                    // K steps of the scores, and 16-column tiles of the sums
     static constexpr int R = 8 * NR;                     // rows of a block
     static constexpr int STAGE = kStep * (2 * RB + 8);   // bytes of a stage: segments as in a page, K codes, V codes, scales
-    static constexpr int STAGES = STAGE > 20480 ? 3 : STAGE > 10240 ? 4 : 6;
-    static constexpr int JOIN = kWarps * R * (D + 2) * 4;
-    static constexpr int RING = ((STAGES * STAGE > JOIN ? STAGES * STAGE : JOIN) + 127) / 128 * 128;
+    static constexpr int STAGES = STAGE > 20480 ? 2 : STAGE > 10240 ? 3 : STAGE > 5120 ? 5 : 6;
+    static constexpr int SUM1 = KS * NR * 4 * 33;        // the sums of a warp in fragment order, 33 floats for 32 lanes
+    static constexpr int SUM = 2 * SUM1 * 4;             // bytes of those of two warps
+    static constexpr int SMEM(int terms) { return STAGES * STAGE + SUM + terms * KS * NR * 256; }
     // place of q element dd in the fragments: step, register, half, lane quarter
     static __device__ __forceinline__ int q_at(int dd, int r, int &plane_words) {
         constexpr int CV = K::V * CW / 4;                // codes of a piece
@@ -128,72 +132,100 @@ struct Geo {
         plane_words = KS * NR * 32 * 2;
         return ((((ks * NR + r / 8) * 32 + (r % 8) * 4 + c) * 2) + reg) * 2 + half;
     }
-    // value column of sum tile mt, half hi (rows g or g + 8 of the tile), lane group g
-    static __device__ __forceinline__ int col_of(int mt, int hi, int g) {
-        constexpr int CV = V::V * CW / 4;
-        const int idx = 2 * mt + hi;
-        return (idx / CV * 8 + g) * CV + idx % CV;
+    // place of (row r, value column c) among the sums in fragment order: the idx-th of a lane's columns is half idx % 2
+    // (rows g or g + 8) of tile idx / 2
+    static __device__ __forceinline__ int sum_at(int r, int c) {
+        constexpr int CV = V::V * CW / 4;                // codes of a piece
+        const int g = c / CV % 8, idx = c / (8 * CV) * CV + c % CV;
+        return ((idx / 2 * NR + r / 8) * 4 + 2 * (idx % 2) + (r & 1)) * 33 + g * 4 + r % 8 / 2;
     }
 };
 
-// Tokens of a part, the same for every sequence so that blocks take equally long: all tokens over a.n_parts parts (kWaves
-// times as many where the batch is large and parts stay above kPart bytes: what a block costs beside its tokens is a few
-// microseconds), but no more than n_splits parts of the longest sequence; whole stages, at least four.  The lengths are on
-// the device (max_pages may be far above them), so this is found here.
-constexpr int kWaves = 4, kPart = 256 * 1024;
-__device__ __forceinline__ int part_tokens(const KvAttendArgs &a, int lane) {
-    int most = 1;
-    long long total = 0;
-    for (int i = lane; i < a.n_seq; i += 32) {
-        const int len = (int)min((int64_t)max(a.lens[i], 0), (int64_t)a.max_pages * a.g.page_tokens);
-        most = max(most, len);
-        total += len;
-    }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, w));
-        total += __shfl_xor_sync(0xffffffffu, total, w);
-    }
-    int per = (int)((total + a.n_parts - 1) / a.n_parts);
-    if (a.many) per = max((per + kWaves - 1) / kWaves, min(per, kPart / (2 * a.g.row_bytes() + 8)));
-    per = max(max(per, (most + a.n_splits - 1) / a.n_splits), 4 * kStep);
-    return (per + kStep - 1) / kStep * kStep;
+// The line of stages.  A sequence of n tokens has ceil(n / 64) of them for each of its units.
+struct Line {
+    long long total;   // stages of all units
+    int per;           // stages of a block
+};
+__device__ __forceinline__ int stages_of(const KvAttendArgs &a, int s) {
+    const int len = a.lens[s];
+    if (len <= 0 || len > (int64_t)a.max_pages * a.g.page_tokens) return 0;
+    return (len + kStep - 1) / kStep;
 }
+__device__ __forceinline__ Line line_of(const KvAttendArgs &a, int lane) {
+    long long n = 0;
+    for (int i = lane; i < a.n_seq; i += 32) n += stages_of(a, i);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
+    n *= a.g.H * a.row_tiles;
+    return {n, (int)((n + a.blocks - 1) / a.blocks)};
+}
+// A place in the line, and the piece of a unit that starts there.
+struct Place {
+    int s = -1, stages = 0;      // sequence, its stages a unit
+    long long base = 0, end = 0; // its stages in the line
+    int unit = 0, first = 0;     // unit of the sequence, stage of the unit
+};
+__device__ __forceinline__ Place place_of(const KvAttendArgs &a, long long w, int lane) {
+    Place p;
+    const int units = a.g.H * a.row_tiles;
+    long long before = 0;
+    for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
+        const long long own = i0 + lane < a.n_seq ? (long long)units * stages_of(a, i0 + lane) : 0;
+        long long upto = own;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > w);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            p.s = i0 + l;
+            p.end = before + __shfl_sync(0xffffffffu, upto, l);
+            p.base = p.end - __shfl_sync(0xffffffffu, own, l);
+            p.stages = (int)((p.end - p.base) / units);
+            p.unit = (int)((w - p.base) / p.stages);
+            p.first = (int)((w - p.base) % p.stages);
+            return p;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return p;
+}
+// The start of the next unit.
+__device__ __forceinline__ void next_unit(const KvAttendArgs &a, Place &p) {
+    p.first = 0;
+    if (p.base + (long long)(++p.unit) * p.stages < p.end) return;
+    p.unit = 0;
+    p.base = p.end;
+    do p.stages = stages_of(a, ++p.s);
+    while (p.stages == 0);
+    p.end = p.base + (long long)a.g.H * a.row_tiles * p.stages;
+}
+__device__ __forceinline__ void put_out(const KvAttendArgs &a, int64_t at, float y) {
+    if (a.dtype == 0) static_cast<float *>(a.o)[at] = y;
+    else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(y);
+    else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
+}
+__device__ __forceinline__ void bar_workers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 template <int BITS, int D, int NR, int TERMS>
 __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) {
     using G = Geo<BITS, D, NR>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *const ring = smem;                                                 // [STAGES] stages
-    float *join = reinterpret_cast<float *>(smem);                              // [kWarps][R][D + 2], after the last stage
-    __half *qf = reinterpret_cast<__half *>(smem + G::RING);                    // [TERMS][KS][NR][32][2] half pairs
-    float *qe = reinterpret_cast<float *>(smem + G::RING + TERMS * G::KS * NR * 256);   // [R] score factor of the row
-    float *qc = qe + G::R;                                                      // [R] what the codes' offset adds to the score
+    float *const sum = reinterpret_cast<float *>(smem + G::STAGES * G::STAGE);  // [2][SUM1]
+    __half *qf = reinterpret_cast<__half *>(smem + G::STAGES * G::STAGE + G::SUM);   // [TERMS][KS][NR][32][2] half pairs
+    __shared__ float qe[G::R];                           // score factor of the row
+    __shared__ float qc[G::R];                           // what the codes' offset adds to the score
+    __shared__ float wref[kWarps][G::R], wtot[kWarps][G::R];
     __shared__ uint64_t full[G::STAGES], empty[G::STAGES];
     const KvGeo &g = a.g;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lc = lane & 3;
     const int group = a.Hq / g.H, rows = a.n_tok * group;
-    int64_t u = blockIdx.x;
-    const int split = (int)(u % a.n_splits);
-    u /= a.n_splits;
-    const int64_t unit = u;
-    const int rt = (int)(u % a.row_tiles);
-    u /= a.row_tiles;
-    const int h = (int)(u % g.H), s = (int)(u / g.H);
-    const int r0 = rt * G::R, nrow = min(G::R, rows - r0);
-
-    const int len = a.lens[s];
-    if (len < 0) return;
-    if (len > (int64_t)a.max_pages * g.page_tokens) {
-        if (threadIdx.x == 0) atomicOr(g.err, kErrKvLen);
-        return;
-    }
-    // this block's tokens: a part of the length
-    const int per = part_tokens(a, lane);
-    const int begin = (int)min((int64_t)len, (int64_t)split * per), end = (int)min((int64_t)len, (int64_t)begin + per);
-    if (split > 0 && begin >= len) return;                                      // the joining kernel knows it is empty
-    const bool whole = per >= len;                                              // one part: nothing to join
-
+    const Line line = line_of(a, lane);
+    const long long w0 = (long long)blockIdx.x * line.per, w1 = min(line.total, w0 + line.per);
+    if (w0 >= w1) return;
     if (threadIdx.x == 0) {
         for (int b = 0; b < G::STAGES; ++b) {
             mbar_init(&full[b], 1);
@@ -202,77 +234,107 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         fence_mbar_init();
     }
     __syncthreads();
+    Place at = place_of(a, w0, lane);
     if (warp == kWarps) {
         // ---- copies ---- a lane takes a.seg tokens of a stage, which lie in one page: seg divides pages and stages.  One
         // copy where that is the page (its rows and scales are neighbours), four otherwise.
-        const int32_t *table = a.table + (int64_t)s * a.max_pages;
-        const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
         const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
         const uint32_t codes = (uint32_t)(a.seg * G::RB), scales = (uint32_t)(a.seg * 4);
-        const int at = lane * a.seg;
+        const int off = lane * a.seg;
         bool bad_page = false;
-        auto lookup = [&](int t, int &row) {
-            const int i = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift);
-            row = t - i * g.page_tokens;
-            return __ldg(table + i);
-        };
-        int row = 0, page = at < kStep && begin + at < end ? lookup(begin + at, row) : 0;
         int b = 0;
         uint32_t round = 0;
-        for (int t0 = begin; t0 < end; t0 += kStep) {
-            const bool mine = at < kStep && t0 + at < end;
-            const int now = page, now_row = row;
-            if (at < kStep && t0 + kStep + at < end) page = lookup(t0 + kStep + at, row);   // ahead of its use
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[b], (round & 1) ^ 1, kPolls))) {
-                if (lane == 0) atomicOr(g.err, kErrKvWait);
-                break;
-            }
-            const uint32_t lanes = __popc(__ballot_sync(0xffffffffu, mine));
-            if (lane == 0) mbar_arrive_expect(&full[b], lanes * 2 * (codes + scales));
-            __syncwarp();
-            if (mine) {
-                const bool in = (uint32_t)now < (uint32_t)g.n_pages;
-                bad_page = bad_page || !in;
-                const uint8_t *base = head + (uint64_t)(in ? (uint32_t)now : 0u) * page_bytes;
-                const uint8_t *src = base + (uint32_t)(now_row * G::RB), *sc = base + 2 * v_off + 4 * now_row;
-                uint8_t *dst = ring + b * G::STAGE + lane * 2 * (codes + scales);   // as in a page of seg tokens
-                if (a.seg == g.page_tokens) {
-                    bulk_g2s(dst, base, 2 * (codes + scales), &full[b]);
-                } else {
-                    bulk_g2s(dst, src, codes, &full[b]);
-                    bulk_g2s(dst + codes, src + v_off, codes, &full[b]);
-                    bulk_g2s(dst + 2 * codes, sc, scales, &full[b]);
-                    bulk_g2s(dst + 2 * codes + scales, sc + 4 * g.page_tokens, scales, &full[b]);
+        for (long long w = w0; w < w1;) {
+            const int n = (int)min(w1 - w, (long long)(at.stages - at.first)), len = a.lens[at.s];
+            const int32_t *table = a.table + (int64_t)at.s * a.max_pages;
+            const uint8_t *const head = a.cache + (int64_t)(at.unit / a.row_tiles) * g.head_bytes();
+            auto lookup = [&](int t, int &row) {
+                const int i = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift);
+                row = t - i * g.page_tokens;
+                return __ldg(table + i);
+            };
+            int t0 = at.first * kStep;
+            const int end = min(len, (at.first + n) * kStep);
+            int row = 0, page = off < kStep && t0 + off < end ? lookup(t0 + off, row) : 0;
+            for (; t0 < end; t0 += kStep) {
+                const bool mine = off < kStep && t0 + off < end;
+                const int now = page, now_row = row;
+                if (off < kStep && t0 + kStep + off < end) page = lookup(t0 + kStep + off, row);   // ahead of its use
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[b], (round & 1) ^ 1, kPolls))) {
+                    if (lane == 0) atomicOr(g.err, kErrKvWait);
+                    return;
+                }
+                const uint32_t lanes = __popc(__ballot_sync(0xffffffffu, mine));
+                if (lane == 0) mbar_arrive_expect(&full[b], lanes * 2 * (codes + scales));
+                __syncwarp();
+                if (mine) {
+                    const bool in = (uint32_t)now < (uint32_t)g.n_pages;
+                    bad_page = bad_page || !in;
+                    const uint8_t *base = head + (uint64_t)(in ? (uint32_t)now : 0u) * page_bytes;
+                    const uint8_t *src = base + (uint32_t)(now_row * G::RB), *sc = base + 2 * v_off + 4 * now_row;
+                    uint8_t *dst = ring + b * G::STAGE + lane * 2 * (codes + scales);   // as in a page of seg tokens
+                    if (a.seg == g.page_tokens) {
+                        bulk_g2s(dst, base, 2 * (codes + scales), &full[b]);
+                    } else {
+                        bulk_g2s(dst, src, codes, &full[b]);
+                        bulk_g2s(dst + codes, src + v_off, codes, &full[b]);
+                        bulk_g2s(dst + 2 * codes, sc, scales, &full[b]);
+                        bulk_g2s(dst + 2 * codes + scales, sc + 4 * g.page_tokens, scales, &full[b]);
+                    }
+                }
+                if (++b == G::STAGES) {
+                    b = 0;
+                    ++round;
                 }
             }
-            if (++b == G::STAGES) {
-                b = 0;
-                ++round;
-            }
+            w += n;
+            if (w < w1) next_unit(a, at);
         }
         if (bad_page) atomicOr(g.err, kErrKvPlace);
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         return;
     }
 
+    // where this lane's rows and scales stand in a stage
+    const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
+    const int seg_at = warp * kTile / a.seg * a.seg * (2 * G::RB + 8), seg_row = warp * kTile % a.seg;
+    const int k_at = seg_at + (seg_row + lg) * G::RB, v_at = seg_at + (a.seg + seg_row + 2 * lc) * G::RB;
+    const int s_at = seg_at + 2 * a.seg * G::RB + 4 * (seg_row + lg);
+    bool ok = true;
+    int b = 0;
+    uint32_t round = 0;
+#pragma unroll 1
+    for (long long w = w0; w < w1;) {
+    const int s = at.s, len = a.lens[s], n = (int)min(w1 - w, (long long)(at.stages - at.first));
+    const int h = at.unit / a.row_tiles, r0 = at.unit % a.row_tiles * G::R, nrow = min(G::R, rows - r0);
+    const int begin = at.first * kStep, end = min(len, (at.first + n) * kStep);
+
     // q rows as fp16 fragments, scaled by a power of two to below 1
-    for (int r = warp; r < G::R; r += kWarps) {
-        float x[D / 32], m = 0.0f;
+    constexpr int QR = G::R / kWarps;
+    float qx[QR][D / 32];
+#pragma unroll
+    for (int y = 0; y < QR; ++y) {
+        const int r = warp + y * kWarps;
         if (r < nrow) {
             const int i = (r0 + r) / group, hq = h * group + (r0 + r) % group;
-            const int64_t at = ((int64_t)s * a.n_tok + i) * a.qs + (int64_t)hq * D;
+            const int64_t from = ((int64_t)s * a.n_tok + i) * a.qs + (int64_t)hq * D + lane;
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) {
-                const int64_t p = at + e * 32 + lane;
-                x[e] = a.dtype == 0   ? static_cast<const float *>(a.q)[p]
-                       : a.dtype == 1 ? to_f32(static_cast<const __half *>(a.q)[p])
-                                      : to_f32(static_cast<const __nv_bfloat16 *>(a.q)[p]);
-                m = fmaxf(m, fabsf(x[e]));
-            }
+            for (int e = 0; e < D / 32; ++e)
+                qx[y][e] = a.dtype == 0   ? static_cast<const float *>(a.q)[from + e * 32]
+                           : a.dtype == 1 ? to_f32(static_cast<const __half *>(a.q)[from + e * 32])
+                                          : to_f32(static_cast<const __nv_bfloat16 *>(a.q)[from + e * 32]);
         } else {
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
+            for (int e = 0; e < D / 32; ++e) qx[y][e] = 0.0f;
         }
+    }
+#pragma unroll
+    for (int y0 = 0; y0 < QR; ++y0) {
+        const int r = warp + y0 * kWarps;
+        const float (&x)[D / 32] = qx[y0];
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) m = fmaxf(m, fabsf(x[e]));
 #pragma unroll
         for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
         int ex = 0;
@@ -299,7 +361,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
             qc[r] = TERMS == 2 ? 0.0f : -1152.0f * sum;   // 1024 + 128; for 4 bits 1024 + 16 * 8 of q / 16
         }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    bar_workers();
 
     float ref[2 * NR], total[2 * NR], lift[2 * NR], offset[2 * NR];
     int limit[2 * NR];                                   // first token that the row does not see
@@ -319,14 +381,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) acc[mt][nr][0] = acc[mt][nr][1] = acc[mt][nr][2] = acc[mt][nr][3] = 0.0f;
 
-    const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
-    // where this lane's rows and scales stand in a stage
-    const int seg_at = warp * kTile / a.seg * a.seg * (2 * G::RB + 8), seg_row = warp * kTile % a.seg;
-    const int k_at = seg_at + (seg_row + lg) * G::RB, v_at = seg_at + (a.seg + seg_row + 2 * lc) * G::RB;
-    const int s_at = seg_at + 2 * a.seg * G::RB + 4 * (seg_row + lg);
-    bool ok = true, first = true;
-    int b = 0;
-    uint32_t round = 0;
+    bool first = true;
 #pragma unroll 1
     for (int t0 = begin + warp * kTile; t0 - warp * kTile < end; t0 += kStep) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[b], round & 1, kPolls));
@@ -337,7 +392,10 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
             b = 0;
             ++round;
         }
-        if (t0 >= end) continue;                         // the last stage, and the last this warp waits for
+        if (t0 >= end) {                                 // the unit's last stage
+            if (lane == 0) mbar_arrive(done);
+            continue;
+        }
         uint32_t kw[2][G::K::W], vw[4][G::V::W];
         float rk[2], rv[2];
         {
@@ -510,73 +568,86 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         }
         first = false;
     }
-    if (!ok && lane == 0) atomicOr(g.err, kErrKvWait);
-
-    // join the warps, in order, where the stages were; the kernel that joins the parts may get ready meanwhile
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    // join the warps: totals and references first, then the sums, (0 + 2) + (1 + 3)
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
         total[j] += __shfl_xor_sync(0xffffffffu, total[j], 4);
         total[j] += __shfl_xor_sync(0xffffffffu, total[j], 8);
         total[j] += __shfl_xor_sync(0xffffffffu, total[j], 16);
-        const int r = 8 * (j / 2) + 2 * lc + j % 2;
-        float *out = join + (warp * G::R + r) * (D + 2);
         if (lg == 0) {
-            out[D] = total[j] == 0.0f ? kNone : ref[j];
-            out[D + 1] = total[j];
+            const int r = 8 * (j / 2) + 2 * lc + j % 2;
+            wref[warp][r] = total[j] == 0.0f ? kNone : ref[j];
+            wtot[warp][r] = total[j];
         }
+    }
+    bar_workers();
+#pragma unroll
+    for (int j = 0; j < 2 * NR; ++j) {
+        const int r = 8 * (j / 2) + 2 * lc + j % 2;
+        float m = wref[0][r];
+#pragma unroll
+        for (int y = 1; y < kWarps; ++y) m = fmaxf(m, wref[y][r]);
+        const float f = ex2(wref[warp][r] - m);
 #pragma unroll
         for (int mt = 0; mt < G::KS; ++mt) {
-            out[G::col_of(mt, 0, lg)] = acc[mt][j / 2][j & 1];
-            out[G::col_of(mt, 1, lg)] = acc[mt][j / 2][2 + (j & 1)];
+            acc[mt][j / 2][j & 1] *= f;
+            acc[mt][j / 2][2 + (j & 1)] *= f;
         }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    auto pass = [&](float *to, const float *from) {      // this warp's sums, plus `from`, to `to`
+#pragma unroll
+        for (int mt = 0; mt < G::KS; ++mt)
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = ((mt * NR + nr) * 4 + e) * 33 + lane;
+                    if (from) acc[mt][nr][e] += from[c];
+                    if (to) to[c] = acc[mt][nr][e];
+                }
+    };
+    if (warp >= 2) pass(sum + (warp - 2) * G::SUM1, nullptr);
+    bar_workers();
+    if (warp < 2) pass(warp == 1 ? sum + G::SUM1 : nullptr, sum + warp * G::SUM1);
+    bar_workers();
+    if (warp == 0) pass(sum, sum + G::SUM1);
+    bar_workers();
+    const bool whole = n == at.stages;
     for (int r = warp; r < nrow; r += kWarps) {
-        const float *in = join + r * (D + 2);
-        float m = kNone, l = 0.0f, f[kWarps];
+        float m = wref[0][r], l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, in[w * G::R * (D + 2) + D]);
+        for (int y = 1; y < kWarps; ++y) m = fmaxf(m, wref[y][r]);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            f[w] = ex2(in[w * G::R * (D + 2) + D] - m);
-            l += f[w] * in[w * G::R * (D + 2) + D + 1];
-        }
-        const int i = (r0 + r) / group, hq = h * group + (r0 + r) % group;
-        const int64_t tok = (int64_t)s * a.n_tok + i;
-        float *part = !whole ? a.part + ((unit * a.n_splits + split) * G::R + r) * D : nullptr;
+        for (int y = 0; y < kWarps; ++y) l += ex2(wref[y][r] - m) * wtot[y][r];
+        const int64_t tok = (int64_t)s * a.n_tok + (r0 + r) / group;
+        const int hq = h * group + (r0 + r) % group;
+        const int64_t place = ((int64_t)blockIdx.x * 2 + (at.first == 0 ? 1 : 0)) * G::R + r;   // if not whole
         for (int c = lane; c < D; c += 32) {
-            float y = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) y += f[w] * in[w * G::R * (D + 2) + c];
-            if (part) {
-                part[c] = y;
-                continue;
-            }
-            y = l == 0.0f ? 0.0f : y / l;
-            const int64_t at = tok * a.os + (int64_t)hq * D + c;
-            if (a.dtype == 0) static_cast<float *>(a.o)[at] = y;
-            else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(y);
-            else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
+            const float y = sum[G::sum_at(r, c)];
+            if (whole) put_out(a, tok * a.os + (int64_t)hq * D + c, l == 0.0f ? 0.0f : y / l);
+            else a.part[place * D + c] = y;
         }
         if (lane == 0) {
-            if (part) {
-                a.meta[(unit * G::R + r) * a.n_splits + split] = make_float2(m, l);
-            } else if (a.lse) {
-                a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
-            }
+            if (!whole) a.meta[place] = make_float2(m, l);
+            else if (a.lse) a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
         }
     }
+    if (!ok) break;
+    w += n;
+    if (w < w1) next_unit(a, at);
+    }
+    if (!ok && lane == 0) atomicOr(g.err, kErrKvWait);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the parts of a row: a block a row.  Factors of all parts first, then groups of D / 4 threads take every
-// (4 kJoin / D)-th part, and the groups' sums are added in order.
+// Joins the pieces of a row that several blocks worked on, in their order: a block a row.  Factors of all pieces first, then
+// groups of D / 4 threads take every (4 kJoin / D)-th piece, and the groups' sums are added in order.  Rows of empty
+// sequences are written here.
 constexpr int kJoin = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     constexpr int L = D / 4, GROUPS = kJoin / L;
-    __shared__ float f[kMaxSplits], red[2][kJoin / 32];
+    __shared__ float f[kMaxBlocks], red[2][kJoin / 32];
     __shared__ __align__(16) float sum[GROUPS][D];
     const KvGeo &g = a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -584,18 +655,29 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     const int rr = (int)(blockIdx.x % rows);
     const int64_t sh = blockIdx.x / rows;
     const int h = (int)(sh % g.H), s = (int)(sh / g.H);
-    const int len = a.lens[s];
-    if (len < 0 || len > (int64_t)a.max_pages * g.page_tokens) return;
-    const int per = part_tokens(a, lane);
-    if (per >= len) return;                              // written by the part itself
-    const int parts = (int)(((int64_t)len + per - 1) / per);
-    const int64_t unit = sh * a.row_tiles + rr / R;
-    const float2 *meta = a.meta + (unit * R + rr % R) * a.n_splits;
-    const float *in = a.part + (unit * a.n_splits * R + rr % R) * D;
-    const int64_t step = (int64_t)R * D;
+    const int len = a.lens[s], stages = stages_of(a, s);
+    const Line line = line_of(a, lane);
+    long long before = 0;
+    for (int i = lane; i < s; i += 32) before += stages_of(a, i);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) before += __shfl_xor_sync(0xffffffffu, before, w);
+    const long long w0 = before * g.H * a.row_tiles + (long long)(h * a.row_tiles + rr / R) * stages;
+    // before any return: what follows this kernel relies on the blocks' work, too
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t tok = (int64_t)s * a.n_tok + rr / group;
+    const int hq = h * group + rr % group;
+    if (stages == 0) {
+        if (len > 0 && tid == 0) atomicOr(g.err, kErrKvLen);   // a length above the page table's
+        if (len == 0 && tid < D) put_out(a, tok * a.os + (int64_t)hq * D + tid, 0.0f);
+        if (len == 0 && tid == 0 && a.lse) a.lse[tok * a.Hq + hq] = -INFINITY;
+        return;
+    }
+    const int b0 = (int)(w0 / line.per), pieces = (int)((w0 + stages - 1) / line.per) - b0 + 1;
+    if (pieces == 1) return;                             // written by its block
+    // the first piece begins a unit, the others do not
+    auto place = [&](int p) { return ((int64_t)(b0 + p) * 2 + (p == 0 ? 1 : 0)) * R + rr % R; };
     float m = kNone;
-    for (int p = tid; p < parts; p += kJoin) m = fmaxf(m, meta[p].x);
+    for (int p = tid; p < pieces; p += kJoin) m = fmaxf(m, a.meta[place(p)].x);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
     if (lane == 0) red[0][warp] = m;
@@ -603,8 +685,8 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
 #pragma unroll
     for (int w = 0; w < kJoin / 32; ++w) m = fmaxf(m, red[0][w]);
     float l = 0.0f;
-    for (int p = tid; p < parts; p += kJoin) {
-        const float2 x = meta[p];
+    for (int p = tid; p < pieces; p += kJoin) {
+        const float2 x = a.meta[place(p)];
         f[p] = ex2(x.x - m);
         l += f[p] * x.y;
     }
@@ -617,8 +699,8 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     for (int w = 0; w < kJoin / 32; ++w) l += red[1][w];
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int p = tid / L; p < parts; p += GROUPS) {
-        const float4 x = *reinterpret_cast<const float4 *>(in + p * step + tid % L * 4);
+    for (int p = tid / L; p < pieces; p += GROUPS) {
+        const float4 x = *reinterpret_cast<const float4 *>(a.part + place(p) * D + tid % L * 4);
         const float w = f[p];
         y.x += w * x.x;
         y.y += w * x.y;
@@ -627,17 +709,11 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     }
     *reinterpret_cast<float4 *>(&sum[tid / L][tid % L * 4]) = y;
     __syncthreads();
-    const int64_t tok = (int64_t)s * a.n_tok + rr / group;
-    const int hq = h * group + rr % group;
     if (tid < D) {
         float z = 0.0f;
 #pragma unroll
         for (int w = 0; w < GROUPS; ++w) z += sum[w][tid];
-        z = l == 0.0f ? 0.0f : z / l;
-        const int64_t at = tok * a.os + (int64_t)hq * D + tid;
-        if (a.dtype == 0) static_cast<float *>(a.o)[at] = z;
-        else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(z);
-        else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(z);
+        put_out(a, tok * a.os + (int64_t)hq * D + tid, l == 0.0f ? 0.0f : z / l);
     }
     if (tid == 0 && a.lse) a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
@@ -645,32 +721,25 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
 template <int BITS, int D, int NR, int TERMS>
 cudaError_t launch_one(const KvAttendArgs &a, cudaStream_t st) {
     using G = Geo<BITS, D, NR>;
-    const int64_t blocks = (int64_t)a.n_seq * a.g.H * a.row_tiles * a.n_splits;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)G::RING + TERMS * G::KS * NR * 256 + G::R * 8;
+    const int64_t rows = (int64_t)a.n_seq * a.n_tok * a.Hq;
+    if (rows > 0x7fffffff) return cudaErrorInvalidValue;
+    constexpr int smem = G::SMEM(TERMS);
+    static_assert(smem <= 226 * 1024, "shared memory of a block");
     auto *kern = k_kv_attend<BITS, D, NR, TERMS>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    kern<<<(unsigned)blocks, 32 * kWarps + 32, smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && a.n_splits > 1) {
-        const int64_t rows = (int64_t)a.n_seq * a.n_tok * a.Hq;
-        if (rows > 0x7fffffff) return cudaErrorInvalidValue;
-        // launched while the parts are still being made: it waits for them itself
-        cudaLaunchAttribute at{};
-        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)rows);
-        cfg.blockDim = dim3(kJoin);
-        cfg.stream = st;
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, k_kv_join<D>, a, G::R);
-    }
-    return e;
+    kern<<<a.blocks, 32 * kWarps + 32, smem, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // launched while the pieces are still being made: it waits for them itself
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)rows);
+    cfg.blockDim = dim3(kJoin);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_kv_join<D>, a, G::R);
 }
 
 template <int BITS, int D>
@@ -681,31 +750,41 @@ cudaError_t launch_d(const KvAttendArgs &a, int nr, cudaStream_t st) {
 
 }  // namespace
 
-KvSplit kv_split(const KvGeo &g, int n_seq, int n_tok, int Hq, int max_pages, int n_sms) {
+KvSplit kv_split(const KvGeo &g, int n_tok, int Hq) {
     KvSplit k;
     const int64_t rows = (int64_t)n_tok * (Hq / g.H);
     k.nr = rows <= 8 ? 1 : 2;
     k.row_tiles = (int)((rows + 8 * k.nr - 1) / (8 * k.nr));
-    // Blocks that an SM holds: by shared memory (Geo::RING) for one tile of rows, by registers for two.
-    const int by_ring = g.bits * g.d == 8 * 256 ? 2 : g.bits * g.d == 8 * 128 ? 3 : 4;
-    const int by_regs = k.nr == 1 ? 4 : g.d == 256 ? 1 : g.d == 128 ? 2 : 3;
-    const int64_t resident = (int64_t)n_sms * (by_ring < by_regs ? by_ring : by_regs);
-    // Few sequences: all parts at once, a little below what fits (16 requests of 2 heads over up to 20,000 tokens: 46 us, 54
-    // to 62 us with up to twice as many parts).  Many: four times as many, so that uneven ends even out (70 requests of 8 heads
-    // over up to 8,192 tokens: 134 us, 141 us with half as many).
-    const int64_t units = (int64_t)n_seq * g.H * k.row_tiles, per_seq = (int64_t)g.H * k.row_tiles;
-    k.many = units * 4 > resident;
-    const int64_t blocks = k.many ? kWaves * resident : resident;
-    int64_t parts = resident / per_seq;
-    if (n_seq > 1 && parts > 2 * n_seq) parts -= n_seq;       // each sequence may have one part more
-    k.n_parts = (int)(parts < 1 ? 1 : parts > 0x7fffffff ? 0x7fffffff : parts);
-    // the grid has room for a sequence of twice the average length, or more of them where the parts are few
-    const int64_t stages = (int64_t)max_pages * g.page_tokens / kStep;
-    int64_t n = n_seq == 1 ? k.n_parts : units > 0 ? (2 * blocks + units - 1) / units : 1;
-    if (n > (stages + 3) / 4) n = (stages + 3) / 4;
-    if (n > kMaxSplits) n = kMaxSplits;
-    k.n_splits = n < 1 ? 1 : (int)n;
     return k;
+}
+
+namespace {
+template <int BITS, int D, int NR, int TERMS>
+cudaError_t blocks_of(int *per_sm) {
+    constexpr int smem = Geo<BITS, D, NR>::SMEM(TERMS);
+    auto *kern = k_kv_attend<BITS, D, NR, TERMS>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e == cudaSuccess ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kern, 32 * kWarps + 32, smem) : e;
+}
+template <int BITS, int D>
+cudaError_t prepare_d(int (*per_sm)[2]) {
+    cudaError_t e = blocks_of<BITS, D, 1, 1>(&per_sm[0][0]);
+    if (e == cudaSuccess) e = blocks_of<BITS, D, 1, 2>(&per_sm[0][1]);
+    if (e == cudaSuccess) e = blocks_of<BITS, D, 2, 1>(&per_sm[1][0]);
+    if (e == cudaSuccess) e = blocks_of<BITS, D, 2, 2>(&per_sm[1][1]);
+    return e;
+}
+}  // namespace
+
+cudaError_t kv_prepare(const KvGeo &g, int n_sms, int (*blocks)[2]) {
+    cudaError_t e;
+    if (g.bits == 8) e = g.d == 64 ? prepare_d<8, 64>(blocks) : g.d == 128 ? prepare_d<8, 128>(blocks) : prepare_d<8, 256>(blocks);
+    else e = g.d == 64 ? prepare_d<4, 64>(blocks) : g.d == 128 ? prepare_d<4, 128>(blocks) : prepare_d<4, 256>(blocks);
+    for (int i = 0; i < 4; ++i) {
+        int &n = blocks[i / 2][i % 2];
+        n = n * n_sms < 1 ? 1 : n * n_sms > kMaxBlocks ? kMaxBlocks : n * n_sms;
+    }
+    return e;
 }
 
 cudaError_t launch_kv_attend(const KvAttendArgs &a, int nr, cudaStream_t st) {
