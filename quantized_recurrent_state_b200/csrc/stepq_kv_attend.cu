@@ -12,11 +12,9 @@
 //                  by two 8 x 8 transposes
 // The index summed over may be permuted at will, so a lane's codes need not be
 // neighbours in the fragment's order: a lane takes contiguous bytes, q is stored to
-// match.  A code becomes fp16 by a mask: 1024 + u has the code in its low bits (1024 + 16 u in the next four).  For the
-// keys that is all: the scores are off by a constant of the query row, 1152 sum q for 8 bits and, with q / 16 stored for 4
-// bits, 72 sum q, which is taken off the fp32 score (the constant is 9 to 18 times the codes' own size, so the sum loses
-// four of its 24 bits; fp32 queries subtract it from each code instead).  The values' sums run over the whole
-// length and could not bear it: one subtraction, or for the high nibbles one fma, leaves z.  The row scales stay outside
+// match.  Codes become fp16 exactly (1024 + u has the code in its low bits, 1024 + 16 u in the next four; one
+// subtraction or fma leaves z.  Leaving the constant in and taking it off the score instead saves 32 of 350 instructions a tile
+// but costs the score eight bits where a few channels stand out and the other codes are small).  The row scales stay outside
 // the products: r_k multiplies the score, r_v the weight.
 //
 // The weight p r_v has to fit fp16, whatever r_v is, so the running reference of a row
@@ -217,12 +215,13 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
     float *const sum = reinterpret_cast<float *>(smem + G::STAGES * G::STAGE);  // [2][SUM1]
     __half *qf = reinterpret_cast<__half *>(smem + G::STAGES * G::STAGE + G::SUM);   // [TERMS][KS][NR][32][2] half pairs
     __shared__ float qe[G::R];                           // score factor of the row
-    __shared__ float qc[G::R];                           // what the codes' offset adds to the score
     __shared__ float wref[kWarps][G::R], wtot[kWarps][G::R];
     __shared__ uint64_t full[G::STAGES], empty[G::STAGES];
     const KvGeo &g = a.g;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lc = lane & 3;
     const int group = a.Hq / g.H, rows = a.n_tok * group;
+    // every block is resident at once, so the joining kernel's may take what is left of the SMs and wait there
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Line line = line_of(a, lane);
     const long long w0 = (long long)blockIdx.x * line.per, w1 = min(line.total, w0 + line.per);
     if (w0 >= w1) return;
@@ -291,12 +290,16 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
             if (w < w1) next_unit(a, at);
         }
         if (bad_page) atomicOr(g.err, kErrKvPlace);
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         return;
     }
 
     // where this lane's rows and scales stand in a stage
+    // 4-bit codes in bits 0-3 / 4-7 of both halves of a word as fp16 pairs: (1024 + u) - 1032, (1024 + 16 u) / 16 - 72
     const uint32_t lo_mask = 0x000f000fu, hi_mask = 0x00f000f0u, magic = 0x64006400u;
+    auto low = [&](uint32_t x) { return minus(pick(x, lo_mask, magic), 0x64086408u); };
+    auto high = [&](uint32_t x) {
+        return bits_of(__hfma2(half2_of(pick(x, hi_mask, magic)), half2_of(0x2c002c00u), half2_of(0xd480d480u)));
+    };
     const int seg_at = warp * kTile / a.seg * a.seg * (2 * G::RB + 8), seg_row = warp * kTile % a.seg;
     const int k_at = seg_at + (seg_row + lg) * G::RB, v_at = seg_at + (a.seg + seg_row + 2 * lc) * G::RB;
     const int s_at = seg_at + 2 * a.seg * G::RB + 4 * (seg_row + lg);
@@ -343,27 +346,19 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         const int e1 = ex / 2, e2 = ex - e1;
         const float f1 = ldexpf(1.0f, -e1), f2 = ldexpf(1.0f, -e2);
         int plane;
-        float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
-            float y = x[e] * f1 * f2;
-            if (TERMS == 1 && BITS == 4) y *= 0.0625f;
+            const float y = x[e] * f1 * f2;
             const int at = G::q_at(e * 32 + lane, r, plane);
             const __half hi = __float2half_rn(y);
             qf[at] = hi;
-            sum += __half2float(hi);
             if constexpr (TERMS == 2) qf[2 * plane + at] = __float2half_rn(y - __half2float(hi));
         }
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        if (lane == 0) {
-            qe[r] = ldexpf(a.scale * kLog2e, ex);
-            qc[r] = TERMS == 2 ? 0.0f : -1152.0f * sum;   // 1024 + 128; for 4 bits 1024 + 16 * 8 of q / 16
-        }
+        if (lane == 0) qe[r] = ldexpf(a.scale * kLog2e, ex);
     }
     bar_workers();
 
-    float ref[2 * NR], total[2 * NR], lift[2 * NR], offset[2 * NR];
+    float ref[2 * NR], total[2 * NR], lift[2 * NR];
     int limit[2 * NR];                                   // first token that the row does not see
     float acc[G::KS][NR][4];
 #pragma unroll
@@ -372,7 +367,6 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         ref[j] = 0.0f;                                   // set by the first tile
         total[j] = 0.0f;
         lift[j] = qe[r];
-        offset[j] = qc[r];
         limit[j] = r < nrow ? len - a.n_tok + 1 + (r0 + r) / group : 0;   // a row without a query sees nothing
     }
     const int clear = len - a.n_tok + 1 + r0 / group;    // tokens below it are seen by every row
@@ -428,12 +422,8 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
                 uint32_t f[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    f[i] = __byte_perm(kw[i][w], 0x64646464u, 0x4140);
-                    f[2 + i] = __byte_perm(kw[i][w], 0x64646464u, 0x4342);
-                    if constexpr (TERMS == 2) {
-                        f[i] = minus(f[i], 0x64806480u);
-                        f[2 + i] = minus(f[2 + i], 0x64806480u);
-                    }
+                    f[i] = minus(__byte_perm(kw[i][w], 0x64646464u, 0x4140), 0x64806480u);
+                    f[2 + i] = minus(__byte_perm(kw[i][w], 0x64646464u, 0x4342), 0x64806480u);
                 }
                 score(w, f);
             } else {
@@ -441,12 +431,10 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {        // codes m and m + 4 of the word
-                        const uint32_t y = m == 0 ? kw[i][w] << 4 : kw[i][w] >> (4 * (m - 1));
-                        f[m / 2][2 * (m % 2) + i] = pick(y, hi_mask, magic);
-                        if constexpr (TERMS == 2)        // (1024 + 16 u) / 16 - 72
-                            f[m / 2][2 * (m % 2) + i] = bits_of(__hfma2(half2_of(f[m / 2][2 * (m % 2) + i]), half2_of(0x2c002c00u),
-                                                                        half2_of(0xd480d480u)));
+                    for (int m = 0; m < 2; ++m) {        // codes 2 m and 2 m + 4, 2 m + 1 and 2 m + 5 of the word
+                        const uint32_t y = kw[i][w] >> (8 * m);
+                        f[m][i] = low(y);
+                        f[m][2 + i] = high(y);
                     }
                 score(2 * w, f[0]);
                 score(2 * w + 1, f[1]);
@@ -468,8 +456,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int j = 2 * nr + (e & 1);
-                const float f = rk[e >> 1] * lift[j];
-                sc[nr][e] = fmaf(sc[nr][e], f, fmaf(offset[j], f, -ref[j]));
+                sc[nr][e] = fmaf(sc[nr][e], rk[e >> 1] * lift[j], -ref[j]);
             }
         const bool masked = t0 + kTile > clear;
         if (masked) {
@@ -556,9 +543,8 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             const uint32_t z = y >> (8 * m);
-                            f[m][2 * i] = minus(pick(z, lo_mask, magic), 0x64086408u);
-                            f[m][2 * i + 1] = bits_of(__hfma2(half2_of(pick(z, hi_mask, magic)), half2_of(0x2c002c00u),
-                                                              half2_of(0xd480d480u)));
+                            f[m][2 * i] = low(z);
+                            f[m][2 * i + 1] = high(z);
                         }
                     }
                     add(4 * w + 2 * half, f[0]);
@@ -637,7 +623,6 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
     if (w < w1) next_unit(a, at);
     }
     if (!ok && lane == 0) atomicOr(g.err, kErrKvWait);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the pieces of a row that several blocks worked on, in their order: a block a row.  Factors of all pieces first, then
