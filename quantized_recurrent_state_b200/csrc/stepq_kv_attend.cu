@@ -445,8 +445,6 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) G::V::template load<8>(vr + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(done);
         // log2 of the weights against the reference: the score less it; log2 r_v on top of that may not pass the slack
         const float lr[2] = {fmaxf(lg2(rv[0]), -60.0f), fmaxf(lg2(rv[1]), -60.0f)};
         const float room[2] = {kSlack - lr[0], kSlack - lr[1]};
@@ -553,6 +551,9 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
             }
         }
         first = false;
+        // only here: a load that has been issued but not used yet may still read the stage after the arrival
+        __syncwarp();
+        if (lane == 0) mbar_arrive(done);
     }
     // join the warps: totals and references first, then the sums, (0 + 2) + (1 + 3)
 #pragma unroll
