@@ -8,6 +8,7 @@
 #include <float.h>
 
 #include "stepq_delta.cuh"
+#include "stepq_dev.cuh"
 #include "stepq_kv.cuh"
 
 namespace stepq {
@@ -23,6 +24,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
     const int h = blockIdx.y >> 1, which = blockIdx.y & 1, part = threadIdx.x % LANES;
     const int64_t t0 = (int64_t)blockIdx.x * (PASS * kRows) + threadIdx.x / LANES;
     const T *src = static_cast<const T *>(a.x[which]) + h * D + part * 8;
+    uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
+    const uint32_t page_bytes = (uint32_t)g.page_bytes();      // below 2 GiB
     float x[kRows][8];
     int64_t place[kRows];
 #pragma unroll
@@ -42,40 +45,42 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
             if (place[i] != -1 && part == 0 && blockIdx.y == 0) atomicOr(g.err, kErrKvPlace);
             continue;
         }
-        float m = 0.0f;
+        // magnitudes compared as their bits: a NaN is above infinity, and both mark the row
+        int m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = fabsf(x[i][e]);
-            m = y <= FLT_MAX ? fmaxf(m, y) : INFINITY;      // a NaN counts as an infinity
-        }
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_int(x[i][e]) & 0x7fffffff);
 #pragma unroll
-        for (int s = LANES / 2; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, s));
-        float r = m / (float)QMAX;
-        if (r < FLT_MIN) r = 1.0f;
-        const bool finite = m <= FLT_MAX;
+        for (int s = LANES / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(group, m, s));
+        const bool finite = m < 0x7f800000;
+        float r = __int_as_float(m) / (float)QMAX;
+        if (!(r >= FLT_MIN)) r = 1.0f;
         const float inv = 1.0f / r;
         uint32_t u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            // 1.5 * 2^23 + the product, rounded once: the nearest integer to the exact product, ties to even
-            const int z = __float_as_int(fmaf(x[i][e], inv, 12582912.0f)) - 0x4B400000;
-            u[e] = finite ? (uint32_t)(min(max(z, -QMAX), QMAX) + QMAX + 1) : (uint32_t)(QMAX + 1);
+            // 1.5 * 2^23 + the code's offset + the product, rounded once: the nearest integer to the exact product, ties to
+            // even (the constant is even); |product| <= qmax (1 + 2^-22), so it needs no clamp
+            const float y = fmaf(x[i][e], inv, 12582912.0f + (float)(QMAX + 1));
+            u[e] = finite ? __float_as_uint(y) : (uint32_t)(QMAX + 1);
         }
-        // 64 bits only for caches of more than 2^32 tokens
-        const int64_t page = place[i] <= 0xffffffffll ? (int64_t)((uint32_t)place[i] / (uint32_t)g.page_tokens) : place[i] / g.page_tokens;
+        const int64_t page = place[i] < (1 << 30) ? (int64_t)(__umulhi((uint32_t)place[i], a.div_mul) >> a.div_shift)
+                                                  : place[i] / g.page_tokens;
         const int at = (int)(place[i] - page * g.page_tokens);
-        uint8_t *dst = a.cache + g.codes_at(page, h, which) + (int64_t)at * (D * BITS / 8) + part * BITS;
+        uint8_t *base = head + (uint64_t)page * page_bytes;
+        uint8_t *dst = base + (uint32_t)(which * g.page_tokens + at) * (uint32_t)(D * BITS / 8) + part * BITS;
         if constexpr (BITS == 8) {
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(u[0] | u[1] << 8 | u[2] << 16 | u[3] << 24,
-                                                         u[4] | u[5] << 8 | u[6] << 16 | u[7] << 24);
+            auto four = [&](int e) {
+                return __byte_perm(__byte_perm(u[e], u[e + 1], 0x0040), __byte_perm(u[e + 2], u[e + 3], 0x0040), 0x5410);
+            };
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(four(0), four(4));
         } else {
             uint32_t w = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w |= u[e] << (4 * e);
+            for (int e = 0; e < 8; ++e) w |= (u[e] & 0xfu) << (4 * e);
             *reinterpret_cast<uint32_t *>(dst) = w;
         }
         if (part == 0)
-            *reinterpret_cast<float *>(a.cache + g.scales_at(page, h, which) + 4 * (int64_t)at) =
+            *reinterpret_cast<float *>(base + (uint32_t)g.page_tokens * (2u * (D * BITS / 8) + 4u * which) + 4u * at) =
                 finite ? r : __int_as_float(0x7fffffff);
     }
 }
@@ -93,6 +98,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
         return;
     }
     const int64_t first = __ldg(a.cu + s);
+    const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
+    const uint32_t page_bytes = (uint32_t)g.page_bytes();      // below 2 GiB
+    const int32_t *table = a.table + (int64_t)s * a.max_pages;
     uint32_t w[kRows][BITS == 8 ? 2 : 1];
     float r[kRows];
     bool ok[kRows];
@@ -101,14 +109,15 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
         const int t = t0 + i * PASS;
         ok[i] = false;
         if (t >= len) continue;
-        const int p = t / g.page_tokens, page = __ldg(a.table + (int64_t)s * a.max_pages + p), at = t - p * g.page_tokens;
+        const int p = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift), page = __ldg(table + p), at = t - p * g.page_tokens;
         ok[i] = page >= 0 && page < g.n_pages && first + t >= 0 && first + t < a.n_rows;
         if (!ok[i]) {
             if (part == 0 && blockIdx.y == 0) atomicOr(g.err, kErrKvPlace);
             continue;
         }
-        const uint8_t *src = a.cache + g.codes_at(page, h, which) + (int64_t)at * (D * BITS / 8) + part * BITS;
-        r[i] = __ldg(reinterpret_cast<const float *>(a.cache + g.scales_at(page, h, which)) + at);
+        const uint8_t *base = head + (uint64_t)(uint32_t)page * page_bytes;
+        const uint8_t *src = base + (uint32_t)(which * g.page_tokens + at) * (uint32_t)(D * BITS / 8) + part * BITS;
+        r[i] = __ldg(reinterpret_cast<const float *>(base + (uint32_t)g.page_tokens * (2u * (D * BITS / 8) + 4u * which) + 4u * at));
         if constexpr (BITS == 8) {
             const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src));
             w[i][0] = y.x;
@@ -123,9 +132,20 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
         if (!ok[i]) continue;
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t u = BITS == 8 ? (w[i][e / 4 % (BITS == 8 ? 2 : 1)] >> (8 * (e % 4))) & 0xffu : (w[i][0] >> (4 * e)) & 0xfu;
-            x[e] = r[i] * (float)((int)u - ZERO);
+        for (int e = 0; e < 8; e += 2) {
+            // 2^23 + u has the code in its low bits
+            float2 y;
+            if constexpr (BITS == 8) {
+                y.x = __uint_as_float(__byte_perm(w[i][e / 4], 0x4b000000u, 0x7440 + e % 4));
+                y.y = __uint_as_float(__byte_perm(w[i][e / 4], 0x4b000000u, 0x7440 + e % 4 + 1));
+            } else {
+                y.x = __uint_as_float(((w[i][0] >> (4 * e)) & 0xfu) | 0x4b000000u);
+                y.y = __uint_as_float(((w[i][0] >> (4 * e + 4)) & 0xfu) | 0x4b000000u);
+            }
+            const float zero = -(8388608.0f + (float)ZERO);
+            y = mul2(add2(y, make_float2(zero, zero)), make_float2(r[i], r[i]));
+            x[e] = y.x;
+            x[e + 1] = y.y;
         }
         T *to = dst + (first + t0 + i * PASS) * a.stride[which];
         if constexpr (sizeof(T) == 2) {

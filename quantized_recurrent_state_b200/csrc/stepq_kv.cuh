@@ -17,13 +17,6 @@ struct KvGeo {
     __host__ __device__ int row_bytes() const { return d * bits / 8; }
     __host__ __device__ int64_t head_bytes() const { return (int64_t)page_tokens * (2 * row_bytes() + 8); }
     __host__ __device__ int64_t page_bytes() const { return head_bytes() * H; }
-    // offset of the (K: which = 0, V: 1) codes of a page's head, and of its scales
-    __host__ __device__ int64_t codes_at(int64_t page, int h, int which) const {
-        return page * page_bytes() + h * head_bytes() + (int64_t)which * page_tokens * row_bytes();
-    }
-    __host__ __device__ int64_t scales_at(int64_t page, int h, int which) const {
-        return page * page_bytes() + h * head_bytes() + (int64_t)page_tokens * (2 * row_bytes() + 4 * which);
-    }
 };
 
 struct KvAppendArgs {
@@ -33,6 +26,8 @@ struct KvAppendArgs {
     int64_t stride[2];
     const int64_t *places;
     int n_tokens;
+    uint32_t div_mul;       // n / page_tokens = umulhi(n, div_mul) >> div_shift for n < 2^30
+    int div_shift;
 };
 
 struct KvReadArgs {
@@ -43,6 +38,8 @@ struct KvReadArgs {
     int64_t n_rows;
     void *x[2];
     int64_t stride[2];
+    uint32_t div_mul;
+    int div_shift;
 };
 
 struct KvAttendArgs {
@@ -58,7 +55,7 @@ struct KvAttendArgs {
     float *part;            // pieces of units: sums [block][2][row][d]
     float2 *meta;           // and (reference, total) [block][2][row]
     int blocks, row_tiles;
-    uint32_t div_mul;       // t / page_tokens = umulhi(t, div_mul) >> div_shift for t < 2^30
+    uint32_t div_mul;
     int div_shift;
     int seg;                // tokens of a copy: divides a page and a stage of 64, at least 16
 };

@@ -89,7 +89,8 @@ extern "C" int stepq_kv_append(stepq_kv *kv, void *cache, int dtype, int n_token
         return rc;
     const stepq::DeviceScope dev(kv->device);
     if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
-    const stepq::KvAppendArgs a{kv->g, static_cast<uint8_t *>(cache), {k, v}, {k_stride, v_stride}, places, n_tokens};
+    const stepq::KvAppendArgs a{kv->g, static_cast<uint8_t *>(cache), {k, v}, {k_stride, v_stride}, places, n_tokens,
+                                kv->div_mul, kv->div_shift};
     const cudaError_t e = stepq::launch_kv_append(dtype, a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_append launch");
 }
@@ -122,7 +123,7 @@ extern "C" int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const i
     const stepq::DeviceScope dev(kv->device);
     if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
     const stepq::KvReadArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, cu_seqlens, n_seq, max_pages,
-                              n_rows, {k, v}, {k_stride, v_stride}};
+                              n_rows, {k, v}, {k_stride, v_stride}, kv->div_mul, kv->div_shift};
     const cudaError_t e = stepq::launch_kv_read(dtype, a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_read launch");
 }
