@@ -1,10 +1,11 @@
 // Quantising keys and values into the paged cache as they are written, and
 // reading sequences back (definitions: include/stepq.h).
 //
-// Both kernels move each byte once: a thread takes eight neighbouring values of a row (one 16-byte load of a 16-bit type),
-// d / 8 lanes share a row, and the row's maximum is log2(d / 8) shuffles.  A block works on the keys or the values
-// of one head (the grid's second dimension, so that no thread divides to find its place); a thread has kRows pieces
-// and loads them all before it works on the first.  HBM-bound at large sizes, launch-bound at small ones.
+// Both kernels move each byte once: a thread takes twice eight neighbouring values of a row (two 16-byte loads of a 16-bit
+// type), one in each half, so d / 16 lanes share a row, a place or page and a scale are looked up once for 16 values, and the
+// row's maximum is log2(d / 16) shuffles.  A block works on the keys or the values
+// of one head; the heads of the same tokens are neighbouring blocks, whose rows lie side by side outside the cache.  A
+// thread has kRows rows and loads them all before it works on the first.  HBM-bound at large sizes, launch-bound at small ones.
 #include <float.h>
 
 #include "stepq_delta.cuh"
@@ -19,14 +20,15 @@ constexpr int kThreads = 256, kRows = 4;
 
 template <int D, int BITS, class T>
 __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
-    constexpr int LANES = D / 8, PASS = kThreads / LANES, QMAX = (1 << (BITS - 1)) - 1;
+    constexpr int LANES = D / 16, PASS = kThreads / LANES, QMAX = (1 << (BITS - 1)) - 1;
     const KvGeo &g = a.g;
-    const int h = blockIdx.y >> 1, which = blockIdx.y & 1, part = threadIdx.x % LANES;
-    const int64_t t0 = (int64_t)blockIdx.x * (PASS * kRows) + threadIdx.x / LANES;
+    const uint32_t tile = blockIdx.x / (2u * g.H), hw = blockIdx.x - tile * 2u * g.H;
+    const int which = hw >= (uint32_t)g.H, h = hw - which * g.H, part = threadIdx.x % LANES;
+    const int64_t t0 = (int64_t)tile * (PASS * kRows) + threadIdx.x / LANES;
     const T *src = static_cast<const T *>(a.x[which]) + h * D + part * 8;
     uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
     const uint32_t page_bytes = (uint32_t)g.page_bytes();      // below 2 GiB
-    float x[kRows][8];
+    float x[kRows][2][8];
     int64_t place[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -34,7 +36,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
         place[i] = -1;
         if (t >= a.n_tokens) continue;
         place[i] = __ldg(a.places + t);
-        load_vec<8>(src + t * a.stride[which], x[i]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) load_vec<8>(src + t * a.stride[which] + c * (D / 2), x[i][c]);
     }
     // rows are whole groups of lanes of one warp (32 is a multiple of LANES), which take the same way
     const unsigned lane0 = (threadIdx.x & 31) / LANES * LANES;
@@ -42,42 +45,45 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         if (place[i] < 0 || place[i] >= (int64_t)g.n_pages * g.page_tokens) {
-            if (place[i] != -1 && part == 0 && blockIdx.y == 0) atomicOr(g.err, kErrKvPlace);
+            if (place[i] != -1 && part == 0 && hw == 0) atomicOr(g.err, kErrKvPlace);
             continue;
         }
         // magnitudes compared as their bits: a NaN is above infinity, and both mark the row
         int m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, __float_as_int(x[i][e]) & 0x7fffffff);
+        for (int e = 0; e < 16; ++e) m = max(m, __float_as_int(x[i][e / 8][e % 8]) & 0x7fffffff);
 #pragma unroll
         for (int s = LANES / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(group, m, s));
         const bool finite = m < 0x7f800000;
         float r = __int_as_float(m) / (float)QMAX;
         if (!(r >= FLT_MIN)) r = 1.0f;
         const float inv = 1.0f / r;
-        uint32_t u[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            // 1.5 * 2^23 + the code's offset + the product, rounded once: the nearest integer to the exact product, ties to
-            // even (the constant is even); |product| <= qmax (1 + 2^-22), so it needs no clamp
-            const float y = fmaf(x[i][e], inv, 12582912.0f + (float)(QMAX + 1));
-            u[e] = finite ? __float_as_uint(y) : (uint32_t)(QMAX + 1);
-        }
         const int64_t page = place[i] < (1 << 30) ? (int64_t)(__umulhi((uint32_t)place[i], a.div_mul) >> a.div_shift)
                                                   : place[i] / g.page_tokens;
         const int at = (int)(place[i] - page * g.page_tokens);
         uint8_t *base = head + (uint64_t)page * page_bytes;
         uint8_t *dst = base + (uint32_t)(which * g.page_tokens + at) * (uint32_t)(D * BITS / 8) + part * BITS;
-        if constexpr (BITS == 8) {
-            auto four = [&](int e) {
-                return __byte_perm(__byte_perm(u[e], u[e + 1], 0x0040), __byte_perm(u[e + 2], u[e + 3], 0x0040), 0x5410);
-            };
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(four(0), four(4));
-        } else {
-            uint32_t w = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w |= (u[e] & 0xfu) << (4 * e);
-            *reinterpret_cast<uint32_t *>(dst) = w;
+        for (int c = 0; c < 2; ++c) {
+            uint32_t u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // 1.5 * 2^23 + the code's offset + the product, rounded once: the nearest integer to the exact product, ties
+                // to even (the constant is even); |product| <= qmax (1 + 2^-22), so it needs no clamp
+                const float y = fmaf(x[i][c][e], inv, 12582912.0f + (float)(QMAX + 1));
+                u[e] = finite ? __float_as_uint(y) : (uint32_t)(QMAX + 1);
+            }
+            if constexpr (BITS == 8) {
+                auto four = [&](int e) {
+                    return __byte_perm(__byte_perm(u[e], u[e + 1], 0x0040), __byte_perm(u[e + 2], u[e + 3], 0x0040), 0x5410);
+                };
+                *reinterpret_cast<uint2 *>(dst + c * (D * BITS / 16)) = make_uint2(four(0), four(4));
+            } else {
+                uint32_t w = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w |= (u[e] & 0xfu) << (4 * e);
+                *reinterpret_cast<uint32_t *>(dst + c * (D * BITS / 16)) = w;
+            }
         }
         if (part == 0)
             *reinterpret_cast<float *>(base + (uint32_t)g.page_tokens * (2u * (D * BITS / 8) + 4u * which) + 4u * at) =
@@ -87,21 +93,22 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
 
 template <int D, int BITS, class T>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
-    constexpr int LANES = D / 8, PASS = kThreads / LANES, ZERO = 1 << (BITS - 1);
+    constexpr int LANES = D / 16, PASS = kThreads / LANES, ZERO = 1 << (BITS - 1);
     const KvGeo &g = a.g;
-    const int s = (int)(blockIdx.x / tiles), t0 = (int)(blockIdx.x % tiles) * (PASS * kRows) + threadIdx.x / LANES;
-    const int h = blockIdx.y >> 1, which = blockIdx.y & 1, part = threadIdx.x % LANES;
+    const uint32_t tile = blockIdx.x / (2u * g.H), hw = blockIdx.x - tile * 2u * g.H;
+    const int which = hw >= (uint32_t)g.H, h = hw - which * g.H, part = threadIdx.x % LANES;
+    const int s = (int)(tile / tiles), t0 = (int)(tile % tiles) * (PASS * kRows) + threadIdx.x / LANES;
     const int len = __ldg(a.lens + s);
     if (t0 >= len) return;
     if (len > (int64_t)a.max_pages * g.page_tokens) {
-        if (part == 0 && blockIdx.y == 0) atomicOr(g.err, kErrKvLen);
+        if (part == 0 && hw == 0) atomicOr(g.err, kErrKvLen);
         return;
     }
     const int64_t first = __ldg(a.cu + s);
     const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
     const uint32_t page_bytes = (uint32_t)g.page_bytes();      // below 2 GiB
     const int32_t *table = a.table + (int64_t)s * a.max_pages;
-    uint32_t w[kRows][BITS == 8 ? 2 : 1];
+    uint32_t w[kRows][2][BITS == 8 ? 2 : 1];
     float r[kRows];
     bool ok[kRows];
 #pragma unroll
@@ -112,47 +119,53 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
         const int p = (int)(__umulhi((uint32_t)t, a.div_mul) >> a.div_shift), page = __ldg(table + p), at = t - p * g.page_tokens;
         ok[i] = page >= 0 && page < g.n_pages && first + t >= 0 && first + t < a.n_rows;
         if (!ok[i]) {
-            if (part == 0 && blockIdx.y == 0) atomicOr(g.err, kErrKvPlace);
+            if (part == 0 && hw == 0) atomicOr(g.err, kErrKvPlace);
             continue;
         }
         const uint8_t *base = head + (uint64_t)(uint32_t)page * page_bytes;
         const uint8_t *src = base + (uint32_t)(which * g.page_tokens + at) * (uint32_t)(D * BITS / 8) + part * BITS;
         r[i] = __ldg(reinterpret_cast<const float *>(base + (uint32_t)g.page_tokens * (2u * (D * BITS / 8) + 4u * which) + 4u * at));
-        if constexpr (BITS == 8) {
-            const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src));
-            w[i][0] = y.x;
-            w[i][1] = y.y;
-        } else {
-            w[i][0] = __ldg(reinterpret_cast<const unsigned int *>(src));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if constexpr (BITS == 8) {
+                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src + c * (D / 2)));
+                w[i][c][0] = y.x;
+                w[i][c][1] = y.y;
+            } else {
+                w[i][c][0] = __ldg(reinterpret_cast<const unsigned int *>(src + c * (D / 4)));
+            }
         }
     }
     T *dst = static_cast<T *>(a.x[which]) + h * D + part * 8;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         if (!ok[i]) continue;
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            // 2^23 + u has the code in its low bits
-            float2 y;
-            if constexpr (BITS == 8) {
-                y.x = __uint_as_float(__byte_perm(w[i][e / 4], 0x4b000000u, 0x7440 + e % 4));
-                y.y = __uint_as_float(__byte_perm(w[i][e / 4], 0x4b000000u, 0x7440 + e % 4 + 1));
-            } else {
-                y.x = __uint_as_float(((w[i][0] >> (4 * e)) & 0xfu) | 0x4b000000u);
-                y.y = __uint_as_float(((w[i][0] >> (4 * e + 4)) & 0xfu) | 0x4b000000u);
-            }
-            const float zero = -(8388608.0f + (float)ZERO);
-            y = mul2(add2(y, make_float2(zero, zero)), make_float2(r[i], r[i]));
-            x[e] = y.x;
-            x[e + 1] = y.y;
-        }
         T *to = dst + (first + t0 + i * PASS) * a.stride[which];
-        if constexpr (sizeof(T) == 2) {
-            store_vec<8>(to, x);
-        } else {
-            *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                // 2^23 + u has the code in its low bits
+                float2 y;
+                if constexpr (BITS == 8) {
+                    y.x = __uint_as_float(__byte_perm(w[i][c][e / 4], 0x4b000000u, 0x7440 + e % 4));
+                    y.y = __uint_as_float(__byte_perm(w[i][c][e / 4], 0x4b000000u, 0x7440 + e % 4 + 1));
+                } else {
+                    y.x = __uint_as_float(((w[i][c][0] >> (4 * e)) & 0xfu) | 0x4b000000u);
+                    y.y = __uint_as_float(((w[i][c][0] >> (4 * e + 4)) & 0xfu) | 0x4b000000u);
+                }
+                const float zero = -(8388608.0f + (float)ZERO);
+                y = mul2(add2(y, make_float2(zero, zero)), make_float2(r[i], r[i]));
+                x[e] = y.x;
+                x[e + 1] = y.y;
+            }
+            if constexpr (sizeof(T) == 2) {
+                store_vec<8>(to + c * (D / 2), x);
+            } else {
+                *reinterpret_cast<float4 *>(to + c * (D / 2)) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4 *>(to + c * (D / 2) + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            }
         }
     }
 }
@@ -176,9 +189,9 @@ cudaError_t dispatch(const KvGeo &g, int dtype, F f) {
 }  // namespace
 
 cudaError_t launch_kv_append(int dtype, const KvAppendArgs &a, cudaStream_t st) {
-    const int64_t tile = kThreads / (a.g.d / 8) * kRows, blocks = (a.n_tokens + tile - 1) / tile;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)blocks, 2 * a.g.H);
+    const int64_t tile = kThreads / (a.g.d / 16) * kRows, blocks = (a.n_tokens + tile - 1) / tile;
+    if (blocks * 2 * a.g.H > 0x7fffffff) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(blocks * 2 * a.g.H);
     return dispatch(a.g, dtype, [&](auto d, auto b, auto t) {
         k_kv_append<decltype(d)::value, decltype(b)::value, decltype(t)><<<grid, kThreads, 0, st>>>(a);
         return cudaGetLastError();
@@ -186,9 +199,9 @@ cudaError_t launch_kv_append(int dtype, const KvAppendArgs &a, cudaStream_t st) 
 }
 
 cudaError_t launch_kv_read(int dtype, const KvReadArgs &a, cudaStream_t st) {
-    const int64_t tile = kThreads / (a.g.d / 8) * kRows, tiles = ((int64_t)a.max_pages * a.g.page_tokens + tile - 1) / tile;
-    if (tiles * a.n_seq > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)(tiles * a.n_seq), 2 * a.g.H);
+    const int64_t tile = kThreads / (a.g.d / 16) * kRows, tiles = ((int64_t)a.max_pages * a.g.page_tokens + tile - 1) / tile;
+    if (tiles * a.n_seq > 0x7fffffff || tiles * a.n_seq * 2 * a.g.H > 0x7fffffff) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(tiles * a.n_seq * 2 * a.g.H);
     return dispatch(a.g, dtype, [&](auto d, auto b, auto t) {
         k_kv_read<decltype(d)::value, decltype(b)::value, decltype(t)><<<grid, kThreads, 0, st>>>(a, (int)tiles);
         return cudaGetLastError();
