@@ -1217,7 +1217,10 @@ extern "C" int stepq_delta_prefill(stepq_ctx *c, int layer, float *S, const int3
     const stepq::DeviceScope dev(c->device);
     if (dev.error() != cudaSuccess) return cuda_fail(dev.error(), "cudaSetDevice");
     LaunchTimer lt(c, 4, c->main);
-    const bool chunked = c->plan->D == 128 && c->plan->mode == 0 && tokens->dtype != STEPQ_FP32;
+    // Chunks of 64 tokens, but token by token where no sequence can fill much of one: many blocks an SM, and no chunk's fixed
+    // cost (4 sequences of 32 heads: 17 us either way up to 16 tokens, 26 against 18 us up to 32).  The chunked kernel does
+    // the same for the short sequences of a mixed batch.
+    const bool chunked = c->plan->D == 128 && c->plan->mode == 0 && tokens->dtype != STEPQ_FP32 && n_tokens > 16;
     const cudaError_t e = chunked ? stepq::launch_delta_chunk(tokens->dtype, a, c->main)
                                   : stepq::launch_delta_seq(c->plan->D, tokens->dtype, c->plan->mode == 1, a, c->main);
     if (e != cudaSuccess) return cuda_fail(e, "delta_prefill launch");

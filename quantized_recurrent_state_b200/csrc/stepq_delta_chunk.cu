@@ -122,6 +122,59 @@ __device__ __forceinline__ __nv_bfloat162 highs(__nv_bfloat162 x, __nv_bfloat162
 __device__ __forceinline__ float2 to_f32x2(__half2 x) { return __half22float2(x); }
 __device__ __forceinline__ float2 to_f32x2(__nv_bfloat162 x) { return __bfloat1622float2(x); }
 
+// A sequence of at most kShort tokens, token by token: a warp has 8 value columns, lane 4 g + c rows [16 g, 16 g + 16) of two.
+// A chunk costs a block about 12 us however few tokens it has (64 sequences of 32 heads: up to 4 tokens 176 us in chunks).
+constexpr int kShort = 12;
+template <class T>
+__device__ __forceinline__ void short_sequence(const DeltaArgs &a, float *Sg, bool fresh, int first, int count, int h, int hk) {
+    const int lane = threadIdx.x & 31, row0 = (lane >> 2) * 16, col0 = 8 * (threadIdx.x >> 5) + 2 * (lane & 3);
+    Sg += (size_t)row0 * D + col0;
+    float2 S[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) S[r] = fresh ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(Sg + (size_t)r * D);
+    auto sum = [&](float2 x) {   // over the eight groups of rows
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) {
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, m);
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, m);
+        }
+        return x;
+    };
+    bool good = true;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        const size_t t = (size_t)(first + i);
+        float k[16], q[16], v[2];
+        load_vec<16>(static_cast<const T *>(a.k) + t * a.ks + hk * D + row0, k);
+        load_vec<16>(static_cast<const T *>(a.q) + t * a.qs + hk * D + row0, q);
+        load_vec<2>(static_cast<const T *>(a.v) + t * a.vs + h * D + col0, v);
+        const float al = __ldg(a.alpha + t * a.H + h), bt = __ldg(a.beta + t * a.H + h);
+        good = good && al > 0.0f && al <= 1.0f;
+        float2 u = make_float2(0.f, 0.f), o = u;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            S[r] = mul2(S[r], make_float2(al, al));
+            u = fma2(make_float2(k[r], k[r]), S[r], u);
+        }
+        u = sum(u);
+        u = make_float2(bt * (v[0] - u.x), bt * (v[1] - u.y));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            S[r] = fma2(make_float2(k[r], k[r]), u, S[r]);
+            o = fma2(make_float2(q[r], q[r]), S[r], o);
+        }
+        o = sum(o);
+        if (lane < 4) {
+            T *dst = static_cast<T *>(a.o) + t * a.os + h * D + col0;
+            *reinterpret_cast<typename Pair<T>::type *>(dst) = typename Pair<T>::type(from_f32<T>(o.x), from_f32<T>(o.y));
+        }
+    }
+    if (!good) atomicOr(a.err, kErrGateRange);
+    if (count > 0 || fresh)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) *reinterpret_cast<float2 *>(Sg + (size_t)r * D) = S[r];
+}
+
 template <class T>
 __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -136,9 +189,8 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
     float *Sg = delta_state(a, s, h, D, kErrBadSlot);
     if (!Sg) return;
     const bool fresh = a.fresh && a.fresh[s];
-    if (count == 0) {
-        if (fresh)
-            for (int e = tid; e < D * D / 4; e += NT) reinterpret_cast<float4 *>(Sg)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (count <= kShort) {
+        short_sequence<T>(a, Sg, fresh, first, count, h, hk);
         return;
     }
     const int chunks = (count + C - 1) / C;
@@ -772,6 +824,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
 
 template <class T>
 cudaError_t launch(const DeltaArgs &a, cudaStream_t st) {
+    static_assert(NT / 32 * 8 == D, "a warp to every eight value columns");
     static_assert(sizeof(Smem<T>) <= 227 * 1024, "shared memory of a block");
     const long long blocks = (long long)a.n_seq * a.H;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;

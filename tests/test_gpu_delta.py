@@ -147,6 +147,25 @@ def test_prefill_ragged(stepq, lens, dtype, D, rows):
     assert torch.equal(pool[idle], before[idle])
 
 
+def test_prefill_mixed_with_single_tokens(stepq):
+    """Short sequences run token by token and long ones in chunks, in one call: each sequence is done once, by one of them."""
+    lens, H, D = [1, 12, 13, 200, 0, 1, 3, 64, 0, 11], 4, 128
+    ctx = _ctx(stepq, H, D, len(lens))
+    x = _inputs(11, sum(lens), H, 2, D, "bf16", wide=True)
+    S = torch.randn(len(lens), H, D, D, device="cuda")
+    before = S.clone()
+    cu = np.cumsum([0] + lens).tolist()
+    fresh = torch.zeros(len(lens), dtype=torch.uint8, device="cuda")
+    fresh[[5, 7, 8]] = 1
+    ctx.delta_prefill(S, None, torch.tensor(cu, dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"], x["alpha"], x["beta"],
+                      x["o"], fresh=fresh)
+    ctx.sync()
+    for s, n in enumerate(lens):
+        part = _slice(x, cu[s], cu[s + 1])
+        R, o, C = _reference(before[s].double() * (1 - int(fresh[s])), part, False)
+        _check(S[s], part["o"], R, o, C, n, D, "bf16", part["q"], chunked=n > 12)
+
+
 def test_prefill_dense_states_and_one_head_group(stepq):
     """slots None: states [n_seq][H][D][D]; every value head with its own q and k."""
     lens, H, D = [70, 3], 3, 128
