@@ -326,7 +326,14 @@ int stepq_delta_step(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, 
  * is skipped).  Sequences may be empty.  Where fresh (device uint8[n_seq], NULL: none) is
  * nonzero the sequence starts from S = 0 (an empty one leaves zeros).
  * alpha in (0, 1]: a gate outside it sets the device error word and that
- * head's results are not valid. */
+ * head's results are not valid.
+ * Per-head plans at d = 128 with fp16 or bfloat16 tokens run chunks of 64
+ * tokens on the tensor cores (sequences of up to 12 tokens, and all other calls, run
+ * token by token): states stay fp32, with operands as sums of two fp16
+ * values under powers of two, so results match the token-by-token form to the tolerances
+ * stated in the tests, not bit for bit.  The chunked form holds for beta_t |k_t|^2
+ * <= 2, where the recurrence does not grow; beyond that intermediate values may leave
+ * fp16, which sets the device error word ("prefill range"). */
 int stepq_delta_prefill(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, const uint8_t *fresh,
                         int n_seq, const int32_t *cu_seqlens, int n_tokens, const stepq_tokens *tokens);
 
@@ -389,8 +396,12 @@ int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const int32_t *pag
  *   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max)
  * lse (fp32 [n_seq][n_tok][n_q_heads], or NULL) receives the logarithm of
  * sum_t exp(scale q.k_t).  A token that sees nothing gets o = 0 and lse =
- * -infinity.  scale is finite and above 0.  workspace: stepq_kv_attend_workspace_bytes (of the same
- * arguments) bytes, 16-byte aligned, used by one call at a time. */
+ * -infinity.  scale is finite and above 0.  Sums and softmax statistics are fp32;
+ * the weights p_t r_t enter their product in fp16 (two terms for fp32 queries), and
+ * value rows with r below 2^-60 may count as zeros.  Results do not depend on
+ * timing.  workspace: stepq_kv_attend_workspace_bytes (of the same arguments) bytes,
+ * 16-byte aligned, used by one call at a time (two captured graphs that may run
+ * at the same time need one each). */
 int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const int32_t *page_table, int max_pages,
                     const int32_t *lens, int dtype, int n_tok, int n_q_heads, const void *q, int64_t q_stride,
                     float scale, void *o, int64_t o_stride, float *lse, void *workspace, void *stream);
