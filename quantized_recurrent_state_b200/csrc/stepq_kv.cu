@@ -4,8 +4,12 @@
 // Both kernels move each byte once: a thread takes twice eight neighbouring values of a row (two 16-byte loads of a 16-bit
 // type), one in each half, so d / 16 lanes share a row, a place or page and a scale are looked up once for 16 values, and the
 // row's maximum is log2(d / 16) shuffles.  A block works on the keys or the values
-// of one head; the heads of the same tokens are neighbouring blocks, whose rows lie side by side outside the cache.  A
-// thread has kRows rows and loads them all before it works on the first.  HBM-bound at large sizes, launch-bound at small ones.
+// of one head; the heads of the same tokens are neighbouring blocks, whose rows lie side by side outside the cache.
+// Bytes in flight hide the latency.  Writing: one row a thread and many threads (6,144 tokens, 8 heads of 128, 8 bits, bf16: 15.4 us,
+// 38 MB; two and four rows, whose registers leave fewer warps, 16.4 and 23 us).  Reading, where a row is 16 bytes a
+// thread behind three dependent loads: eight rows at once (31,000 such tokens: 46 us, 192 MB, 4.2 TB/s; four and two rows 47 and
+// 66 us).  Bound by those latencies and HBM at large sizes, by the launch at small ones (70 tokens of 4 heads of 64 written: 2.3 us;
+// 70 sequences of up to 300 read: 7.2 us, four rows 8.9).
 #include <float.h>
 
 #include "stepq_delta.cuh"
@@ -16,7 +20,7 @@ namespace stepq {
 
 namespace {
 
-constexpr int kThreads = 256, kRows = 4;
+constexpr int kThreads = 256, kReadRows = 8;
 
 template <int D, int BITS, class T>
 __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
@@ -24,71 +28,63 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
     const KvGeo &g = a.g;
     const uint32_t tile = blockIdx.x / (2u * g.H), hw = blockIdx.x - tile * 2u * g.H;
     const int which = hw >= (uint32_t)g.H, h = hw - which * g.H, part = threadIdx.x % LANES;
-    const int64_t t0 = (int64_t)tile * (PASS * kRows) + threadIdx.x / LANES;
-    const T *src = static_cast<const T *>(a.x[which]) + h * D + part * 8;
+    const int64_t t = (int64_t)tile * PASS + threadIdx.x / LANES;
+    if (t >= a.n_tokens) return;
+    const int64_t place = __ldg(a.places + t);
+    const T *src = static_cast<const T *>(a.x[which]) + t * a.stride[which] + h * D + part * 8;
+    float x[2][8];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) load_vec<8>(src + c * (D / 2), x[c]);
     uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
     const uint32_t page_bytes = (uint32_t)g.page_bytes();      // below 2 GiB
-    float x[kRows][2][8];
-    int64_t place[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t t = t0 + i * PASS;
-        place[i] = -1;
-        if (t >= a.n_tokens) continue;
-        place[i] = __ldg(a.places + t);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) load_vec<8>(src + t * a.stride[which] + c * (D / 2), x[i][c]);
-    }
     // rows are whole groups of lanes of one warp (32 is a multiple of LANES), which take the same way
     const unsigned lane0 = (threadIdx.x & 31) / LANES * LANES;
     const unsigned group = (LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u)) << lane0;
+    // magnitudes compared as their bits: a NaN is above infinity, and both mark the row
+    int m = 0;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        if (place[i] < 0 || place[i] >= (int64_t)g.n_pages * g.page_tokens) {
-            if (place[i] != -1 && part == 0 && hw == 0) atomicOr(g.err, kErrKvPlace);
-            continue;
-        }
-        // magnitudes compared as their bits: a NaN is above infinity, and both mark the row
-        int m = 0;
+    for (int e = 0; e < 16; ++e) m = max(m, __float_as_int(x[e / 8][e % 8]) & 0x7fffffff);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) m = max(m, __float_as_int(x[i][e / 8][e % 8]) & 0x7fffffff);
-#pragma unroll
-        for (int s = LANES / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(group, m, s));
-        const bool finite = m < 0x7f800000;
-        float r = __int_as_float(m) / (float)QMAX;
-        if (!(r >= FLT_MIN)) r = 1.0f;
-        const float inv = 1.0f / r;
-        const int64_t page = place[i] < (1 << 30) ? (int64_t)(__umulhi((uint32_t)place[i], a.div_mul) >> a.div_shift)
-                                                  : place[i] / g.page_tokens;
-        const int at = (int)(place[i] - page * g.page_tokens);
-        uint8_t *base = head + (uint64_t)page * page_bytes;
-        uint8_t *dst = base + (uint32_t)(which * g.page_tokens + at) * (uint32_t)(D * BITS / 8) + part * BITS;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t u[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                // 1.5 * 2^23 + the code's offset + the product, rounded once: the nearest integer to the exact product, ties
-                // to even (the constant is even); |product| <= qmax (1 + 2^-22), so it needs no clamp
-                const float y = fmaf(x[i][c][e], inv, 12582912.0f + (float)(QMAX + 1));
-                u[e] = finite ? __float_as_uint(y) : (uint32_t)(QMAX + 1);
-            }
-            if constexpr (BITS == 8) {
-                auto four = [&](int e) {
-                    return __byte_perm(__byte_perm(u[e], u[e + 1], 0x0040), __byte_perm(u[e + 2], u[e + 3], 0x0040), 0x5410);
-                };
-                *reinterpret_cast<uint2 *>(dst + c * (D * BITS / 16)) = make_uint2(four(0), four(4));
-            } else {
-                uint32_t w = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w |= (u[e] & 0xfu) << (4 * e);
-                *reinterpret_cast<uint32_t *>(dst + c * (D * BITS / 16)) = w;
-            }
-        }
-        if (part == 0)
-            *reinterpret_cast<float *>(base + (uint32_t)g.page_tokens * (2u * (D * BITS / 8) + 4u * which) + 4u * at) =
-                finite ? r : __int_as_float(0x7fffffff);
+    for (int s = LANES / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(group, m, s));
+    // (asked here, so that the row's loads do not wait for its place)
+    if (place < 0 || place >= (int64_t)g.n_pages * g.page_tokens) {
+        if (place != -1 && part == 0 && hw == 0) atomicOr(g.err, kErrKvPlace);
+        return;
     }
+    const bool finite = m < 0x7f800000;
+    float r = __int_as_float(m) / (float)QMAX;
+    if (!(r >= FLT_MIN)) r = 1.0f;
+    const float inv = 1.0f / r;
+    const int64_t page = place < (1 << 30) ? (int64_t)(__umulhi((uint32_t)place, a.div_mul) >> a.div_shift)
+                                           : place / g.page_tokens;
+    const int at = (int)(place - page * g.page_tokens);
+    uint8_t *base = head + (uint64_t)page * page_bytes;
+    uint8_t *dst = base + (uint32_t)(which * g.page_tokens + at) * (uint32_t)(D * BITS / 8) + part * BITS;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // 1.5 * 2^23 + the code's offset + the product, rounded once: the nearest integer to the exact product, ties
+            // to even (the constant is even); |product| <= qmax (1 + 2^-22), so it needs no clamp
+            const float y = fmaf(x[c][e], inv, 12582912.0f + (float)(QMAX + 1));
+            u[e] = finite ? __float_as_uint(y) : (uint32_t)(QMAX + 1);
+        }
+        if constexpr (BITS == 8) {
+            auto four = [&](int e) {
+                return __byte_perm(__byte_perm(u[e], u[e + 1], 0x0040), __byte_perm(u[e + 2], u[e + 3], 0x0040), 0x5410);
+            };
+            *reinterpret_cast<uint2 *>(dst + c * (D * BITS / 16)) = make_uint2(four(0), four(4));
+        } else {
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w |= (u[e] & 0xfu) << (4 * e);
+            *reinterpret_cast<uint32_t *>(dst + c * (D * BITS / 16)) = w;
+        }
+    }
+    if (part == 0)
+        *reinterpret_cast<float *>(base + (uint32_t)g.page_tokens * (2u * (D * BITS / 8) + 4u * which) + 4u * at) =
+            finite ? r : __int_as_float(0x7fffffff);
 }
 
 template <int D, int BITS, class T>
@@ -97,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
     const KvGeo &g = a.g;
     const uint32_t tile = blockIdx.x / (2u * g.H), hw = blockIdx.x - tile * 2u * g.H;
     const int which = hw >= (uint32_t)g.H, h = hw - which * g.H, part = threadIdx.x % LANES;
-    const int s = (int)(tile / tiles), t0 = (int)(tile % tiles) * (PASS * kRows) + threadIdx.x / LANES;
+    const int s = (int)(tile / tiles), t0 = (int)(tile % tiles) * (PASS * kReadRows) + threadIdx.x / LANES;
     const int len = __ldg(a.lens + s);
     if (t0 >= len) return;
     if (len > (int64_t)a.max_pages * g.page_tokens) {
@@ -108,11 +104,11 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
     const uint8_t *const head = a.cache + (int64_t)h * g.head_bytes();
     const uint32_t page_bytes = (uint32_t)g.page_bytes();      // below 2 GiB
     const int32_t *table = a.table + (int64_t)s * a.max_pages;
-    uint32_t w[kRows][2][BITS == 8 ? 2 : 1];
-    float r[kRows];
-    bool ok[kRows];
+    uint32_t w[kReadRows][2][BITS == 8 ? 2 : 1];
+    float r[kReadRows];
+    bool ok[kReadRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
         const int t = t0 + i * PASS;
         ok[i] = false;
         if (t >= len) continue;
@@ -138,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvReadArgs a, int tiles) {
     }
     T *dst = static_cast<T *>(a.x[which]) + h * D + part * 8;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
         if (!ok[i]) continue;
         T *to = dst + (first + t0 + i * PASS) * a.stride[which];
 #pragma unroll
@@ -189,7 +185,7 @@ cudaError_t dispatch(const KvGeo &g, int dtype, F f) {
 }  // namespace
 
 cudaError_t launch_kv_append(int dtype, const KvAppendArgs &a, cudaStream_t st) {
-    const int64_t tile = kThreads / (a.g.d / 16) * kRows, blocks = (a.n_tokens + tile - 1) / tile;
+    const int64_t tile = kThreads / (a.g.d / 16), blocks = (a.n_tokens + tile - 1) / tile;
     if (blocks * 2 * a.g.H > 0x7fffffff) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(blocks * 2 * a.g.H);
     return dispatch(a.g, dtype, [&](auto d, auto b, auto t) {
@@ -199,7 +195,7 @@ cudaError_t launch_kv_append(int dtype, const KvAppendArgs &a, cudaStream_t st) 
 }
 
 cudaError_t launch_kv_read(int dtype, const KvReadArgs &a, cudaStream_t st) {
-    const int64_t tile = kThreads / (a.g.d / 16) * kRows, tiles = ((int64_t)a.max_pages * a.g.page_tokens + tile - 1) / tile;
+    const int64_t tile = kThreads / (a.g.d / 16) * kReadRows, tiles = ((int64_t)a.max_pages * a.g.page_tokens + tile - 1) / tile;
     if (tiles * a.n_seq > 0x7fffffff || tiles * a.n_seq * 2 * a.g.H > 0x7fffffff) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(tiles * a.n_seq * 2 * a.g.H);
     return dispatch(a.g, dtype, [&](auto d, auto b, auto t) {
