@@ -31,6 +31,11 @@
 // The cache comes in by bulk copies of whole rows of a page into a ring of stages, issued by a fifth warp that runs ahead
 // across units.  Each of the other four warps works on its own 16 tokens of every stage with its own reference, total and sums,
 // joined in a fixed order at the end of a unit.
+//
+// Measured: 70 requests of up to 8,192 tokens, 8 cache heads of 128, 8 bits, 32 query heads: 130 to 138 us, 0.66 GB, 5 TB/s (the stages
+// alone run at the copy's rate; the start of a block costs 6 us, the end of a unit 3 to 4, the join 7).  One request of
+// 131,072 tokens at 4 bits: 49 us against 22: 4-bit codes cost 350 instructions a tile of 16 tokens, and the SM issues 59 % of the
+// time.  16 requests of up to 20,000 tokens, two heads of 256: 53 us against 29.  Few short ones: 14 us, launch and host.
 #include <float.h>
 
 #include <type_traits>

@@ -12,7 +12,7 @@ direction; a factor of 4 covers it for the lengths tested with long memories
 o adds |q| times that, its own dot product, and half a step of its type.
 
 The chunked form (d = 128, per-head gates, 16-bit tokens, prompts) sums in another order, and takes S, U and the
-triangular inverse as two bfloat16 terms (2^-18 of each value is left out).  For one token that is
+triangular inverse as two 16-bit terms (2^-22 of each value is left out with fp16, 2^-18 with bfloat16: the bound is for either).  For one token that is
 2^-18 |S_j| of k^T S, 2^-17 (128 fp32 additions), and twice two terms of the solve, whose rows sum to at most 2 for the
 tested gates: 2^-15 C together at the worst.  Those are roundings of different values from token to token, so they add up as
 the root of the number of tokens.  Its readout of bfloat16 tokens takes S, U and A rounded once (2^-8 at the worst, half of that
