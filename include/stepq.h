@@ -292,7 +292,7 @@ int stepq_prefill(stepq_ctx *ctx, void *pool, const int32_t *slots, int n_req, i
  * and o n_heads x d; value head h reads q and k head h / (n_heads / n_qk_heads).
  * Row t of q starts at q + t * q_stride elements (likewise k, v, o): a stride
  * is at least the row's width and a multiple of 16 bytes, and the arrays are
- * 16-byte aligned, so q, k and v may be slices of one wider row.  alpha
+ * 16-byte aligned, so q, k and v may be slices of one wider row.  o overlaps no input.  alpha
  * (fp32) is dense, [tokens][n_heads] for per-head plans, [tokens][n_heads][d]
  * (16-byte aligned) for per-row plans; beta (fp32) is [tokens][n_heads]. */
 typedef struct stepq_tokens {
@@ -333,7 +333,9 @@ int stepq_delta_step(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, 
  * values under powers of two, so results match the token-by-token form to the tolerances
  * stated in the tests, not bit for bit.  The chunked form holds for beta_t |k_t|^2
  * <= 2, where the recurrence does not grow; beyond that intermediate values may leave
- * fp16, which sets the device error word ("prefill range"). */
+ * fp16, which sets the device error word ("prefill range").  An infinity or NaN in k or v reaches
+ * its head's state and outputs from that token on, in the chunked form from the first token
+ * of its chunk on; one in q reaches its own token's output. */
 int stepq_delta_prefill(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, const uint8_t *fresh,
                         int n_seq, const int32_t *cu_seqlens, int n_tokens, const stepq_tokens *tokens);
 
@@ -396,7 +398,7 @@ int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const int32_t *pag
  *   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max)
  * lse (fp32 [n_seq][n_tok][n_q_heads], or NULL) receives the logarithm of
  * sum_t exp(scale q.k_t).  A token that sees nothing gets o = 0 and lse =
- * -infinity.  scale is finite and above 0.  Sums and softmax statistics are fp32;
+ * -infinity.  o overlaps no input.  scale is finite and above 0.  Sums and softmax statistics are fp32;
  * the weights p_t r_t enter their product in fp16 (two terms for fp32 queries), and
  * value rows with r below 2^-60 may count as zeros.  Results do not depend on
  * timing.  workspace: stepq_kv_attend_workspace_bytes (of the same arguments) bytes,

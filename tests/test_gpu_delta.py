@@ -343,3 +343,40 @@ def test_prefill_zero_beta_leaves_the_state(stepq):
     assert torch.equal(S, before)
     ref = torch.einsum("thi,hij->thj", x["q"].double(), before[0].double())
     assert ((x["o"].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -6 * 2).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefill_not_finite_tokens_stay_in_their_head(stepq, dtype, bad):
+    """One infinite or NaN token: in v, its head's column from its chunk on; in k, the heads that share it; in q, its own
+    output row.  Everything else is bit for bit what it is without."""
+    H, Hk, D, T = 4, 2, 128, 200
+    ctx = _ctx(stepq, H, D, 1)
+    cu = torch.tensor([0, T, T + 30], dtype=torch.int32, device="cuda")
+    S0 = torch.randn(2, H, D, D, device="cuda")
+
+    def run(change):
+        x = _inputs(12, T + 30, H, Hk, D, dtype)
+        change(x)
+        S = S0.clone()
+        ctx.delta_prefill(S, None, cu, x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["o"])
+        ctx.sync()
+        return S, x["o"]
+
+    S, o = run(lambda x: None)
+    Sv, ov = run(lambda x: x["v"][100, 1].__setitem__(5, bad))
+    same = torch.ones_like(o, dtype=torch.bool)
+    same[64:T, 1, 5] = False
+    assert torch.equal(ov[same], o[same]) and not torch.isfinite(ov[100:T, 1, 5]).any()
+    same = torch.ones_like(S, dtype=torch.bool)
+    same[0, 1, :, 5] = False
+    assert torch.equal(Sv[same], S[same]) and not torch.isfinite(Sv[0, 1, :, 5]).all()
+    Sk, ok = run(lambda x: x["k"][100, 1].__setitem__(5, bad))
+    same = torch.ones_like(o, dtype=torch.bool)
+    same[64:T, 2:] = False
+    assert torch.equal(ok[same], o[same]) and not torch.isfinite(ok[100, 2:]).any()
+    assert torch.equal(Sk[0, :2], S[0, :2]) and torch.equal(Sk[1], S[1])
+    Sq, oq = run(lambda x: x["q"][100, 0].__setitem__(5, bad))
+    same = torch.ones_like(o, dtype=torch.bool)
+    same[100, :2] = False
+    assert torch.equal(oq[same], o[same]) and torch.equal(Sq, S) and not torch.isfinite(oq[100, :2]).any()
