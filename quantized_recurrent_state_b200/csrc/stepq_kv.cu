@@ -5,11 +5,11 @@
 // type), one in each half, so d / 16 lanes share a row, a place or page and a scale are looked up once for 16 values, and the
 // row's maximum is log2(d / 16) shuffles.  A block works on the keys or the values
 // of one head; the heads of the same tokens are neighbouring blocks, whose rows lie side by side outside the cache.
-// Bytes in flight hide the latency.  Writing: one row a thread and many threads (6,144 tokens, 8 heads of 128, 8 bits, bf16: 15.4 us,
+// Bytes in flight hide the latency.  Writing: one row a thread and many threads (6,144 tokens, 8 heads of 128, 8 bits, bf16: 15.2 us,
 // 38 MB; two and four rows, whose registers leave fewer warps, 16.4 and 23 us).  Reading, where a row is 16 bytes a
-// thread behind three dependent loads: eight rows at once (31,000 such tokens: 46 us, 192 MB, 4.2 TB/s; four and two rows 47 and
-// 66 us).  Bound by those latencies and HBM at large sizes, by the launch at small ones (70 tokens of 4 heads of 64 written: 2.3 us;
-// 70 sequences of up to 300 read: 7.2 us, four rows 8.9).
+// thread behind three dependent loads: eight rows at once (31,000 such tokens: 45 us, 192 MB, 4.3 TB/s; with 256 threads a block 46 us, and four and two rows
+// 47 and 66 us; 512 threads 52 us).  Bound by those latencies and HBM at large sizes, by the launch at small ones (70 tokens of 4 heads of 64 written: 2.1 us;
+// 70 sequences of up to 300 read: 7.4 us, four rows 8.9).
 #include <float.h>
 
 #include "stepq_delta.cuh"
@@ -20,7 +20,7 @@ namespace stepq {
 
 namespace {
 
-constexpr int kThreads = 256, kReadRows = 8;
+constexpr int kThreads = 128, kReadRows = 8;
 
 template <int D, int BITS, class T>
 __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
