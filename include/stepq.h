@@ -341,7 +341,8 @@ int stepq_delta_prefill(stepq_ctx *ctx, int layer, float *S, const int32_t *slot
 
 /* Order the context's main stream after the work enqueued so far on a
  * stream of the caller (a cudaStream_t on the context's device), and the
- * other way round. */
+ * other way round.  These two and the two calls above may come from several host threads (whose
+ * calls share `main` and must not share states in use). */
 int stepq_ctx_wait_stream(stepq_ctx *ctx, void *stream);
 int stepq_stream_wait_ctx(stepq_ctx *ctx, void *stream);
 

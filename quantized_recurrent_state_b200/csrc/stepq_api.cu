@@ -640,6 +640,7 @@ struct stepq_ctx {
     std::vector<cudaEvent_t> dec_done;   // per chunk index
     cudaEvent_t ev_main = nullptr, ev_side = nullptr;
     cudaEvent_t ev_join = nullptr;  // orders main and a caller's stream
+    std::mutex join_mu;             // from its record to its wait
     int *err = nullptr;
     void *tables_mem = nullptr;
     stepq::Tables t{};
@@ -1234,6 +1235,7 @@ static int join_streams(stepq_ctx *c, void *stream, bool main_waits) {
     if (other == c->main) return STEPQ_OK;
     const stepq::DeviceScope dev(c->device);
     cudaError_t e = dev.error();
+    const std::lock_guard<std::mutex> hold(c->join_mu);
     if (e == cudaSuccess) e = cudaEventRecord(c->ev_join, main_waits ? other : c->main);
     if (e == cudaSuccess) e = cudaStreamWaitEvent(main_waits ? c->main : other, c->ev_join, 0);
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "stream join");

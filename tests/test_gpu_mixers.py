@@ -147,3 +147,38 @@ def test_two_caches_and_contexts_at_once(stepq):
         res.append([t.clone() for job in jobs for t in (job[7], job[10]["o"], job[11])])
     for a, b in zip(*res):
         assert torch.equal(a, b)
+
+
+def test_one_context_from_two_threads(stepq):
+    """Two host threads with a stream each step states of their own through one context: what a thread enqueues before its
+    call is seen by it, whatever the other does in between."""
+    import threading
+    ctx = stepq.Context(stepq.Plan.build_uniform(0, 1, H, D, 6), 1)
+    steps = 150
+
+    def run(parallel):
+        S = [torch.zeros(2, H, D, D, device="cuda") for _ in range(2)]
+        x = [_tokens(20 + j, 2, torch.float32) for j in range(2)]
+        out = [torch.zeros(steps, 2, 1, H, D, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+
+        def work(j):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                y = {n: t.unsqueeze(1) for n, t in x[j].items() if n in "qkv"}
+                for i in range(steps):
+                    y["v"].mul_(-0.9375).add_(0.125 * j)
+                    ctx.delta_step(S[j], None, y["q"], y["k"], y["v"], x[j]["alpha"], x[j]["beta"], out[j][i])
+                torch.cuda.current_stream().synchronize()
+
+        threads = [threading.Thread(target=work, args=(j,)) for j in range(2)]
+        for t in threads:
+            t.start()
+            if not parallel:
+                t.join()
+        for t in threads:
+            t.join()
+        ctx.sync()
+        return S + out
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
