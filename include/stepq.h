@@ -351,9 +351,10 @@ int stepq_stream_wait_ctx(stepq_ctx *ctx, void *stream);
  * delta-rule layers, quantised as it is written with the per-row
  * absmax quantizer of STEPQ_QUANT_ABSMAX, a row being one token's key (or value)
  * of one head:
- *   r = fl(max_j |x_j| / qmax), 1 where that is below 2^-126 (a row of zeros);
+ *   r = fl(max_j |x_j| / qmax), 0 where that is below 2^-126 (a row of zeros,
+ *   which the state's quantizer gives 1);
  *   z_j = nearest integer, ties to even, to the exact x_j * fl(1/r), in
- *   [-qmax, qmax]; it reads back as fl(r z_j), rounded to the type asked for.
+ *   [-qmax, qmax], 0 where r is 0; it reads back as fl(r z_j), rounded to the type asked for.
  *   A row that holds an infinity or NaN gets r = NaN and reads back as NaN.
  * qmax = 127 (8 bits) or 7 (4 bits).  Codes are offset-binary (z + 128, or
  * z + 8 with element 2m in the low half of byte m).
@@ -400,8 +401,9 @@ int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const int32_t *pag
  * lse (fp32 [n_seq][n_tok][n_q_heads], or NULL) receives the logarithm of
  * sum_t exp(scale q.k_t).  A token that sees nothing gets o = 0 and lse =
  * -infinity.  o overlaps no input.  scale is finite and above 0.  Sums and softmax statistics are fp32;
- * the weights p_t r_t enter their product in fp16 (two terms for fp32 queries), and
- * value rows with r below 2^-60 may count as zeros.  Results do not depend on
+ * the weights p_t r_t enter their product in fp16 (two terms for fp32 queries), which ends
+ * at 2^-25 of the largest p_t max(r_t, 2^-60): value rows with r below 2^-60 may count as zeros, rows of
+ * zeros (r = 0) take nothing from the others.  Results do not depend on
  * timing.  workspace: stepq_kv_attend_workspace_bytes (of the same arguments) bytes,
  * 16-byte aligned, used by one call at a time (two captured graphs that may run
  * at the same time need one each). */

@@ -52,9 +52,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
         return;
     }
     const bool finite = m < 0x7f800000;
+    // a row of zeros has the scale 0: it reads back the same as under any other, and attention must not take it for a large one
     float r = __int_as_float(m) / (float)QMAX;
-    if (!(r >= FLT_MIN)) r = 1.0f;
-    const float inv = 1.0f / r;
+    if (r < FLT_MIN) r = 0.0f;
+    const float inv = r > 0.0f ? 1.0f / r : 0.0f;
     const int64_t page = place < (1 << 30) ? (int64_t)(__umulhi((uint32_t)place, a.div_mul) >> a.div_shift)
                                            : place / g.page_tokens;
     const int at = (int)(place - page * g.page_tokens);

@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) G::V::template load<8>(vr + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
         }
-        // log2 of the weights against the reference: the score less it; log2 r_v on top of that may not pass the slack
+        // log2 of the weights against the reference: the score less it; log2 r_v on top of that may not pass the slack.  A row of
+        // zeros (r_v = 0) and one marked NaN count as the smallest, so that they do not move the others' weights down.
         const float lr[2] = {fmaxf(lg2(rv[0]), -60.0f), fmaxf(lg2(rv[1]), -60.0f)};
         const float room[2] = {kSlack - lr[0], kSlack - lr[1]};
         bool far = false;

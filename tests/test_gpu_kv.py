@@ -376,3 +376,52 @@ def test_captured(stepq):
     graph.replay()
     k[[299, 339]], v[[299, 339]] = k1, v1
     _check_attend(s, q, o, None, k, v, 128 ** -0.5)
+
+
+def _exact_rows(s, q, k, v, i, t, scale):
+    """Sequence i, query token t, from the values that the cache holds in 64 bits: softmax weights, value rows, output and
+    the bound of a score's error."""
+    kd, vd = (r.double().unsqueeze(-1) * z.double() for z, r in (_quantise(x, s.bits) for x in (k, v)))
+    m = s.lens_list[i] - q.shape[1] + 1 + t
+    sl, rep = slice(s.cu_list[i], s.cu_list[i] + m), q.shape[2] // s.H
+    kk, vv = (x[sl].repeat_interleave(rep, 1) for x in (kd, vd))
+    qq = q[i, t].double()
+    sc = torch.einsum("hd,mhd->hm", qq, kk) * scale
+    p = torch.softmax(sc, -1)
+    ds = scale * (q.shape[3] + 2) * 2.0 ** -23 * torch.einsum("hd,mhd->hm", qq.abs(), kk.abs()).amax(-1)
+    return p, vv, torch.einsum("hm,mhd->hd", p, vv), ds + 2.0 ** -22 + 2.0 ** -23 * sc.abs().amax(-1)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype, size", [("fp32", 1e-3), ("fp32", 1e-7), ("fp16", 1e-3), ("bf16", 1e-7)])
+@pytest.mark.parametrize("sink", [False, True])
+def test_attend_zero_value_rows(stepq, bits, dtype, size, sink):
+    """Value rows of zeros (padding, a first token that only takes weight) add nothing, and take no bits from the others.
+    A weight's error is that of its type, or 2^-25 of the largest weight times scale among the rows that are not zero."""
+    d, lens = 64, [130, 70]
+    s = Seqs(stepq, lens, bits, 2, d, 16)
+    k, v = _randn(50, s.total, 2, d), _randn(51, s.total, 2, d) * size
+    zero = [0, 17, 63, 130, 131]
+    v[zero] = 0.0
+    base = _randn(52, 1, 1, 2, d)
+    q = (base.repeat_interleave(2, 2) + 0.01 * _randn(53, 2, 1, 4, d)).to(TYPES[dtype])
+    if sink:                                             # about 18 in base 2 above the other scores
+        k[[0, 130]] = base[0] * (12.5 * d ** 0.5 / base[0].square().sum(-1, keepdim=True))
+    s.fill(k, v)
+    got = s.read(torch.float32)[1]
+    assert (got[zero] == 0).all()
+    o, l = _attend(s, q)
+    _check_attend(s, q, o, l, k, v, d ** -0.5)
+    wt = 2.0 ** -22 if dtype == "fp32" else 2.0 ** -11
+    rv = _quantise(v, bits)[1].double()
+    rv[zero] = 0.0
+    for i in range(2):
+        p, vv, ref, ds = _exact_rows(s, q, k, v, i, 0, d ** -0.5)
+        m = p.shape[1]
+        r = rv[s.cu_list[i]:s.cu_list[i] + m].repeat_interleave(2, 1)
+        mean = torch.einsum("hm,mhd->hd", p, vv.abs())
+        floor = m * 2.0 ** -25 * (2 ** (bits - 1) - 1) * (p.transpose(0, 1) * r).amax(0)
+        bound = (2 * torch.expm1(ds).unsqueeze(-1) + wt + m * 2.0 ** -23) * mean + floor.unsqueeze(-1)
+        bound = bound + torch.finfo(TYPES[dtype]).eps / 2 * (ref.abs() + bound) + 2.0 ** -25 * (dtype == "fp16")
+        err = (o[i, 0].double() - ref).abs()
+        assert (err <= bound).all(), (i, (err / bound).max().item())
