@@ -401,9 +401,9 @@ int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const int32_t *pag
  * lse (fp32 [n_seq][n_tok][n_q_heads], or NULL) receives the logarithm of
  * sum_t exp(scale q.k_t).  A token that sees nothing gets o = 0 and lse =
  * -infinity.  o overlaps no input.  scale is finite and above 0.  Sums and softmax statistics are fp32;
- * the weights p_t r_t enter their product in fp16 (two terms for fp32 queries), which ends
- * at 2^-25 of the largest p_t max(r_t, 2^-60): value rows with r below 2^-60 may count as zeros, rows of
- * zeros (r = 0) take nothing from the others.  Results do not depend on
+ * the weights p_t r_t enter their product in fp16 (2^-11 of themselves, or 2^-32 of the
+ * largest p_t max(r_t, 2^-60)), for fp32 queries in two terms (2^-22, or 2^-42 of the largest): value rows with r
+ * below 2^-60 may count as zeros, rows of zeros (r = 0) take nothing from the others.  Results do not depend on
  * timing.  workspace: stepq_kv_attend_workspace_bytes (of the same arguments) bytes,
  * 16-byte aligned, used by one call at a time (two captured graphs that may run
  * at the same time need one each). */

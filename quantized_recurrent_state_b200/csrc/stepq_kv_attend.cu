@@ -18,10 +18,12 @@
 // the products: r_k multiplies the score, r_v the weight.
 //
 // The weight p r_v has to fit fp16, whatever r_v is, so the running reference of a row
-// is the largest s + log2 r_v instead of the largest s (lr below).  It moves only
-// when a weight would exceed 2^8: sums are fp32, and 2^8 leaves fp16 room; a move costs
-// three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry 2^-12 of
-// themselves as rounding error; fp32 outputs take them (and q) as sums of two fp16 values.
+// is the largest s + log2 r_v instead of the largest s (lr below).  The reference's weight is 2^7, and it moves only
+// when a weight would exceed 2^15: sums are fp32; a move costs
+// three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry up to 2^-11 of
+// themselves as rounding error, or 2^-32 of the reference's where that is more (fp16 ends at 2^-25); fp32 outputs take them as
+// sums of two fp16 values, the second held 2^11 times as large (2^-22 of the weight, or 2^-43 of the reference's), and q likewise
+// without that factor (2^-22 of a value, or 2^-39 of the row's largest).
 //
 // Work is cut evenly: all stages of 64 tokens of all (sequence, cache head, tile of rows) units lie in one line, and block i of
 // as many as the GPU holds at once takes the i-th piece of it, whatever the lengths are (they are on the device, and each
@@ -51,7 +53,10 @@ namespace {
 constexpr int kWarps = 4, kTile = 16, kMaxBlocks = 1024;
 constexpr int kStep = kWarps * kTile;    // tokens of a stage
 constexpr uint32_t kPolls = 1u << 22;
-constexpr float kSlack = 8.0f;           // log2 of the largest weight
+// log2 of the largest weight, and of the reference's: fp16 ends at 2^16 above and 2^-25 below, so a weight is lost 2^32 below the
+// reference's, and the reference moves when a weight is 2^8 of it
+constexpr float kSlack = 15.0f, kLift = 7.0f;
+constexpr int kLiftQ = 15;               // the queries' largest value is below 2^15: their small values stay above fp16's end, too
 constexpr float kNone = -1e30f;          // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -212,8 +217,10 @@ __device__ __forceinline__ void put_out(const KvAttendArgs &a, int64_t at, float
 }
 __device__ __forceinline__ void bar_workers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
+// Blocks an SM that the compiler is held to with two terms, whose independent sums it would otherwise run side by side in the
+// registers of a block: those of one term have as many without being told.
 template <int BITS, int D, int NR, int TERMS>
-__global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) {
+__global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 256 ? 1 : NR * D > 128 ? 2 : NR * D > 64 ? 3 : 4) k_kv_attend(KvAttendArgs a) {
     using G = Geo<BITS, D, NR>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *const ring = smem;                                                 // [STAGES] stages
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
     const int h = at.unit / a.row_tiles, r0 = at.unit % a.row_tiles * G::R, nrow = min(G::R, rows - r0);
     const int begin = at.first * kStep, end = min(len, (at.first + n) * kStep);
 
-    // q rows as fp16 fragments, scaled by a power of two to below 1
+    // q rows as fp16 fragments, scaled by a power of two to below 2^kLiftQ
     constexpr int QR = G::R / kWarps;
     float qx[QR][D / 32];
 #pragma unroll
@@ -347,6 +354,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
         for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
         int ex = 0;
         if (m > 0.0f && m <= FLT_MAX) frexpf(m, &ex);
+        ex -= kLiftQ;
         // 2^-ex in two factors, each of which is a normal number
         const int e1 = ex / 2, e2 = ex - e1;
         const float f1 = ldexpf(1.0f, -e1), f2 = ldexpf(1.0f, -e2);
@@ -483,6 +491,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                 // by how much the reference moves: down only while there are no sums (a row that sees nothing in its first
                 // tile sees nothing at all)
+                m -= kLift;
                 const float by = first ? (m == -INFINITY ? 0.0f : m) : fmaxf(m, 0.0f), f = first ? 1.0f : ex2(-by);
                 ref[j] += by;
                 sc[j / 2][j & 1] -= by;
@@ -512,15 +521,29 @@ __global__ void __launch_bounds__(32 * kWarps + 32) k_kv_attend(KvAttendArgs a) 
                 pb[0][nr][i] = transpose8(bits_of(hi));
                 if constexpr (TERMS == 2) {
                     const float2 back = __half22float2(hi);
-                    pb[1][nr][i] = transpose8(bits_of(__floats2half2_rn(wgt[0] - back.x, wgt[1] - back.y)));
+                    pb[1][nr][i] = transpose8(bits_of(__floats2half2_rn((wgt[0] - back.x) * 2048.0f, (wgt[1] - back.y) * 2048.0f)));
                 }
             }
-        // sums
+        // sums; the weights' second terms are 2^11 times what they stand for, their codes 2^-11 (exact).  The instruction cuts off
+        // what it adds to a larger sum, so for fp32 a tile is summed by itself and added rounded (2 to 9 %: 16 requests of 20,000 tokens, two
+        // heads of 256, 8 bits, 88 us for 84; d = 128 52.5 for 51).
         auto add = [&](int mt, const uint32_t (&f)[4]) {
+            if constexpr (TERMS == 1) {
 #pragma unroll
-            for (int p = 0; p < TERMS; ++p)
+                for (int nr = 0; nr < NR; ++nr) mma16816(acc[mt][nr], f, pb[0][nr][0], pb[0][nr][1]);
+            } else {
+                uint32_t g[4];
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) mma16816(acc[mt][nr], f, pb[p][nr][0], pb[p][nr][1]);
+                for (int i = 0; i < 4; ++i) g[i] = bits_of(__hmul2(half2_of(f[i]), half2_of(0x10001000u)));
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816(x, f, pb[0][nr][0], pb[0][nr][1]);
+                    mma16816(x, g, pb[1][nr][0], pb[1][nr][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[mt][nr][e] += x[e];
+                }
+            }
         };
 #pragma unroll
         for (int w = 0; w < G::V::W; ++w) {

@@ -425,3 +425,45 @@ def test_attend_zero_value_rows(stepq, bits, dtype, size, sink):
         bound = bound + torch.finfo(TYPES[dtype]).eps / 2 * (ref.abs() + bound) + 2.0 ** -25 * (dtype == "fp16")
         err = (o[i, 0].double() - ref).abs()
         assert (err <= bound).all(), (i, (err / bound).max().item())
+
+
+def test_attend_many_small_weights_beside_a_large_one(stepq):
+    """fp32 queries: 8,191 tokens of 2^-25.5 of the first one's weight each, all in one block's share.  The scores are single
+    products; a warp adds 128 tiles, the block 4 warps.  |do| <= sum p |v - o| 2 (e^ds - 1) + (weights 2^-22, sums) sum p |v|."""
+    n, d, H, copies = 8192, 64, 8, 64
+    s = Seqs(stepq, [n], 8, H, d, 64)
+    k, v = torch.zeros(n, H, d, device="cuda"), torch.full((n, H, d), -1.0, device="cuda")
+    k[0, :, 0] = 1.0
+    k[1:, :, 1] = 1.0
+    v[0] = 1.0
+    s.fill(k, v)
+    s.table, s.lens, s.max_pages = s.table.expand(copies, -1).contiguous(), s.lens.expand(copies).contiguous(), s.table.shape[1]
+    q = torch.zeros(copies, 1, H, d, device="cuda")
+    q[..., 0] = 25.5 * math.log(2.0) * d ** 0.5
+    o, _ = _attend(s, q)
+    p, vv, ref, ds = _exact_rows(s, q, k, v, 0, 0, d ** -0.5)
+    away = torch.einsum("hm,mhd->hd", p, (vv - ref).abs())
+    bound = 2 * torch.expm1(ds).unsqueeze(-1) * away + (2.0 ** -22 + (128 + 4 + 2) * 2.0 ** -24) * torch.einsum("hm,mhd->hd", p, vv.abs())
+    err = (o[:, 0].double() - ref).abs()
+    assert (err <= bound).all(), (err.max().item(), bound.max().item())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_attend_query_channel_that_stands_out(stepq, dtype):
+    """One channel of q is 2^14 times the others and meets keys that are 0 there: the others' products count in full."""
+    n, d = 300, 64
+    s = Seqs(stepq, [n], 8, 1, d, 32)
+    k, v = _randn(54, n, 1, d), _randn(55, n, 1, d)
+    k[..., 5] = 0.0
+    s.fill(k, v)
+    q = _randn(56, 1, 1, 4, d) * 2
+    q[..., 5] = 2.0 ** 14
+    q = q.to(TYPES[dtype])
+    o, l = _attend(s, q)
+    p, vv, ref, ds = _exact_rows(s, q, k, v, 0, 0, d ** -0.5)
+    wt = 2.0 ** -22 if dtype == "fp32" else 2.0 ** -11
+    mean = torch.einsum("hm,mhd->hd", p, vv.abs())
+    bound = (2 * torch.expm1(ds).unsqueeze(-1) + wt + n * 2.0 ** -23) * mean
+    bound = bound + torch.finfo(TYPES[dtype]).eps / 2 * (ref.abs() + bound) + 2.0 ** -25 * (dtype == "fp16")
+    err = (o[0, 0].double() - ref).abs()
+    assert (err <= bound).all(), (err / bound).max().item()
