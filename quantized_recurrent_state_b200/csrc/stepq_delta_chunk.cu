@@ -10,9 +10,9 @@
 //   S  <- gamma_C S + K'^T diag(gamma_C / gamma) U'
 // Every Gamma is at most 1, so nothing overflows however fast a gate decays.
 //
-// Precision: q' and k' are exact fp16 operands (bfloat16 tokens: to 2^-25 of the row's largest value).  fp32
-// operands (S, R, U', X) enter as the sum of two fp16 values, 2^-22 of the value: each value column's S, and its R and U',
-// are scaled by a power of two taken from an upper bound, which may be 2^13 too large before a bit is
+// Precision: q' and k' are exact fp16 operands (bfloat16 tokens: to 2^-25 of the row's largest value).  Gates are multiplied
+// up in fp32, 64 of them at most.  fp32 operands (S, R, U', X) enter as the sum of two fp16 values, 2^-22 of the value: each value
+// column's S, and its R and U', are scaled by a power of two taken from an upper bound, which may be 2^13 too large before a bit is
 // lost.  Accumulators are fp32, S is held in fp32.  The readout uses the leading terms alone for bfloat16
 // outputs (2^-12 of a term against their own 2^-9) and both terms for fp16.  X stays below 2^5 while beta |k|^2 <= 2, where the recurrence
 // does not grow; a chunk whose X or U' leaves fp16 sets kErrRange.
@@ -74,8 +74,8 @@ struct Smem {
     alignas(16) float gk[2][C], bk[2][C];      // gamma ks, beta ks
     alignas(16) float f[2][C];                 // gamma_C / gamma
     alignas(16) float go[2][C], qs[2][C];      // gamma qs, qs
-    alignas(16) float ks[2][C], lg[2][C];      // by group: ks, log2 gamma
-    alignas(16) float be[2][C], e2[2][C];      // beta ks^2; gamma at the end of the block of 16 over gamma
+    alignas(16) float ks[2][C], be[2][C];      // by group: ks, beta ks^2
+    alignas(16) float al[2][C], up[2][C], down[2][C];   // the gate; the product of its half chunk's up to it, and after it
     float gl[2], mb[2], mg[2];                 // gamma_C, the largest beta ks, the largest gamma ks
     float smx[2][D], vmx[2][D], umx[2][D];     // largest |S|, |v|, |u'| of a lane, by half
     float ss[2][D], sr[2][D];                  // a lane's scales of the S and R terms
@@ -93,11 +93,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 // 16 bytes of global memory into shared memory, or zeros.
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_addr(dst)), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 pair_of(const uint32_t *v, int i) {
@@ -442,12 +437,12 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
         const int r0 = p >> 4, i8 = p & 15;                                          // 16 lanes to a row: rows r0 + 8 i
         const T *gq = static_cast<const T *>(a.q) + (size_t)hk * D, *gk = static_cast<const T *>(a.k) + (size_t)hk * D;
         const T *gv = static_cast<const T *>(a.v) + (size_t)h * D;
-        float *const n = sm.n[gp], *const ks = sm.ks[gp], *const lg = sm.lg[gp], *const be = sm.be[gp], *const e2 = sm.e2[gp];
+        float *const n = sm.n[gp], *const ks = sm.ks[gp], *const be = sm.be[gp], *const gate = sm.al[gp], *const up = sm.up[gp], *const down = sm.down[gp];
         bool gates_ok = true;
-        // warp 3: a chunk's gates, two tokens a lane: base-2 logarithms of the running products in the chunk, and from them
-        // gamma, gamma_C / gamma, and gamma at the end of the token's block of 16 over gamma
-        float al[2] = {1.0f, 1.0f}, bt[2] = {0.0f, 0.0f}, lgt[2], total = 0.0f;
-        float2 gam, fin, blk;
+        // warp 3: a chunk's gates, two tokens a lane, 16 lanes a half: gamma and gamma_C / gamma, products of the gates up to
+        // and after a token
+        float al[2] = {1.0f, 1.0f}, bt[2] = {0.0f, 0.0f}, total = 1.0f;
+        float2 gam, fin;
         auto load_gates = [&](int c) {
             if (pw == 3) {
 #pragma unroll
@@ -460,20 +455,25 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
         };
         auto running = [&]() {
             gates_ok = gates_ok && al[0] > 0.0f && al[0] <= 1.0f && al[1] > 0.0f && al[1] <= 1.0f;
-            const float l1 = log2f(al[1]);
-            float sum = log2f(al[0]) + l1;
+            float p = al[0] * al[1], q = p;
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, sum, m);
-                if (lane >= m) sum += y;
+            for (int m = 1; m < 16; m <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, p, m, 16), z = __shfl_down_sync(0xffffffffu, q, m, 16);
+                if ((lane & 15) >= m) p *= y;
+                if ((lane & 15) + m < 16) q *= z;
             }
-            total = __shfl_sync(0xffffffffu, sum, 31);
-            const float block = __shfl_sync(0xffffffffu, sum, lane | 7);
-            lgt[0] = sum - l1;
-            lgt[1] = sum;
-            gam = make_float2(exp2f(lgt[0]), exp2f(lgt[1]));
-            fin = make_float2(exp2f(total - lgt[0]), exp2f(total - lgt[1]));
-            blk = make_float2(exp2f(block - lgt[0]), exp2f(block - lgt[1]));
+            float before = __shfl_up_sync(0xffffffffu, p, 1, 16), after = __shfl_down_sync(0xffffffffu, q, 1, 16);
+            if ((lane & 15) == 0) before = 1.0f;
+            if ((lane & 15) == 15) after = 1.0f;
+            const float h0 = __shfl_sync(0xffffffffu, p, 15), h1 = __shfl_sync(0xffffffffu, p, 31);
+            const float2 u = make_float2(before * al[0], p), w = make_float2(al[1] * after, after);
+            total = h0 * h1;
+            gam = lane < 16 ? u : mul2(u, both(h0));
+            fin = lane < 16 ? mul2(w, both(h1)) : w;
+            // the group is done with its last chunk's
+            *reinterpret_cast<float2 *>(&gate[2 * lane]) = make_float2(al[0], al[1]);
+            *reinterpret_cast<float2 *>(&up[2 * lane]) = u;
+            *reinterpret_cast<float2 *>(&down[2 * lane]) = w;
         };
         // K and Q rows as they are into their operand places (16-bit types all), zeros behind the last token; 64 rows keep
         // a row's place in its group of eight
@@ -628,9 +628,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 const float2 kk = *reinterpret_cast<const float2 *>(&ks[2 * lane]);
                 const float2 qq = *reinterpret_cast<const float2 *>(&sm.qs[b][2 * lane]);
                 const float2 gkk = mul2(gam, kk), bkk = mul2(bb, kk);
-                *reinterpret_cast<float2 *>(&lg[2 * lane]) = make_float2(lgt[0], lgt[1]);
                 *reinterpret_cast<float2 *>(&be[2 * lane]) = mul2(bkk, kk);
-                *reinterpret_cast<float2 *>(&e2[2 * lane]) = blk;
                 *reinterpret_cast<float2 *>(&sm.gk[b][2 * lane]) = gkk;
                 *reinterpret_cast<float2 *>(&sm.bk[b][2 * lane]) = bkk;
                 *reinterpret_cast<float2 *>(&sm.f[b][2 * lane]) = fin;
@@ -642,7 +640,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                     mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, w));
                 }
                 if (lane == 0) {
-                    sm.gl[b] = exp2f(total);
+                    sm.gl[b] = total;
                     sm.mb[b] = mb;
                     sm.mg[b] = mg;
                 }
@@ -660,12 +658,14 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             }
             ok = warp_wait(&sm.full[b], ph2) && warp_wait(&sm.g[gp], ph2);
             tc::fence_after();
-            // A row of Gamma o [K; Q] K^T a lane.  Right of the diagonal: N is not read there, A is 0.  Columns of an
-            // earlier block of 16: Gamma_ts as gamma_t over gamma at that block's end, times e2_s, each at most 1.
+            // A row of Gamma o [K; Q] K^T a lane.  Right of the diagonal: N is not read there, A is 0.  Gamma_ts is the product of
+            // the gates between, column after column to the left of the diagonal (at most 32 roundings, whatever gates came
+            // before; the difference of logarithms of gamma loses what a run of strong gates adds to both); over the
+            // middle of the chunk, up_t down_s, each at most 1.
             {
                 const int t = (32 * pw + lane) & 63;
                 const bool is_n = pw < 2;
-                const float lt = lg[t], row = is_n ? be[t] : 1.0f;
+                const float row = is_n ? be[t] : 1.0f;
 #pragma unroll 1
                 for (int s0 = 0; s0 < C; s0 += 32) {
                     if (s0 > 0 && !(pw & 1)) {     // right of the diagonal for every row of the warp
@@ -681,19 +681,26 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                     uint32_t g[32];
                     tc::ld32(quad + TG + C * gp + s0, g);
                     float2 x[16];
-                    if (s0 == 0 && (pw & 1)) {     // earlier blocks for every row of the warp
-                        const float2 far[2] = {both(row * ex2(lt - lg[15])), both(row * ex2(lt - lg[31]))};
+                    if (s0 == 0 && (pw & 1)) {     // the first half for every row of the second
+                        const float2 far = both(row * up[t]);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            x[i] = mul2(mul2(far[i >> 3], *reinterpret_cast<const float2 *>(&e2[2 * i])), pair_of(g, i));
+                            x[i] = mul2(mul2(far, *reinterpret_cast<const float2 *>(&down[2 * i])), pair_of(g, i));
                     } else {
+                        float y = row;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 ls = *reinterpret_cast<const float2 *>(&lg[s0 + 2 * i]);
-                            const float2 y = make_float2(ex2(lt - ls.x), ex2(lt - ls.y));   // right of the diagonal: anything
-                            x[i] = mul2(is_n ? mul2(both(row), y) : y, pair_of(g, i));
-                            if (s0 + 2 * i > t) x[i].x = 0.0f;
-                            if (s0 + 2 * i + 1 > t) x[i].y = 0.0f;
+                        for (int i = 15; i >= 0; --i) {
+                            const float2 a2 = *reinterpret_cast<const float2 *>(&gate[s0 + 2 * i]);
+                            float2 w = make_float2(0.0f, 0.0f);
+                            if (s0 + 2 * i + 1 <= t) {
+                                w.y = y;
+                                y *= a2.y;
+                            }
+                            if (s0 + 2 * i <= t) {
+                                w.x = y;
+                                y *= a2.x;
+                            }
+                            x[i] = mul2(w, pair_of(g, i));
                         }
                     }
                     if (is_n) {

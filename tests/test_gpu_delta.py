@@ -380,3 +380,27 @@ def test_prefill_not_finite_tokens_stay_in_their_head(stepq, dtype, bad):
     same = torch.ones_like(o, dtype=torch.bool)
     same[100, :2] = False
     assert torch.equal(oq[same], o[same]) and torch.equal(Sq, S) and not torch.isfinite(oq[100, :2]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("strong, gate", [(20, 1e-30), (32, 1e-30), (50, 1e-38), (3, 1e-20)])
+@pytest.mark.parametrize("same_key", [False, True])
+def test_prefill_gentle_gates_after_strong_ones(stepq, strong, gate, dtype, same_key):
+    """A run of gates that forget everything, then gates of 0.6 to 1 in the same chunk: the decays between later tokens keep
+    their bits.  Keys are unit vectors, so a row of S is a scalar recurrence: decays within 2^-21 (exponential and
+    logarithms), operands 2^-22, at most 64 additions of at most the largest value (2^-18): 2^-17 of it together."""
+    T, H, D = 64, 2, 128
+    ctx = _ctx(stepq, H, D, 1)
+    x = _inputs(13, T, H, 1, D, dtype)
+    x["alpha"].copy_(0.6 + 0.4 * torch.rand(T, H, generator=torch.Generator(device="cuda").manual_seed(14), device="cuda"))
+    x["alpha"][:strong] = gate
+    x["k"].zero_()
+    x["k"][torch.arange(T), 0, 0 if same_key else torch.arange(T)] = 1.0
+    S = torch.randn(1, H, D, D, device="cuda")
+    R, o, C = _reference(S[0].double(), x, False)
+    ctx.delta_prefill(S, None, torch.tensor([0, T], dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"], x["alpha"],
+                      x["beta"], x["o"])
+    ctx.sync()
+    err, top = (S[0].double() - R).abs().max().item(), x["v"].abs().max().item()
+    assert err <= 2.0 ** -17 * top, err / top
+    _check(S[0], x["o"], R, o, C, T, D, dtype, x["q"], chunked=True)
