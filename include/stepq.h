@@ -332,8 +332,8 @@ int stepq_delta_step(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, 
  * token by token): states stay fp32, with operands as sums of two fp16
  * values under powers of two, so results match the token-by-token form to the tolerances
  * stated in the tests, not bit for bit.  The chunked form holds for beta_t |k_t|^2
- * <= 2, where the recurrence does not grow; beyond that intermediate values may leave
- * fp16, which sets the device error word ("prefill range").  An infinity or NaN in k or v reaches
+ * <= 2, where the recurrence does not grow, and for states and values up to 2^100; beyond that intermediate
+ * values may leave fp16, which sets the device error word ("prefill range"; that head's results are not valid).  An infinity or NaN in k or v reaches
  * its head's state and outputs from that token on, in the chunked form from the first token
  * of its chunk on; one in q reaches its own token's output. */
 int stepq_delta_prefill(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, const uint8_t *fresh,

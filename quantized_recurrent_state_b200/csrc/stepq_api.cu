@@ -1061,7 +1061,7 @@ extern "C" int stepq_sync(stepq_ctx *c, int timeout_ms) {
         return fail(STEPQ_EDEVICE, "device error word 0x%x (%s%s%s%s%s%s%s)", word,
                     (word & stepq::kErrBadSlot) ? "slot out of range " : "", (word & stepq::kErrWait) ? "copy wait gave up " : "",
                     (word & stepq::kErrArgs) ? "bad width " : "", (word & stepq::kErrGateRange) ? "prefill gate out of range " : "",
-                    (word & stepq::kErrRange) ? "prefill range: beta |k|^2 above 2? " : "",
+                    (word & stepq::kErrRange) ? "prefill range: beta |k|^2 above 2, or values beyond 2^100? " : "",
                     (word & stepq::kErrSeq) ? "sequence outside the batch's tokens " : "",
                     (word & stepq::kErrTmemDrain) ? "tensor memory freed with a product in flight (context now unusable) " : "");
     }

@@ -15,7 +15,8 @@
 // column's S, and its R and U', are scaled by a power of two taken from an upper bound, which may be 2^13 too large before a bit is
 // lost.  Accumulators are fp32, S is held in fp32.  The readout uses the leading terms alone for bfloat16
 // outputs (2^-12 of a term against their own 2^-9) and both terms for fp16.  X stays below 2^5 while beta |k|^2 <= 2, where the recurrence
-// does not grow; a chunk whose X or U' leaves fp16 sets kErrRange.
+// does not grow.  An operand that leaves fp16 is the sum of infinity and its opposite, which every product takes on to U' as
+// NaN; a U' beyond fp16 from tokens and a state that are numbers sets kErrRange.
 //
 // One block per (sequence, head) walks the chunks; blocks of heads that share k and q are neighbours.  The
 // chain S -> R -> U' -> S is serial, so the block is split by what it waits for:
@@ -77,6 +78,7 @@ struct Smem {
     alignas(16) float ks[2][C], be[2][C];      // by group: ks, beta ks^2
     alignas(16) float al[2][C], up[2][C], down[2][C];   // the gate; the product of its half chunk's up to it, and after it
     float gl[2], mb[2], mg[2];                 // gamma_C, the largest beta ks, the largest gamma ks
+    int finite[2];                             // the chunk's keys are numbers and its gates in range
     float smx[2][D], vmx[2][D], umx[2][D];     // largest |S|, |v|, |u'| of a lane, by half
     float ss[2][D], sr[2][D];                  // a lane's scales of the S and R terms
     alignas(8) uint64_t full[2], vfull[2], ready[2], empty[2], sput, rput, uput[2], w, u, d, z[2], out, g[2], drain[3];
@@ -108,6 +110,12 @@ __device__ __forceinline__ void scale_for(float bound, int top, float &s, float 
 __device__ __forceinline__ int exponent_of(float x) {
     const int e = (int)(__float_as_uint(x) >> 23);
     return e == 0 || e == 255 ? 127 : min(max(e, 27), 227);
+}
+// The larger of both, NaN where one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
 }
 template <class T>
 struct Pair;
@@ -233,10 +241,12 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
         for (int i = 0; i < 32; ++i) {
             S[i].x = fresh ? 0.0f : Sg[(size_t)(64 * hh + 2 * i) * D + j];
             S[i].y = fresh ? 0.0f : Sg[(size_t)(64 * hh + 2 * i + 1) * D + j];
-            smax = fmaxf(smax, fmaxf(fabsf(S[i].x), fabsf(S[i].y)));
+            smax = max_nan(smax, max_nan(fabsf(S[i].x), fabsf(S[i].y)));
         }
         sm.smx[hh][j] = smax;
         tc16::group_and(1, NS, true);
+        // what the column has taken in so far are numbers: if u' is none, it has left the range of its operands
+        bool finite = sm.smx[0][j] <= kFloatMax && sm.smx[1][j] <= kFloatMax;
         // S as operand of chunk c, and the chunk's V into registers
         auto put = [&](int c, float bound) {
             const int b = c & 1;
@@ -256,10 +266,10 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 v[i] = T2(src[2 * i * D], src[(2 * i + 1) * D]);
-                m = __hmax2(m, __habs2(v[i]));
+                m = __hmax2_nan(m, __habs2(v[i]));
             }
             const float2 mf = to_f32x2(m);
-            sm.vmx[hh][j] = fmaxf(mf.x, mf.y);
+            sm.vmx[hh][j] = max_nan(mf.x, mf.y);
             tc16::st_wait();
             tc::fence_before();
             mbar_arrive(&sm.sput);
@@ -341,6 +351,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             tc::fence_after();
             float sR;
             const float before = fmaxf(sm.smx[0][j], sm.smx[1][j]);
+            finite = finite && sm.finite[b] && sm.vmx[0][j] <= kFloatMax && sm.vmx[1][j] <= kFloatMax;
             {
                 uint32_t w[32], hi[16], lo[16];
                 tc::ld32(quad + TW + 32 * hh, w);
@@ -376,7 +387,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 x = pair_of(u, i);
-                    um = fmaxf(um, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    um = max_nan(um, max_nan(fabsf(x.x), fabsf(x.y)));
                     tc16::split2(mul2(x, *reinterpret_cast<const float2 *>(&sm.f[b][32 * hh + 2 * i])), hi[i], lo[i]);
                 }
                 tc16::st16(quad + TFH + 16 * hh, hi);
@@ -389,7 +400,7 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 tc16::st16(quad + TUH + 16 * hh, hi);
                 if constexpr (TWO) tc16::st16(quad + TUL + 16 * hh, lo);
                 sm.umx[hh][j] = um;
-                if (um > kHalfMax && um <= kFloatMax) atomicOr(a.err, kErrRange);
+                if (finite && !(um <= kHalfMax)) atomicOr(a.err, kErrRange);
                 tc16::st_wait();
             }
             tc::fence_before();
@@ -579,17 +590,17 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                 for (int i = 0; i < 8; ++i) rw[i] = *reinterpret_cast<const uint4 *>(at + (i & 1) * C * 128 + (i >> 1) * 8 * 128);
                 auto most = [](const uint4 &x) {
                     const T2 *pr = reinterpret_cast<const T2 *>(&x);
-                    return __hmax2(__hmax2(__habs2(pr[0]), __habs2(pr[1])), __hmax2(__habs2(pr[2]), __habs2(pr[3])));
+                    return __hmax2_nan(__hmax2_nan(__habs2(pr[0]), __habs2(pr[1])), __hmax2_nan(__habs2(pr[2]), __habs2(pr[3])));
                 };
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {     // (of K, of Q)
                     const T2 k = most(rw[2 * i]), q = most(rw[2 * i + 1]);
-                    m[i] = __hmax2(lows(k, q), highs(k, q));
+                    m[i] = __hmax2_nan(lows(k, q), highs(k, q));
                 }
 #pragma unroll
                 for (int w = 8; w > 0; w >>= 1)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m[i] = __hmax2(m[i], __shfl_xor_sync(0xffffffffu, m[i], w));
+                    for (int i = 0; i < 4; ++i) m[i] = __hmax2_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], w));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const T2 *pr = reinterpret_cast<const T2 *>(&rw[i]);
@@ -602,7 +613,10 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                     out.z = tc16::pack2(mul2(to_f32x2(pr[2]), inv));
                     out.w = tc16::pack2(mul2(to_f32x2(pr[3]), inv));
                     *reinterpret_cast<uint4 *>(at + (i & 1) * C * 128 + (i >> 1) * 8 * 128) = out;
-                    if (i8 == 0) (i & 1 ? sm.qs[b] : ks)[r0 + 8 * (i0 + (i >> 1))] = __uint_as_float((uint32_t)e << 23);
+                    // (a key that is not finite has the scale NaN)
+                    if (i8 == 0)
+                        (i & 1 ? sm.qs[b] : ks)[r0 + 8 * (i0 + (i >> 1))] =
+                            __uint_as_float(i & 1 || mf.x <= kFloatMax ? (uint32_t)e << 23 : 0x7fffffffu);
                 }
             }
             tc::fence_smem_to_async();
@@ -639,7 +653,9 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                     mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
                     mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, w));
                 }
+                const bool numbers = __all_sync(0xffffffffu, gates_ok && kk.x == kk.x && kk.y == kk.y);
                 if (lane == 0) {
+                    sm.finite[b] = numbers;
                     sm.gl[b] = total;
                     sm.mb[b] = mb;
                     sm.mg[b] = mg;
@@ -794,7 +810,6 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
             join(std::integral_constant<int, 32>(), std::integral_constant<int, 2>(), 0, 16 * (pw >> 1), 16 * (pw & 1));
             {   // X as operand, zeros right of the diagonal
                 const int t = p & 63, s0 = 32 * (p >> 6);
-                float m = 0.0f;
                 float4 y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = *reinterpret_cast<const float4 *>(&n[t * SN + s0 + 4 * i]);
@@ -808,14 +823,12 @@ __global__ void __launch_bounds__(NT, 1) k_delta_chunk(DeltaArgs a) {
                         const int ss = s0 + 8 * e + 2 * i;
                         if (ss > t) x.x = 0.0f;
                         if (ss + 1 > t) x.y = 0.0f;
-                        m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
                         tc16::split2(x, hi[i], lo[i]);
                     }
                     uint8_t *dst = sm.x[b] + tc16::sw_off(t, s0 + 8 * e);
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(dst + C * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                if (m > kHalfMax && m <= kFloatMax) atomicOr(a.err, kErrRange);
             }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.ready[b]);

@@ -404,3 +404,56 @@ def test_prefill_gentle_gates_after_strong_ones(stepq, strong, gate, dtype, same
     err, top = (S[0].double() - R).abs().max().item(), x["v"].abs().max().item()
     assert err <= 2.0 ** -17 * top, err / top
     _check(S[0], x["o"], R, o, C, T, D, dtype, x["q"], chunked=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("what", ["identical keys", "two large keys", "large values", "large state"])
+def test_prefill_out_of_range_is_reported(stepq, dtype, what):
+    """Intermediate values that leave fp16 are an error, never silent NaN: keys with beta |k|^2 of 3.5 throughout; two tokens in
+    different blocks of 16 that share a key of beta |k|^2 = 1e5 among orthogonal ones; a state near the end of fp32.  A value near
+    it (times its beta and the key's size it may still fit) is reported or right."""
+    if what == "large values" and dtype == "fp16":
+        pytest.skip("fp16 holds no such value")
+    T, H, D = 64, 2, 128
+    ctx = _ctx(stepq, H, D, 2)
+    x = _inputs(15, 2 * T, H, 1, D, dtype)
+    x["alpha"].fill_(1.0)
+    S = torch.zeros(2, H, D, D, device="cuda")
+    if what == "identical keys":
+        x["k"][:T] = x["k"][0] / x["k"][0].float().norm() * 3.5 ** 0.5
+        x["beta"][:T] = 1.0
+    elif what == "two large keys":
+        x["k"][:T].zero_()
+        x["k"][torch.arange(T), 0, torch.arange(T)] = 1.0
+        x["k"][20] = x["k"][0]
+        x["k"][[0, 20]] *= 1e5 ** 0.5
+        x["beta"][:T] = 1.0
+    elif what == "large values":
+        x["v"][5, 1, 7] = 3e38
+    else:
+        S[0, 1, 3, 9] = 1e38
+    args = [x[m] for m in ("q", "k", "v", "alpha", "beta", "o")]
+    cu = torch.tensor([0, T, 2 * T], dtype=torch.int32, device="cuda")
+    ctx.delta_prefill(S, None, cu, *args)
+    try:
+        ctx.sync()
+        assert what == "large values"
+        R, o, C = _reference(torch.zeros(H, D, D, dtype=torch.float64, device="cuda"), _slice(x, 0, T), False)
+        _check(S[0], x["o"][:T], R, o, C, T, D, dtype, x["q"], chunked=True)
+    except stepq.StepqError as e:
+        assert "prefill range" in str(e)
+    R, o, C = _reference(torch.zeros(H, D, D, dtype=torch.float64, device="cuda"), _slice(x, T, 2 * T), False)
+    _check(S[1], x["o"][T:], R, o, C, T, D, dtype, x["q"], chunked=True)       # the other sequence
+    for bad in ("k", "v"):                               # tokens that are not numbers are no range error
+        y = _inputs(16, 2 * T, H, 1, D, dtype)
+        y[bad][70, 0, 3] = float("nan")
+        y[bad][3, 0, 3] = float("inf")
+        S = torch.zeros(2, H, D, D, device="cuda")
+        ctx.delta_prefill(S, None, cu, *(y[m] for m in ("q", "k", "v", "alpha", "beta", "o")))
+        ctx.sync()
+        assert not torch.isfinite(S).all()
+    S[0, 0, 0, 0] = float("nan")                         # nor is a state that is not
+    S[0, 1, 0, 0] = float("inf")
+    y = _inputs(17, 2 * T, H, 1, D, dtype)
+    ctx.delta_prefill(S, None, cu, *(y[m] for m in ("q", "k", "v", "alpha", "beta", "o")))
+    ctx.sync()
