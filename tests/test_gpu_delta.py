@@ -457,3 +457,22 @@ def test_prefill_out_of_range_is_reported(stepq, dtype, what):
     y = _inputs(17, 2 * T, H, 1, D, dtype)
     ctx.delta_prefill(S, None, cu, *(y[m] for m in ("q", "k", "v", "alpha", "beta", "o")))
     ctx.sync()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_prefill_readout_on_average(stepq, dtype):
+    """The readout's root mean square error: one fp16 term of S, U and A each (bfloat16 tokens) is off by at most 2^-12 of itself,
+    two by 2^-22; a term that is lost would be of the order |q| C."""
+    T, H, D = 300, 4, 128
+    ctx = _ctx(stepq, H, D, 1)
+    x = _inputs(18, T, H, 2, D, dtype)
+    S = torch.randn(1, H, D, D, device="cuda")
+    R, o, C = _reference(S[0].double(), x, False)
+    ctx.delta_prefill(S, None, torch.tensor([0, T], dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"], x["alpha"],
+                      x["beta"], x["o"])
+    ctx.sync()
+    rms = lambda y: y.double().square().mean().sqrt().item()  # noqa: E731
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    own = (3 * 2.0 ** -12 if dtype == "bf16" else 2.0 ** -15) * x["q"].float().norm(dim=-1).max().item()
+    # errors of single terms are independent: spread over the 128 rows, on average C / sqrt(128) a value
+    assert rms(x["o"].double() - o) <= half * rms(o) + own * C / D ** 0.5
