@@ -106,10 +106,10 @@ __device__ __forceinline__ void scale_for(float bound, int top, float &s, float 
     s = __uint_as_float((uint32_t)e << 23);
     inv = __uint_as_float((uint32_t)(254 - e) << 23);
 }
-// The power of two at or below x (0, infinity, NaN: 1), within 2^+-100.
+// The exponent of the power of two at or below x >= 0 (0, infinity, NaN: of 1), its inverse a normal number, too.
 __device__ __forceinline__ int exponent_of(float x) {
     const int e = (int)(__float_as_uint(x) >> 23);
-    return e == 0 || e == 255 ? 127 : min(max(e, 27), 227);
+    return e == 0 || e == 255 ? 127 : min(e, 253);
 }
 // The larger of both, NaN where one is.
 __device__ __forceinline__ float max_nan(float x, float y) {

@@ -476,3 +476,21 @@ def test_prefill_readout_on_average(stepq, dtype):
     own = (3 * 2.0 ** -12 if dtype == "bf16" else 2.0 ** -15) * x["q"].float().norm(dim=-1).max().item()
     # errors of single terms are independent: spread over the 128 rows, on average C / sqrt(128) a value
     assert rms(x["o"].double() - o) <= half * rms(o) + own * C / D ** 0.5
+
+
+@pytest.mark.parametrize("power", [118, 90, -90, -100])
+def test_prefill_queries_of_all_sizes(stepq, power):
+    """Queries times a power of two: readouts times the same, bit for bit (as long as the bfloat16 queries and readouts themselves
+    stay normal: their values of 2^-20 and more, times 2^-100)."""
+    T, H, D = 100, 2, 128
+    ctx = _ctx(stepq, H, D, 1)
+    out = []
+    for p in (0, power):
+        x = _inputs(19, T, H, 1, D, "bf16")
+        x["q"].mul_(2.0 ** p)
+        S = torch.zeros(1, H, D, D, device="cuda")
+        ctx.delta_prefill(S, None, torch.tensor([0, T], dtype=torch.int32, device="cuda"), x["q"], x["k"], x["v"], x["alpha"],
+                          x["beta"], x["o"])
+        ctx.sync()
+        out.append(x["o"].clone())
+    assert torch.equal(out[0] * 2.0 ** power, out[1]) and torch.isfinite(out[1]).all()
