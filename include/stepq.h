@@ -412,6 +412,11 @@ int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const int32_t *p
                     float scale, void *o, int64_t o_stride, float *lse, void *workspace, void *stream);
 size_t stepq_kv_attend_workspace_bytes(const stepq_kv *kv, int n_seq, int n_tok, int n_q_heads, int max_pages);
 
+/* Bounded copy waits of the cache's attention, as stepq_ctx_set_wait_limit sets those of the step kernels: after `polls` polls (0:
+ * the default, 2^22) a wait gives up, the block ends and the error word is set ("copy wait gave up"; the call's outputs are not
+ * valid).  phantom_bytes (< 65536, normally 0) makes every wait run out. */
+int stepq_kv_set_wait_limit(stepq_kv *kv, uint32_t polls, uint32_t phantom_bytes);
+
 /* Wait for `stream` and return the error word (STEPQ_OK or STEPQ_EDEVICE; the
  * word is cleared). */
 int stepq_kv_check(stepq_kv *kv, void *stream);

@@ -58,6 +58,8 @@ struct KvAttendArgs {
     uint32_t div_mul;
     int div_shift;
     int seg;                // tokens of a copy: divides a page and a stage of 64, at least 16
+    uint32_t polls;         // before a wait gives up
+    uint32_t phantom_tx;    // bytes a stage waits for that never arrive (0: none; the test of that)
 };
 
 // dtype 0 fp32, 1 fp16, 2 bf16

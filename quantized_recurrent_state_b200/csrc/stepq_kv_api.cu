@@ -20,6 +20,7 @@ struct stepq_kv {
     uint32_t div_mul = 0;
     int div_shift = 0;
     int blocks[2][2] = {};  // of an attend call, by tiles of rows and terms of q
+    uint32_t polls = 1u << 22, phantom_tx = 0;
 };
 
 extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, int n_pages, stepq_kv **out) {
@@ -163,9 +164,18 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
                                 part, reinterpret_cast<float2 *>(part + (size_t)blocks * 2 * 8 * k.nr * kv->g.d),
                                 blocks, k.row_tiles, kv->div_mul, kv->div_shift,
-                                kv->g.page_tokens % 64 == 0 ? 64 : kv->g.page_tokens % 32 == 0 ? 32 : 16};
+                                kv->g.page_tokens % 64 == 0 ? 64 : kv->g.page_tokens % 32 == 0 ? 32 : 16,
+                                kv->polls, kv->phantom_tx};
     const cudaError_t e = stepq::launch_kv_attend(a, k.nr, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STEPQ_OK : cuda_fail(e, "kv_attend launch");
+}
+
+extern "C" int stepq_kv_set_wait_limit(stepq_kv *kv, uint32_t polls, uint32_t phantom_bytes) {
+    if (!kv) return fail(STEPQ_EINVAL, "kv_set_wait_limit: null cache handle");
+    if (phantom_bytes >= (1u << 16)) return fail(STEPQ_EINVAL, "kv_set_wait_limit: phantom_bytes %u", phantom_bytes);
+    kv->polls = polls ? polls : (1u << 22);
+    kv->phantom_tx = phantom_bytes;
+    return STEPQ_OK;
 }
 
 extern "C" int stepq_kv_check(stepq_kv *kv, void *stream) {

@@ -34,6 +34,9 @@
 // across units.  Each of the other four warps works on its own 16 tokens of every stage with its own reference, total and sums,
 // joined in a fixed order at the end of a unit.
 //
+// Every wait is bounded.  A warp whose wait gives up goes to the unit's end, where the four agree on whether to go on, and the
+// copying warp stays until its copies have landed: shared memory is not given back under them.
+//
 // Measured: 70 requests of up to 8,192 tokens, 8 cache heads of 128, 8 bits, 32 query heads: 130 to 138 us, 0.66 GB, 5 TB/s (the stages
 // alone run at the copy's rate; the start of a block costs 6 us, the end of a unit 3 to 4, the join 7).  One request of
 // 131,072 tokens at 4 bits: 49 us against 22: 4-bit codes cost 350 instructions a tile of 16 tokens, and the SM issues 59 % of the
@@ -45,6 +48,7 @@
 #include "stepq_delta.cuh"
 #include "stepq_dev.cuh"
 #include "stepq_kv.cuh"
+#include "stepq_tc16.cuh"
 
 namespace stepq {
 
@@ -52,7 +56,6 @@ namespace {
 
 constexpr int kWarps = 4, kTile = 16, kMaxBlocks = 1024;
 constexpr int kStep = kWarps * kTile;    // tokens of a stage
-constexpr uint32_t kPolls = 1u << 22;
 // log2 of the largest weight, and of the reference's: fp16 ends at 2^16 above and 2^-25 below, so a weight is lost 2^32 below the
 // reference's, and the reference moves when a weight is 2^8 of it
 constexpr float kSlack = 15.0f, kLift = 7.0f;
@@ -252,10 +255,10 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
         const uint32_t page_bytes = (uint32_t)g.page_bytes(), v_off = (uint32_t)(g.page_tokens * G::RB);
         const uint32_t codes = (uint32_t)(a.seg * G::RB), scales = (uint32_t)(a.seg * 4);
         const int off = lane * a.seg;
-        bool bad_page = false;
+        bool bad_page = false, in_time = true;
         int b = 0;
         uint32_t round = 0;
-        for (long long w = w0; w < w1;) {
+        for (long long w = w0; w < w1 && in_time;) {
             const int n = (int)min(w1 - w, (long long)(at.stages - at.first)), len = a.lens[at.s];
             const int32_t *table = a.table + (int64_t)at.s * a.max_pages;
             const uint8_t *const head = a.cache + (int64_t)(at.unit / a.row_tiles) * g.head_bytes();
@@ -271,12 +274,10 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
                 const bool mine = off < kStep && t0 + off < end;
                 const int now = page, now_row = row;
                 if (off < kStep && t0 + kStep + off < end) page = lookup(t0 + kStep + off, row);   // ahead of its use
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[b], (round & 1) ^ 1, kPolls))) {
-                    if (lane == 0) atomicOr(g.err, kErrKvWait);
-                    return;
-                }
+                in_time = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[b], (round & 1) ^ 1, a.polls));
+                if (!in_time) break;
                 const uint32_t lanes = __popc(__ballot_sync(0xffffffffu, mine));
-                if (lane == 0) mbar_arrive_expect(&full[b], lanes * 2 * (codes + scales));
+                if (lane == 0) mbar_arrive_expect(&full[b], lanes * 2 * (codes + scales) + a.phantom_tx);
                 __syncwarp();
                 if (mine) {
                     const bool in = (uint32_t)now < (uint32_t)g.n_pages;
@@ -302,6 +303,12 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
             if (w < w1) next_unit(a, at);
         }
         if (bad_page) atomicOr(g.err, kErrKvPlace);
+        if (lane == 0) {
+            // stage i was last filled in this round, or in the one before
+            for (int i = 0; i < G::STAGES; ++i)
+                if (i < b || round > 0) in_time = mbar_wait_bounded(&full[i], (i < b ? round : round - 1) & 1, a.polls) && in_time;
+            if (!in_time) atomicOr(g.err, kErrKvWait);
+        }
         return;
     }
 
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
     bool first = true;
 #pragma unroll 1
     for (int t0 = begin + warp * kTile; t0 - warp * kTile < end; t0 += kStep) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[b], round & 1, kPolls));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[b], round & 1, a.polls));
         if (!ok) break;
         const uint8_t *const stage = ring + b * G::STAGE;
         uint64_t *const done = &empty[b];
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
             wtot[warp][r] = total[j];
         }
     }
-    bar_workers();
+    ok = tc16::group_and(1, 32 * kWarps, ok);            // all four stop, or none
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
         const int r = 8 * (j / 2) + 2 * lc + j % 2;

@@ -30,7 +30,7 @@ EXPORTED = [
     "stepq_ctx_set_step_kernel",
     "stepq_delta_step", "stepq_delta_prefill", "stepq_ctx_wait_stream", "stepq_stream_wait_ctx",
     "stepq_kv_create", "stepq_kv_free", "stepq_kv_bytes", "stepq_kv_append", "stepq_kv_read", "stepq_kv_attend",
-    "stepq_kv_attend_workspace_bytes", "stepq_kv_check",
+    "stepq_kv_attend_workspace_bytes", "stepq_kv_set_wait_limit", "stepq_kv_check",
 ]
 FP32, FP16, BF16 = 0, 1, 2   # types of token rows
 PAD = -1                     # slot or cache place of a padding request
@@ -135,6 +135,7 @@ def lib():
         l.stepq_kv_attend.argtypes = [P, P, I, P, I, P, I, I, I, P, I64, ctypes.c_float, P, I64, P, P, P]
         l.stepq_kv_attend_workspace_bytes.argtypes = [P, I, I, I, I]
         l.stepq_kv_attend_workspace_bytes.restype = ctypes.c_size_t
+        l.stepq_kv_set_wait_limit.argtypes = [P, ctypes.c_uint32, ctypes.c_uint32]
         l.stepq_kv_check.argtypes = [P, P]
         _lib = l
     return _lib
@@ -537,6 +538,11 @@ class KVCache:
 
     def attend_workspace_bytes(self, n_seq: int, n_tok: int, n_q_heads: int, max_pages: int) -> int:
         return int(_lib.stepq_kv_attend_workspace_bytes(self._h, n_seq, n_tok, n_q_heads, max_pages))
+
+    def set_wait_limit(self, polls: int = 0, phantom_bytes: int = 0):
+        """Copy-wait poll limit of later attend calls (0: default); phantom_bytes > 0 makes every wait run out (tests of the
+        timeout path)."""
+        return _check(_lib.stepq_kv_set_wait_limit(self._h, int(polls), int(phantom_bytes)))
 
     def check(self):
         """Wait for the caller's current stream; raises if a call found a place, page or length out of range."""

@@ -467,3 +467,21 @@ def test_attend_query_channel_that_stands_out(stepq, dtype):
     bound = bound + torch.finfo(TYPES[dtype]).eps / 2 * (ref.abs() + bound) + 2.0 ** -25 * (dtype == "fp16")
     err = (o[0, 0].double() - ref).abs()
     assert (err <= bound).all(), (err / bound).max().item()
+
+
+@pytest.mark.parametrize("bits, d, page", [(8, 128, 64), (4, 64, 16), (8, 256, 32)])
+def test_attend_copy_wait_that_runs_out(stepq, bits, d, page):
+    """Every stage waits for 16 bytes that never arrive: the call ends and is reported, and later calls give what they gave."""
+    lens = [20000, 3000, 64, 5, 0]
+    s = Seqs(stepq, lens, bits, 2, d, page)
+    k, v = _randn(58, s.total, 2, d), _randn(59, s.total, 2, d)
+    s.fill(k, v)
+    q = _randn(60, len(lens), 2, 8, d).bfloat16()
+    good, lgood = _attend(s, q)
+    s.kv.set_wait_limit(4096, 16)
+    with pytest.raises(stepq.StepqError, match="copy wait gave up") as e:
+        _attend(s, q)
+    assert e.value.code == stepq.EDEVICE
+    s.kv.set_wait_limit()
+    again, l = _attend(s, q)
+    assert torch.equal(good, again) and torch.equal(lgood, l)

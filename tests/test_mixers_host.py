@@ -52,6 +52,10 @@ def test_kv_calls_refuse_null_handles(lib):
     lib.stepq_kv_free(None)
 
 
+def test_kv_wait_limit_refuses_a_null_handle(lib):
+    _einval(lib.stepq_kv_set_wait_limit(None, 0, 0), "null cache handle")
+
+
 def test_row_stride():
     x = torch.zeros(6, 10, 16)
     assert stepq._row_stride(x[:, 2:5], (6,), 3, 16, "x") == 160
