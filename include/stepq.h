@@ -342,7 +342,8 @@ int stepq_delta_prefill(stepq_ctx *ctx, int layer, float *S, const int32_t *slot
 /* Order the context's main stream after the work enqueued so far on a
  * stream of the caller (a cudaStream_t on the context's device), and the
  * other way round.  These two and the two calls above may come from several host threads (whose
- * calls share `main` and must not share states in use). */
+ * calls share `main` and must not share states in use); their launches are all counted and timed, and a launch's
+ * time may hold that of another thread's which was enqueued in between. */
 int stepq_ctx_wait_stream(stepq_ctx *ctx, void *stream);
 int stepq_stream_wait_ctx(stepq_ctx *ctx, void *stream);
 

@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <chrono>
 #include <cmath>
 #include <cstdarg>
@@ -645,13 +646,14 @@ struct stepq_ctx {
     void *tables_mem = nullptr;
     stepq::Tables t{};
     std::vector<uint32_t> layer_max_rec;  // max non-pivot record bytes per layer
-    uint64_t launches = 0;
-    bool timing = false;
+    std::atomic<uint64_t> launches{0};
+    std::atomic<bool> timing{false};
     uint32_t wait_polls = 1u << 22, phantom_tx = 0;
     int prefill_kernel = STEPQ_PREFILL_TCGEN05;
     int step_kernel = STEPQ_STEP_REGISTERS;
     bool poisoned = false;  // a tensor-memory drain failure was reported: refuse further work
     struct Timed { int kind; cudaEvent_t a, b; };
+    std::mutex time_mu;                  // guards the two below: delta calls come from several threads
     std::vector<Timed> timed;
     std::vector<cudaEvent_t> ev_pool;
 };
@@ -706,10 +708,13 @@ void set_stages(stepq_ctx *c, stepq::Args &a, int lb, int le) {
 }
 
 cudaEvent_t take_event(stepq_ctx *c) {
-    if (!c->ev_pool.empty()) {
-        cudaEvent_t e = c->ev_pool.back();
-        c->ev_pool.pop_back();
-        return e;
+    {
+        const std::lock_guard<std::mutex> hold(c->time_mu);
+        if (!c->ev_pool.empty()) {
+            cudaEvent_t e = c->ev_pool.back();
+            c->ev_pool.pop_back();
+            return e;
+        }
     }
     cudaEvent_t e = nullptr;
     cudaEventCreate(&e);
@@ -733,6 +738,7 @@ struct LaunchTimer {
         c->launches++;
         if (a && b) {
             cudaEventRecord(b, st);
+            const std::lock_guard<std::mutex> hold(c->time_mu);
             c->timed.push_back({kind, a, b});
         }
     }
@@ -879,7 +885,7 @@ extern "C" size_t stepq_workspace_bytes(const stepq_ctx *c, int n_req, int nL) {
     return (size_t)n_req * nL * c->plan->H * c->plan->D * sizeof(float);
 }
 
-extern "C" uint64_t stepq_launch_count(const stepq_ctx *c) { return c ? c->launches : 0; }
+extern "C" uint64_t stepq_launch_count(const stepq_ctx *c) { return c ? c->launches.load() : 0; }
 
 // ---------------------------------------------------------------------------
 // the step
@@ -1317,19 +1323,26 @@ extern "C" int stepq_kernel_stats(stepq_ctx *c, double *ms, uint64_t *launches) 
     int rc = set_device(c);
     if (rc) return rc;
     for (int k = 0; k < 5; ++k) { ms[k] = 0.0; launches[k] = 0; }
-    for (auto &t : c->timed) {
+    std::vector<stepq_ctx::Timed> timed;
+    {
+        const std::lock_guard<std::mutex> hold(c->time_mu);
+        timed.swap(c->timed);
+    }
+    for (auto &t : timed) {
+        if (rc) break;
         cudaError_t e = cudaEventSynchronize(t.b);
-        if (e != cudaSuccess) return cuda_fail(e, "kernel_stats: cudaEventSynchronize");
         float dt = 0.f;
-        e = cudaEventElapsedTime(&dt, t.a, t.b);
-        if (e != cudaSuccess) return cuda_fail(e, "kernel_stats: cudaEventElapsedTime");
+        if (e == cudaSuccess) e = cudaEventElapsedTime(&dt, t.a, t.b);
+        if (e != cudaSuccess) rc = cuda_fail(e, "kernel_stats: event");
         ms[t.kind] += dt;
         launches[t.kind] += 1;
+    }
+    const std::lock_guard<std::mutex> hold(c->time_mu);
+    for (auto &t : timed) {
         c->ev_pool.push_back(t.a);
         c->ev_pool.push_back(t.b);
     }
-    c->timed.clear();
-    return STEPQ_OK;
+    return rc;
 }
 
 extern "C" const char *stepq_last_error(void) { return g_err.c_str(); }

@@ -182,3 +182,42 @@ def test_one_context_from_two_threads(stepq):
 
     for a, b in zip(run(False), run(True)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("timing", [False, True])
+def test_launches_of_four_threads_are_all_counted(stepq, timing):
+    """Steps and prompts of four host threads through one context, timed or not: every launch is counted, every timed one
+    reported, while another thread asks for the times."""
+    import threading
+    ctx = stepq.Context(stepq.Plan.build_uniform(0, 1, H, D, 6), 1)
+    steps, names = 400, ("q", "k", "v", "alpha", "beta", "o")
+    S = [torch.zeros(1, H, D, D, device="cuda") for _ in range(4)]
+    x = [_tokens(30 + j, 20, torch.bfloat16) for j in range(4)]
+    cu, seen, errors = _int(0, 20), [0], []
+    torch.cuda.synchronize()
+    ctx.set_timing(timing)
+
+    def collect():
+        seen[0] += sum(n for _, n in ctx.kernel_stats().values())
+
+    def work(j):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for i in range(steps):
+                    if i % 2:
+                        ctx.delta_prefill(S[j], None, cu, *(x[j][n] for n in names))
+                    else:
+                        ctx.delta_step(S[j], None, *(x[j][n][:1].unsqueeze(0) for n in names))
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in range(4)]
+    for t in threads:
+        t.start()
+    while any(t.is_alive() for t in threads):
+        collect()
+    for t in threads:
+        t.join()
+    collect()
+    ctx.sync()
+    assert not errors and ctx.launches == 4 * steps and seen[0] == (4 * steps if timing else 0)
