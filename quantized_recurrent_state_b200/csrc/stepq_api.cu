@@ -60,6 +60,31 @@ int cuda_fail(cudaError_t e, const char *what) {
     return fail(STEPQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+static __global__ void k_take_word(int *word) { word[1] = atomicExch(word, 0); }
+
+cudaError_t ErrorWord::create() {
+    cudaError_t e = cudaMalloc(&mem_, 2 * sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(mem_, 0, 2 * sizeof(int));
+    // the default stream orders nothing against the callers' non-blocking streams
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    return e;
+}
+
+void ErrorWord::destroy() {
+    if (mem_) cudaFree(mem_);  // waits for the device's work
+    mem_ = nullptr;
+}
+
+cudaError_t ErrorWord::take(cudaStream_t st, int &word) {
+    cudaError_t e = cudaMemcpyAsync(&word, mem_, sizeof word, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess || !word) return e;
+    const std::lock_guard<std::mutex> hold(mu_);
+    k_take_word<<<1, 1, 0, st>>>(mem_);
+    if ((e = cudaGetLastError()) == cudaSuccess) e = cudaMemcpyAsync(&word, mem_ + 1, sizeof word, cudaMemcpyDeviceToHost, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
 int check_ptr(const void *p, size_t align, const char *name) {
     if (!p) return fail(STEPQ_EINVAL, "%s is null", name);
     if (reinterpret_cast<uintptr_t>(p) % align) return fail(STEPQ_EINVAL, "%s is not %zu-byte aligned", name, align);

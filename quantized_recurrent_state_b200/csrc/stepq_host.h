@@ -5,6 +5,8 @@
 #include <nvtx3/nvToolsExt.h>
 #include <stddef.h>
 
+#include <mutex>
+
 namespace stepq {
 
 // Sets the thread's stepq_last_error() message and returns `code`.
@@ -21,6 +23,22 @@ struct NvtxRange {
     ~NvtxRange() { nvtxRangePop(); }
     NvtxRange(const NvtxRange &) = delete;
     NvtxRange &operator=(const NvtxRange &) = delete;
+};
+
+// A device error word: kernels set bits of it, the host takes them.  Both are atomic, so that no bit is lost whatever
+// streams the kernels run on, and nothing waits for a stream that is not named.
+class ErrorWord {
+   public:
+    // Allocates the word on the current device; zero when this returns.
+    cudaError_t create();
+    void destroy();
+    // The word after all that `st` holds, and 0 in its place.
+    cudaError_t take(cudaStream_t st, int &word);
+    int *device() const { return mem_; }
+
+   private:
+    int *mem_ = nullptr;  // the word, and where a take puts it
+    std::mutex mu_;       // from a take's exchange to its copy
 };
 
 // Makes `device` current for a scope and puts the caller's device back.

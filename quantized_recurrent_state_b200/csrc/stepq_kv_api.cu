@@ -15,6 +15,7 @@ using stepq::NvtxRange;
 
 struct stepq_kv {
     stepq::KvGeo g{};
+    stepq::ErrorWord err;
     int device = 0;
     // ceil(2^(30 + l) / page_tokens), l = ceil(log2 page_tokens) >= 4: exact quotients of numbers below 2^30
     uint32_t div_mul = 0;
@@ -53,13 +54,12 @@ extern "C" int stepq_kv_create(int bits, int n_heads, int d, int page_tokens, in
         delete kv;
         return cuda_fail(e, "kv_create: kernel setup");
     }
-    e = cudaMalloc(&kv->g.err, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemset(kv->g.err, 0, sizeof(int));
-    if (e != cudaSuccess) {
-        if (kv->g.err) cudaFree(kv->g.err);
+    if ((e = kv->err.create()) != cudaSuccess) {
+        kv->err.destroy();
         delete kv;
         return cuda_fail(e, "cudaMalloc(error word)");
     }
+    kv->g.err = kv->err.device();
     *out = kv;
     return STEPQ_OK;
 }
@@ -68,7 +68,7 @@ extern "C" void stepq_kv_free(stepq_kv *kv) {
     if (!kv) return;
     {
         const stepq::DeviceScope dev(kv->device);
-        cudaFree(kv->g.err);  // waits for the device's work
+        kv->err.destroy();
     }
     delete kv;
 }
@@ -182,13 +182,10 @@ extern "C" int stepq_kv_check(stepq_kv *kv, void *stream) {
     if (!kv) return fail(STEPQ_EINVAL, "kv_check: null cache handle");
     const stepq::DeviceScope dev(kv->device);
     cudaError_t e = dev.error();
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int word = 0;
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) e = cudaMemcpy(&word, kv->g.err, sizeof word, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess) e = kv->err.take(static_cast<cudaStream_t>(stream), word);
     if (e != cudaSuccess) return cuda_fail(e, "kv_check");
     if (!word) return STEPQ_OK;
-    cudaMemset(kv->g.err, 0, sizeof(int));
     return fail(STEPQ_EDEVICE, "device error word 0x%x (%s%s%s)", word,
                 (word & stepq::kErrKvPlace) ? "place, page or output row out of range " : "",
                 (word & stepq::kErrKvLen) ? "length above the page table's " : "",

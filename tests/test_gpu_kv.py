@@ -485,3 +485,29 @@ def test_attend_copy_wait_that_runs_out(stepq, bits, d, page):
     s.kv.set_wait_limit()
     again, l = _attend(s, q)
     assert torch.equal(good, again) and torch.equal(lgood, l)
+
+
+def test_check_waits_for_its_own_stream_alone(stepq):
+    """A check on one stream neither waits for the default stream's work nor leaves anything to be done behind it: a bad place
+    is reported by the next check, however soon it was found."""
+    import gc
+    gc.collect()                                         # a handle freed below would wait for the device
+    s = Seqs(stepq, [16], 8, 1, 64, 16)
+    k = _randn(57, 16, 1, 64)
+    bad = torch.full((16,), -2, dtype=torch.int64, device="cuda")
+    side, end = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        s.kv.append(s.cache, k, k, bad)                  # (what the first call sets up is in place)
+        with pytest.raises(stepq.StepqError, match="out of range"):
+            s.kv.check()
+    torch.cuda._sleep(4_000_000_000)                     # two seconds on the default stream
+    end.record()
+    with torch.cuda.stream(side):
+        for _ in range(500):
+            s.kv.append(s.cache, k, k, bad)
+            with pytest.raises(stepq.StepqError, match="out of range"):
+                s.kv.check()
+        s.kv.check()
+        assert not end.query()
+    torch.cuda.synchronize()
