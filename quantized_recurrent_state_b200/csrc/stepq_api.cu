@@ -667,7 +667,8 @@ struct stepq_ctx {
     cudaEvent_t ev_main = nullptr, ev_side = nullptr;
     cudaEvent_t ev_join = nullptr;  // orders main and a caller's stream
     std::mutex join_mu;             // from its record to its wait
-    int *err = nullptr;
+    stepq::ErrorWord word;
+    int *err = nullptr;             // the word on the device
     void *tables_mem = nullptr;
     stepq::Tables t{};
     std::vector<uint32_t> layer_max_rec;  // max non-pivot record bytes per layer
@@ -863,9 +864,9 @@ extern "C" int stepq_ctx_create(const stepq_plan *plan, void *main_stream, void 
     c->t.rho = (const float *)put(p->rho.data(), sz_f, sz_f);
     e = cudaGetLastError();
     if (e != cudaSuccess || o > total) { cudaFree(c->tables_mem); delete c; return cuda_fail(e, "table upload"); }
-    e = cudaMalloc(&c->err, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemset(c->err, 0, sizeof(int));
-    if (e != cudaSuccess) { cudaFree(c->tables_mem); delete c; return cuda_fail(e, "cudaMalloc(error word)"); }
+    e = c->word.create();  // and the tables' copies, on the same stream, have ended
+    if (e != cudaSuccess) { c->word.destroy(); cudaFree(c->tables_mem); delete c; return cuda_fail(e, "cudaMalloc(error word)"); }
+    c->err = c->word.device();
     c->side_done.resize(p->L);
     c->dec_done.resize(p->L);
     for (int l = 0; l < p->L && e == cudaSuccess; ++l) {
@@ -900,7 +901,7 @@ extern "C" void stepq_ctx_free(stepq_ctx *c) {
     if (c->ev_main) cudaEventDestroy(c->ev_main);
     if (c->ev_side) cudaEventDestroy(c->ev_side);
     if (c->ev_join) cudaEventDestroy(c->ev_join);
-    if (c->err) cudaFree(c->err);
+    c->word.destroy();
     if (c->tables_mem) cudaFree(c->tables_mem);
     delete c;
 }
@@ -1084,10 +1085,9 @@ extern "C" int stepq_sync(stepq_ctx *c, int timeout_ms) {
         std::this_thread::sleep_for(std::chrono::microseconds(20));
     }
     int word = 0;
-    e = cudaMemcpy(&word, c->err, sizeof word, cudaMemcpyDeviceToHost);
+    e = c->word.take(c->main, word);
     if (e != cudaSuccess) return cuda_fail(e, "sync: read error word");
     if (word) {
-        cudaMemset(c->err, 0, sizeof(int));
         if (word & stepq::kErrTmemDrain) c->poisoned = true;
         return fail(STEPQ_EDEVICE, "device error word 0x%x (%s%s%s%s%s%s%s)", word,
                     (word & stepq::kErrBadSlot) ? "slot out of range " : "", (word & stepq::kErrWait) ? "copy wait gave up " : "",

@@ -221,3 +221,31 @@ def test_launches_of_four_threads_are_all_counted(stepq, timing):
     collect()
     ctx.sync()
     assert not errors and ctx.launches == 4 * steps and seen[0] == (4 * steps if timing else 0)
+
+
+def test_sync_waits_for_its_own_streams_alone(stepq):
+    """sync neither waits for the default stream's work nor leaves anything to be done behind it: a bad slot is reported by the
+    next one, however soon it was found."""
+    import gc
+    gc.collect()                                         # a handle freed below would wait for the device
+    ctx = stepq.Context(stepq.Plan.build_uniform(0, 1, H, D, 6), 1)
+    x = _tokens(40, 1, torch.bfloat16)
+    pool, bad = torch.zeros(1, 1, H, D, D, device="cuda"), _int(3)
+    side, end = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+
+    def step():
+        ctx.delta_step(pool, bad, *(x[n].unsqueeze(1) for n in ("q", "k", "v", "alpha", "beta", "o")))
+        with pytest.raises(stepq.StepqError, match="slot out of range"):
+            ctx.sync()
+
+    with torch.cuda.stream(side):
+        step()                                           # (what the first call sets up is in place)
+    torch.cuda._sleep(4_000_000_000)                     # two seconds on the default stream
+    end.record()
+    with torch.cuda.stream(side):
+        for _ in range(500):
+            step()
+        ctx.sync()
+        assert not end.query()
+    torch.cuda.synchronize()
