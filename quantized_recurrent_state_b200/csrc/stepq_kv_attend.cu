@@ -18,12 +18,13 @@
 // the products: r_k multiplies the score, r_v the weight.
 //
 // The weight p r_v has to fit fp16, whatever r_v is, so the running reference of a row
-// is the largest s + log2 r_v instead of the largest s (lr below).  The reference's weight is 2^7, and it moves only
-// when a weight would exceed 2^15: sums are fp32; a move costs
+// is the largest s + log2 r_v instead of the largest s (lr below).  Weights are held 2^7 times as large, and the
+// reference moves only when one would exceed 2^15: sums are fp32; a move costs
 // three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry up to 2^-11 of
 // themselves as rounding error, or 2^-32 of the reference's where that is more (fp16 ends at 2^-25); fp32 outputs take them as
 // sums of two fp16 values, the second held 2^11 times as large (2^-22 of the weight, or 2^-43 of the reference's), and q likewise
-// without that factor (2^-22 of a value, or 2^-39 of the row's largest).
+// without that factor (2^-22 of a value, or 2^-39 of the row's largest).  The score less the reference is an fp32 number, whose
+// rounding a weight takes on: 2^-22 where log2 r_v is of the order of -5, 2^-18 at most (rows of zeros alone, which count as 2^-60).
 //
 // Work is cut evenly: all stages of 64 tokens of all (sequence, cache head, tile of rows) units lie in one line, and block i of
 // as many as the GPU holds at once takes the i-th piece of it, whatever the lengths are (they are on the device, and each
@@ -56,9 +57,9 @@ namespace {
 
 constexpr int kWarps = 4, kTile = 16, kMaxBlocks = 1024;
 constexpr int kStep = kWarps * kTile;    // tokens of a stage
-// log2 of the largest weight, and of the reference's: fp16 ends at 2^16 above and 2^-25 below, so a weight is lost 2^32 below the
-// reference's, and the reference moves when a weight is 2^8 of it
-constexpr float kSlack = 15.0f, kLift = 7.0f;
+// The reference moves when a weight is 2^kSlack of it.  Weights are held kLift times as large: fp16 ends at 2^16 above and 2^-25
+// below, so a weight is lost 2^32 below the reference's.
+constexpr float kSlack = 8.0f, kLift = 128.0f;
 constexpr int kLiftQ = 15;               // the queries' largest value is below 2^15: their small values stay above fp16's end, too
 constexpr float kNone = -1e30f;          // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -217,6 +218,13 @@ __device__ __forceinline__ void put_out(const KvAttendArgs &a, int64_t at, float
     if (a.dtype == 0) static_cast<float *>(a.o)[at] = y;
     else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(y);
     else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
+}
+// Natural logarithm of 2^m l: the reference, which holds value scales, too, is cancelled by l's exponent before any rounding.
+__device__ __forceinline__ float log_sum(float m, float l) {
+    if (l == 0.0f) return -INFINITY;
+    int e;
+    const float f = frexpf(l, &e);
+    return (m + (float)e) * kLn2 + logf(f);
 }
 __device__ __forceinline__ void bar_workers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
@@ -498,9 +506,9 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                 // by how much the reference moves: down only while there are no sums (a row that sees nothing in its first
                 // tile sees nothing at all)
-                m -= kLift;
-                const float by = first ? (m == -INFINITY ? 0.0f : m) : fmaxf(m, 0.0f), f = first ? 1.0f : ex2(-by);
-                ref[j] += by;
+                const float to = ref[j] + (first ? (m == -INFINITY ? 0.0f : m) : fmaxf(m, 0.0f)), by = to - ref[j];
+                const float f = first ? 1.0f : ex2(-by);
+                ref[j] = to;
                 sc[j / 2][j & 1] -= by;
                 sc[j / 2][2 + (j & 1)] -= by;
                 total[j] *= f;
@@ -511,6 +519,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
                 }
             }
         }
+        const float rw[2] = {rv[0] * kLift, rv[1] * kLift};
         uint32_t pb[TERMS][NR][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
@@ -521,7 +530,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
                 for (int b = 0; b < 2; ++b) {
                     const float y = sc[nr][2 * i + b], p = ex2(y);
                     total[2 * nr + b] += p;
-                    wgt[b] = p * rv[i];
+                    wgt[b] = p * rw[i];
                     if (masked && y == -INFINITY) wgt[b] = 0.0f;     // nothing of a masked row, whatever its scale
                 }
                 const __half2 hi = __floats2half2_rn(wgt[0], wgt[1]);
@@ -647,12 +656,12 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
         const int64_t place = ((int64_t)blockIdx.x * 2 + (at.first == 0 ? 1 : 0)) * G::R + r;   // if not whole
         for (int c = lane; c < D; c += 32) {
             const float y = sum[G::sum_at(r, c)];
-            if (whole) put_out(a, tok * a.os + (int64_t)hq * D + c, l == 0.0f ? 0.0f : y / l);
+            if (whole) put_out(a, tok * a.os + (int64_t)hq * D + c, l == 0.0f ? 0.0f : y * (1.0f / kLift) / l);
             else a.part[place * D + c] = y;
         }
         if (lane == 0) {
             if (!whole) a.meta[place] = make_float2(m, l);
-            else if (a.lse) a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+            else if (a.lse) a.lse[tok * a.Hq + hq] = log_sum(m, l);
         }
     }
     if (!ok) break;
@@ -735,9 +744,9 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
         float z = 0.0f;
 #pragma unroll
         for (int w = 0; w < GROUPS; ++w) z += sum[w][tid];
-        put_out(a, tok * a.os + (int64_t)hq * D + tid, l == 0.0f ? 0.0f : z / l);
+        put_out(a, tok * a.os + (int64_t)hq * D + tid, l == 0.0f ? 0.0f : z * (1.0f / kLift) / l);
     }
-    if (tid == 0 && a.lse) a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+    if (tid == 0 && a.lse) a.lse[tok * a.Hq + hq] = log_sum(m, l);
 }
 
 template <int BITS, int D, int NR, int TERMS>

@@ -511,3 +511,20 @@ def test_check_waits_for_its_own_stream_alone(stepq):
         s.kv.check()
         assert not end.query()
     torch.cuda.synchronize()
+
+
+def test_attend_log_sum_of_zero_value_rows(stepq):
+    """One token with a value row of zeros: o = 0, and the logarithm of the sum is its score.  The score less the reference is
+    near 60 and rounded twice (2^-19 each in base 2)."""
+    n, d = 64, 64
+    s = Seqs(stepq, [1] * n, 8, 1, d, 16)
+    k, v = _randn(61, n, 1, d), torch.zeros(n, 1, d, device="cuda")
+    s.fill(k, v)
+    q = _randn(62, n, 1, 4, d) * 0.05
+    o, l = _attend(s, q)
+    z, r = _quantise(k, 8)
+    kd = r.double().unsqueeze(-1) * z.double()
+    ref = torch.einsum("sihd,sd->sih", q.double(), kd[:, 0]) * d ** -0.5
+    ds = d ** -0.5 * (d + 2) * 2.0 ** -23 * torch.einsum("sihd,sd->sih", q.double().abs(), kd[:, 0].abs())
+    bound = ds + 2.0 ** -22 + 2 * 2.0 ** -19 * math.log(2.0) + 2.0 ** -22 * ref.abs()
+    assert (o == 0).all() and ((l.double() - ref).abs() <= bound).all()
