@@ -331,7 +331,8 @@ int stepq_delta_step(stepq_ctx *ctx, int layer, float *S, const int32_t *slots, 
  * tokens on the tensor cores (sequences of up to 12 tokens, and all other calls, run
  * token by token): states stay fp32, with operands as sums of two fp16
  * values under powers of two, so results match the token-by-token form to the tolerances
- * stated in the tests, not bit for bit.  The chunked form holds for beta_t |k_t|^2
+ * stated in the tests, not bit for bit: relative to the largest state and value that a value column meets within the
+ * 64 tokens, also where a gate then forgets them.  The chunked form holds for beta_t |k_t|^2
  * <= 2, where the recurrence does not grow, and for states and values up to 2^100; beyond that intermediate
  * values may leave fp16, which sets the device error word ("prefill range"; that head's results are not valid).  An infinity or NaN in k or v reaches
  * its head's state and outputs from that token on, in the chunked form from the first token
@@ -343,7 +344,8 @@ int stepq_delta_prefill(stepq_ctx *ctx, int layer, float *S, const int32_t *slot
  * stream of the caller (a cudaStream_t on the context's device), and the
  * other way round.  These two and the two calls above may come from several host threads (whose
  * calls share `main` and must not share states in use); their launches are all counted and timed, and a launch's
- * time may hold that of another thread's which was enqueued in between. */
+ * time may hold that of another thread's which was enqueued in between.  A capture that takes `main` in
+ * takes in what any thread enqueues there: only the capturing thread may call the context until it ends. */
 int stepq_ctx_wait_stream(stepq_ctx *ctx, void *stream);
 int stepq_stream_wait_ctx(stepq_ctx *ctx, void *stream);
 
@@ -379,7 +381,7 @@ size_t stepq_kv_bytes(const stepq_kv *kv);
 /* Quantise n_tokens rows of k and v ([n_tokens][n_heads][d], row strides in
  * elements, as in stepq_tokens) into the cache at places[t] (device int64;
  * STEPQ_PAD skips the token; a place outside the cache sets the error word and
- * is skipped; of several tokens with one place, which one stays is undefined). */
+ * is skipped; a row that several tokens of a call have as their place holds parts of any of them). */
 int stepq_kv_append(stepq_kv *kv, void *cache, int dtype, int n_tokens, const void *k, const void *v,
                     int64_t k_stride, int64_t v_stride, const int64_t *places, void *stream);
 

@@ -13,7 +13,7 @@
 // it sends 2 + 1 + 1 values.
 //
 // Bound: HBM, each state read and written once (8 D^2 bytes), as long as there are few tokens: 70 requests of 48 heads at D = 128,
-// one token each, 74 us, 5.9 TB/s (65 us of it in the kernel, whose 12 warps an SM have 768 16-byte loads in
+// one token each, 74 us, 5.9 TB/s (65 us of it in the kernel, whose 12 warps an SM have 6,144 16-byte loads in
 // flight).  One request is bound by the launch and the host's call (13 us).  From about four tokens on the shuffles count, which are latency: with
 // several tokens the next one's rows are loaded before the current one's sums (MANY, up to 242 registers instead of 168;
 // 17 requests of 32 heads with four fp32 tokens and gates per key row: 28 to 32 us against a floor of 12).  A warp for

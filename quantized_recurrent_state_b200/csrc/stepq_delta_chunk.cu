@@ -33,10 +33,10 @@
 // (64-127); W^T 128-191 and R terms 192-255, later the state's increment; Y^T = S^T Q'^T 256-319; U'^T 320-383, later
 // A U'; [K; Q] K^T 384-511, one for each group.
 //
-// Bound: latency, not HBM (12 %) nor the tensor pipe (22 %).  A chunk of a head takes 9,000 cycles: S to operands 1,700, W 700,
+// Bound: latency, not HBM (14 %) nor the tensor pipe (23 %).  A chunk of a head takes 9,000 cycles: S to operands 1,700, W 700,
 // R 1,600, U' 900, the increment 900, S 550, the rest hand-overs; a group's preparation takes 13,000 for every other chunk.  The SM
-// issues 52 % of the time, 24,000 warp instructions a chunk.  2,048 tokens of one prompt and 48 heads 171 us; 16 prompts of up
-// to 2,048 tokens 585 us (floor 107: 0.7 GB); 37 prompts of up to 130 tokens and 32 heads 151 us.
+// issues 52 % of the time, 24,000 warp instructions a chunk.  2,048 tokens of one prompt and 48 heads 173 us; 16 prompts of up
+// to 2,048 tokens 572 us (floor 107: 0.7 GB); 37 prompts of up to 130 tokens and 32 heads 148 us.
 // C = 64: X costs C^2 a token and the hand-overs 1 / C; 64 rows of K and 64 of Q fill the 128 rows of one product.
 //
 // Sequences of at most 12 tokens go token by token in the same launch (short_sequence): their state is all they cost, and a
