@@ -422,7 +422,8 @@ int stepq_kv_set_wait_limit(stepq_kv *kv, uint32_t polls, uint32_t phantom_bytes
 
 /* Wait for `stream` and return the error word (STEPQ_OK or STEPQ_EDEVICE; the
  * word is cleared).  The word is the handle's: it also holds what calls on other streams
- * have set so far, which is then not reported to them; what they set later is kept. */
+ * have set so far, which is then not reported to them; what they set later is kept.  Refused while `stream`
+ * captures; the capture goes on. */
 int stepq_kv_check(stepq_kv *kv, void *stream);
 
 /* Pack fp32 states S into the pool records of (slots, layers [lb, le)):

@@ -76,7 +76,11 @@ void ErrorWord::destroy() {
 }
 
 cudaError_t ErrorWord::take(cudaStream_t st, int &word) {
-    cudaError_t e = cudaMemcpyAsync(&word, mem_, sizeof word, cudaMemcpyDeviceToHost, st);
+    // a capture would take the copy in, to an address that is gone when it is replayed
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &capture);
+    if (e == cudaSuccess && capture != cudaStreamCaptureStatusNone) e = cudaErrorStreamCaptureUnsupported;
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&word, mem_, sizeof word, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess || !word) return e;
     const std::lock_guard<std::mutex> hold(mu_);

@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
         }
         if (bad_page) atomicOr(g.err, kErrKvPlace);
         if (lane == 0) {
-            // stage i was last filled in this round, or in the one before
+            // stage i was last filled in this turn of the ring, or in the one before
             for (int i = 0; i < G::STAGES; ++i)
                 if (i < b || round > 0) in_time = mbar_wait_bounded(&full[i], (i < b ? round : round - 1) & 1, a.polls) && in_time;
             if (!in_time) atomicOr(g.err, kErrKvWait);

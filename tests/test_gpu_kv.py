@@ -528,3 +528,18 @@ def test_attend_log_sum_of_zero_value_rows(stepq):
     ds = d ** -0.5 * (d + 2) * 2.0 ** -23 * torch.einsum("sihd,sd->sih", q.double().abs(), kd[:, 0].abs())
     bound = ds + 2.0 ** -22 + 2 * 2.0 ** -19 * math.log(2.0) + 2.0 ** -22 * ref.abs()
     assert (o == 0).all() and ((l.double() - ref).abs() <= bound).all()
+
+
+def test_check_is_refused_in_a_capture(stepq):
+    """The check raises, takes nothing into the graph, and the capture goes on."""
+    s = Seqs(stepq, [20], 8, 1, 64, 16)
+    k, v = _randn(63, 20, 1, 64), _randn(64, 20, 1, 64)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.fill(k, v)
+        with pytest.raises(stepq.StepqError, match="captur"):
+            s.kv.check()
+    graph.replay()
+    z, r = _quantise(k, 8)
+    assert torch.equal(s.read(torch.float32)[0], r.unsqueeze(-1) * z.float())
