@@ -53,7 +53,7 @@ struct KvAttendArgs {
     float scale;
     float *lse;
     float *part;            // pieces of units: sums [block][2][row][d]
-    float2 *meta;           // and (reference, total) [block][2][row]
+    float4 *meta;           // and (score reference, total, scale reference, -) [block][2][row]
     int blocks, row_tiles;
     uint32_t div_mul;
     int div_shift;

@@ -131,10 +131,10 @@ extern "C" int stepq_kv_read(stepq_kv *kv, const void *cache, int n_seq, const i
 
 extern "C" size_t stepq_kv_attend_workspace_bytes(const stepq_kv *kv, int n_seq, int n_tok, int n_q_heads, int max_pages) {
     if (!kv || n_seq < 0 || n_tok < 1 || n_q_heads < 1 || n_q_heads % kv->g.H || max_pages < 1) return 0;
-    // two pieces a block: sums, (reference, total)
+    // two pieces a block: sums, (references, total)
     const int nr = stepq::kv_split(kv->g, n_tok, n_q_heads).nr;
     const int blocks = kv->blocks[nr - 1][0] > kv->blocks[nr - 1][1] ? kv->blocks[nr - 1][0] : kv->blocks[nr - 1][1];
-    return (size_t)blocks * 2 * 8 * nr * (kv->g.d + 2) * sizeof(float);
+    return (size_t)blocks * 2 * 8 * nr * (kv->g.d + 4) * sizeof(float);
 }
 
 extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const int32_t *page_table, int max_pages,
@@ -162,7 +162,7 @@ extern "C" int stepq_kv_attend(stepq_kv *kv, const void *cache, int n_seq, const
     float *const part = static_cast<float *>(workspace);
     const stepq::KvAttendArgs a{kv->g, static_cast<const uint8_t *>(cache), page_table, lens, n_seq, max_pages, n_tok,
                                 n_q_heads, dtype, q, o, q_stride, o_stride, scale, lse,
-                                part, reinterpret_cast<float2 *>(part + (size_t)blocks * 2 * 8 * k.nr * kv->g.d),
+                                part, reinterpret_cast<float4 *>(part + (size_t)blocks * 2 * 8 * k.nr * kv->g.d),
                                 blocks, k.row_tiles, kv->div_mul, kv->div_shift,
                                 kv->g.page_tokens % 64 == 0 ? 64 : kv->g.page_tokens % 32 == 0 ? 32 : 16,
                                 kv->polls, kv->phantom_tx};

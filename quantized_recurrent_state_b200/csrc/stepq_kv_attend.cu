@@ -17,14 +17,14 @@
 // but costs the score eight bits where a few channels stand out and the other codes are small).  The row scales stay outside
 // the products: r_k multiplies the score, r_v the weight.
 //
-// The weight p r_v has to fit fp16, whatever r_v is, so the running reference of a row
-// is the largest s + log2 r_v instead of the largest s (lr below).  Weights are held 2^7 times as large, and the
-// reference moves only when one would exceed 2^15: sums are fp32; a move costs
-// three shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry up to 2^-11 of
-// themselves as rounding error, or 2^-32 of the reference's where that is more (fp16 ends at 2^-25); fp32 outputs take them as
-// sums of two fp16 values, the second held 2^11 times as large (2^-22 of the weight, or 2^-43 of the reference's), and q likewise
-// without that factor (2^-22 of a value, or 2^-39 of the row's largest).  The score less the reference is an fp32 number, whose
-// rounding a weight takes on: 2^-22 where log2 r_v is of the order of -5, 2^-18 at most (rows of zeros alone, which count as 2^-60).
+// The weight p r_v has to fit fp16, whatever r_v is, while the sum of p wants p near 1 at the largest score.  So a row has two
+// references: one of the scores, near the largest, which p = 2^(s - ref) is taken against, and an integer power of two for the value
+// scales on top of it, which the weight p r_v is multiplied by: 2^7 at the largest.  Both stay where they are until a weight would
+// exceed 2^15 or a p 2^16: sums are fp32; a move costs six shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry
+// up to 2^-11 of themselves as rounding error, or 2^-32 of the largest's where that is more (fp16 ends at 2^-25); fp32 outputs take
+// them as sums of two fp16 values, the second held 2^11 times as large (2^-22 of the weight, or 2^-43 of the largest's), and q
+// likewise without that factor (2^-22 of a value, or 2^-39 of the row's largest).  (One reference for both, the largest s + log2 r_v,
+// was 1 to 3 % faster, and lost the tokens that it pushed below 2^-126 beside value rows of 1e35 and more.)
 //
 // Work is cut evenly: all stages of 64 tokens of all (sequence, cache head, tile of rows) units lie in one line, and block i of
 // as many as the GPU holds at once takes the i-th piece of it, whatever the lengths are (they are on the device, and each
@@ -57,9 +57,10 @@ namespace {
 
 constexpr int kWarps = 4, kTile = 16, kMaxBlocks = 1024;
 constexpr int kStep = kWarps * kTile;    // tokens of a stage
-// The reference moves when a weight is 2^kSlack of it.  Weights are held kLift times as large: fp16 ends at 2^16 above and 2^-25
-// below, so a weight is lost 2^32 below the reference's.
-constexpr float kSlack = 8.0f, kLift = 128.0f;
+// The largest weight and p that do not move the references; log2 of the largest just after a move.  fp16 ends at 2^16 above and
+// 2^-25 below, so a weight is lost 2^32 below the largest.
+constexpr float kMost = 32768.0f, kMostP = 65536.0f;
+constexpr int kLift = 7;
 constexpr int kLiftQ = 15;               // the queries' largest value is below 2^15: their small values stay above fp16's end, too
 constexpr float kNone = -1e30f;          // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -219,13 +220,18 @@ __device__ __forceinline__ void put_out(const KvAttendArgs &a, int64_t at, float
     else if (a.dtype == 1) static_cast<__half *>(a.o)[at] = __float2half_rn(y);
     else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
 }
-// Natural logarithm of 2^m l: the reference, which holds value scales, too, is cancelled by l's exponent before any rounding.
+// Natural logarithm of 2^m l.
 __device__ __forceinline__ float log_sum(float m, float l) {
     if (l == 0.0f) return -INFINITY;
     int e;
     const float f = frexpf(l, &e);
     return (m + (float)e) * kLn2 + logf(f);
 }
+// The value scales' reference k (an integer within [-60, 126]) as the factor of the weights, and what undoes it at the end.
+__device__ __forceinline__ float factor_of(int k) { return __uint_as_float((uint32_t)(127 + kLift - k) << 23); }
+__device__ __forceinline__ float undo_of(int k) { return __uint_as_float((uint32_t)(127 - kLift + k) << 23); }
+__device__ __forceinline__ int k_of(float factor) { return 127 + kLift - (int)(__float_as_uint(factor) >> 23); }
+__device__ __forceinline__ int scale_ref(float x) { return (int)fminf(fmaxf(ceilf(x), -60.0f), 126.0f); }
 __device__ __forceinline__ void bar_workers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 // Blocks an SM that the compiler is held to with two terms, whose independent sums it would otherwise run side by side in the
@@ -239,6 +245,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
     __half *qf = reinterpret_cast<__half *>(smem + G::STAGES * G::STAGE + G::SUM);   // [TERMS][KS][NR][32][2] half pairs
     __shared__ float qe[G::R];                           // score factor of the row
     __shared__ float wref[kWarps][G::R], wtot[kWarps][G::R];
+    __shared__ float wsc[kWarps][G::R];
     __shared__ uint64_t full[G::STAGES], empty[G::STAGES];
     const KvGeo &g = a.g;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lc = lane & 3;
@@ -387,12 +394,14 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
     bar_workers();
 
     float ref[2 * NR], total[2 * NR], lift[2 * NR];
+    float fac[2 * NR];                                   // of the value scales' reference
     int limit[2 * NR];                                   // first token that the row does not see
     float acc[G::KS][NR][4];
 #pragma unroll
     for (int j = 0; j < 2 * NR; ++j) {
         const int r = 8 * (j / 2) + 2 * lc + j % 2;
         ref[j] = 0.0f;                                   // set by the first tile
+        fac[j] = factor_of(0);
         total[j] = 0.0f;
         lift[j] = qe[r];
         limit[j] = r < nrow ? len - a.n_tok + 1 + (r0 + r) / group : 0;   // a row without a query sees nothing
@@ -473,17 +482,16 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
 #pragma unroll
             for (int i = 0; i < 4; ++i) G::V::template load<8>(vr + ((i & 1) + 8 * (i >> 1)) * G::RB, lg, vw[i]);
         }
-        // log2 of the weights against the reference: the score less it; log2 r_v on top of that may not pass the slack.  A row of
-        // zeros (r_v = 0) and one marked NaN count as the smallest, so that they do not move the others' weights down.
-        const float lr[2] = {fmaxf(lg2(rv[0]), -60.0f), fmaxf(lg2(rv[1]), -60.0f)};
-        const float room[2] = {kSlack - lr[0], kSlack - lr[1]};
-        bool far = false;
+        // the score less its reference
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 2 * nr + (e & 1);
-                sc[nr][e] = fmaf(sc[nr][e], rk[e >> 1] * lift[j], -ref[j]);
+            for (int i = 0; i < 2; ++i) {
+                const float2 y = fma2(make_float2(sc[nr][2 * i], sc[nr][2 * i + 1]),
+                                      mul2(make_float2(rk[i], rk[i]), make_float2(lift[2 * nr], lift[2 * nr + 1])),
+                                      make_float2(-ref[2 * nr], -ref[2 * nr + 1]));
+                sc[nr][2 * i] = y.x;
+                sc[nr][2 * i + 1] = y.y;
             }
         const bool masked = t0 + kTile > clear;
         if (masked) {
@@ -493,51 +501,77 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
                 for (int e = 0; e < 4; ++e)
                     if (t0 + lg + 8 * (e >> 1) >= limit[2 * nr + (e & 1)]) sc[nr][e] = -INFINITY;
         }
+        float p[NR][4], wgt[NR][4];
+        auto weigh = [&]() {                             // true: a weight or a p is too large for the references
+            bool far = false;
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) far = far || sc[nr][e] > room[e >> 1];
-        if (first || __any_sync(0xffffffffu, far)) {
+                for (int i = 0; i < 2; ++i) {
+                    const float2 p2 = make_float2(ex2(sc[nr][2 * i]), ex2(sc[nr][2 * i + 1]));
+                    float2 w = mul2(mul2(p2, make_float2(rv[i], rv[i])), make_float2(fac[2 * nr], fac[2 * nr + 1]));
+                    if (masked) {                        // nothing of a masked row, whatever its scale
+                        if (sc[nr][2 * i] == -INFINITY) w.x = 0.0f;
+                        if (sc[nr][2 * i + 1] == -INFINITY) w.y = 0.0f;
+                    }
+                    far = far || p2.x > kMostP || p2.y > kMostP || w.x > kMost || w.y > kMost;
+                    p[nr][2 * i] = p2.x;
+                    p[nr][2 * i + 1] = p2.y;
+                    wgt[nr][2 * i] = w.x;
+                    wgt[nr][2 * i + 1] = w.y;
+                }
+            return far;
+        };
+        if (first || __any_sync(0xffffffffu, weigh())) {
+            // A row of zeros (r_v = 0) and one marked NaN count as 2^-60, so that they do not move the others' weights down.
+            const float lr[2] = {fmaxf(lg2(rv[0]), -60.0f), fmaxf(lg2(rv[1]), -60.0f)};
 #pragma unroll
             for (int j = 0; j < 2 * NR; ++j) {
-                float m = fmaxf(sc[j / 2][j & 1] + lr[0], sc[j / 2][2 + (j & 1)] + lr[1]);
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                // by how much the reference moves: down only while there are no sums (a row that sees nothing in its first
-                // tile sees nothing at all)
-                const float to = ref[j] + (first ? (m == -INFINITY ? 0.0f : m) : fmaxf(m, 0.0f)), by = to - ref[j];
-                const float f = first ? 1.0f : ex2(-by);
+                const float s0 = sc[j / 2][j & 1], s1 = sc[j / 2][2 + (j & 1)];
+                float ms = fmaxf(s0, s1), mw = fmaxf(s0 + lr[0], s1 + lr[1]);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) {
+                    ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, w));
+                    mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, w));
+                }
+                // the row's own need, whatever its neighbours': down only while there are no sums (a row that sees nothing in
+                // its first tile sees nothing at all)
+                const int was = k_of(fac[j]);
+                const bool own = ms > 8.0f || mw - (float)was > 8.0f;
+                float to = ref[j];
+                int k = was;
+                if (first) to = ms == -INFINITY ? 0.0f : ms;
+                else if (own) to += fmaxf(ms, 0.0f);
+                const float by = to - ref[j];
+                if (first) k = mw > -INFINITY ? scale_ref(mw - by) : 0;
+                else if (own) k = scale_ref(fmaxf((float)was, mw) - by);
+                const float f = first ? 1.0f : ex2(-by), fa = first ? 1.0f : ex2((float)(was - k) - by);
                 ref[j] = to;
-                sc[j / 2][j & 1] -= by;
-                sc[j / 2][2 + (j & 1)] -= by;
+                fac[j] = factor_of(k);
+                sc[j / 2][j & 1] = s0 - by;
+                sc[j / 2][2 + (j & 1)] = s1 - by;
                 total[j] *= f;
 #pragma unroll
                 for (int mt = 0; mt < G::KS; ++mt) {
-                    acc[mt][j / 2][j & 1] *= f;
-                    acc[mt][j / 2][2 + (j & 1)] *= f;
+                    acc[mt][j / 2][j & 1] *= fa;
+                    acc[mt][j / 2][2 + (j & 1)] *= fa;
                 }
             }
+            weigh();
         }
-        const float rw[2] = {rv[0] * kLift, rv[1] * kLift};
         uint32_t pb[TERMS][NR][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float wgt[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float y = sc[nr][2 * i + b], p = ex2(y);
-                    total[2 * nr + b] += p;
-                    wgt[b] = p * rw[i];
-                    if (masked && y == -INFINITY) wgt[b] = 0.0f;     // nothing of a masked row, whatever its scale
-                }
-                const __half2 hi = __floats2half2_rn(wgt[0], wgt[1]);
+                const float w0 = wgt[nr][2 * i], w1 = wgt[nr][2 * i + 1];
+                total[2 * nr] += p[nr][2 * i];
+                total[2 * nr + 1] += p[nr][2 * i + 1];
+                const __half2 hi = __floats2half2_rn(w0, w1);
                 pb[0][nr][i] = transpose8(bits_of(hi));
                 if constexpr (TERMS == 2) {
                     const float2 back = __half22float2(hi);
-                    pb[1][nr][i] = transpose8(bits_of(__floats2half2_rn((wgt[0] - back.x) * 2048.0f, (wgt[1] - back.y) * 2048.0f)));
+                    pb[1][nr][i] = transpose8(bits_of(__floats2half2_rn((w0 - back.x) * 2048.0f, (w1 - back.y) * 2048.0f)));
                 }
             }
         // sums; the weights' second terms are 2^11 times what they stand for, their codes 2^-11 (exact).  The instruction cuts off
@@ -610,6 +644,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
             const int r = 8 * (j / 2) + 2 * lc + j % 2;
             wref[warp][r] = total[j] == 0.0f ? kNone : ref[j];
             wtot[warp][r] = total[j];
+            wsc[warp][r] = (float)k_of(fac[j]);
         }
     }
     ok = tc16::group_and(1, 32 * kWarps, ok);            // all four stop, or none
@@ -619,7 +654,10 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
         float m = wref[0][r];
 #pragma unroll
         for (int y = 1; y < kWarps; ++y) m = fmaxf(m, wref[y][r]);
-        const float f = ex2(wref[warp][r] - m);
+        float top = wref[0][r] - m + wsc[0][r];
+#pragma unroll
+        for (int y = 1; y < kWarps; ++y) top = fmaxf(top, wref[y][r] - m + wsc[y][r]);
+        const float f = ex2(wref[warp][r] - m + wsc[warp][r] - (float)scale_ref(top));
 #pragma unroll
         for (int mt = 0; mt < G::KS; ++mt) {
             acc[mt][j / 2][j & 1] *= f;
@@ -651,16 +689,21 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
         for (int y = 1; y < kWarps; ++y) m = fmaxf(m, wref[y][r]);
 #pragma unroll
         for (int y = 0; y < kWarps; ++y) l += ex2(wref[y][r] - m) * wtot[y][r];
+        float top = wref[0][r] - m + wsc[0][r];
+#pragma unroll
+        for (int y = 1; y < kWarps; ++y) top = fmaxf(top, wref[y][r] - m + wsc[y][r]);
+        const int k = scale_ref(top);
+        const float undo = undo_of(k);
         const int64_t tok = (int64_t)s * a.n_tok + (r0 + r) / group;
         const int hq = h * group + (r0 + r) % group;
         const int64_t place = ((int64_t)blockIdx.x * 2 + (at.first == 0 ? 1 : 0)) * G::R + r;   // if not whole
         for (int c = lane; c < D; c += 32) {
             const float y = sum[G::sum_at(r, c)];
-            if (whole) put_out(a, tok * a.os + (int64_t)hq * D + c, l == 0.0f ? 0.0f : y * (1.0f / kLift) / l);
+            if (whole) put_out(a, tok * a.os + (int64_t)hq * D + c, l == 0.0f ? 0.0f : y / l * undo);
             else a.part[place * D + c] = y;
         }
         if (lane == 0) {
-            if (!whole) a.meta[place] = make_float2(m, l);
+            if (!whole) a.meta[place] = make_float4(m, l, (float)k, 0.0f);
             else if (a.lse) a.lse[tok * a.Hq + hq] = log_sum(m, l);
         }
     }
@@ -678,7 +721,7 @@ constexpr int kJoin = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     constexpr int L = D / 4, GROUPS = kJoin / L;
-    __shared__ float f[kMaxBlocks], red[2][kJoin / 32];
+    __shared__ float f[kMaxBlocks], red[3][kJoin / 32];
     __shared__ __align__(16) float sum[GROUPS][D];
     const KvGeo &g = a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -715,24 +758,35 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kJoin / 32; ++w) m = fmaxf(m, red[0][w]);
-    float l = 0.0f;
+    float l = 0.0f, top = -60.0f;
     for (int p = tid; p < pieces; p += kJoin) {
-        const float2 x = a.meta[place(p)];
-        f[p] = ex2(x.x - m);
-        l += f[p] * x.y;
+        const float4 x = a.meta[place(p)];
+        l += ex2(x.x - m) * x.y;
+        f[p] = x.x - m + x.z;                            // log2 of the piece's sums against the largest score
+        top = fmaxf(top, f[p]);
     }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    if (lane == 0) red[1][warp] = l;
+    for (int w = 16; w > 0; w >>= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, w);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    }
+    if (lane == 0) {
+        red[1][warp] = l;
+        red[2][warp] = top;
+    }
     __syncthreads();
     l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoin / 32; ++w) l += red[1][w];
+    for (int w = 0; w < kJoin / 32; ++w) {
+        l += red[1][w];
+        top = fmaxf(top, red[2][w]);
+    }
+    const int k = scale_ref(top);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int p = tid / L; p < pieces; p += GROUPS) {
         const float4 x = *reinterpret_cast<const float4 *>(a.part + place(p) * D + tid % L * 4);
-        const float w = f[p];
+        const float w = ex2(f[p] - (float)k);
         y.x += w * x.x;
         y.y += w * x.y;
         y.z += w * x.z;
@@ -744,7 +798,7 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(KvAttendArgs a, int R) {
         float z = 0.0f;
 #pragma unroll
         for (int w = 0; w < GROUPS; ++w) z += sum[w][tid];
-        put_out(a, tok * a.os + (int64_t)hq * D + tid, l == 0.0f ? 0.0f : z * (1.0f / kLift) / l);
+        put_out(a, tok * a.os + (int64_t)hq * D + tid, l == 0.0f ? 0.0f : z / l * undo_of(k));
     }
     if (tid == 0 && a.lse) a.lse[tok * a.Hq + hq] = log_sum(m, l);
 }

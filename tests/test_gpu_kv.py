@@ -543,3 +543,28 @@ def test_check_is_refused_in_a_capture(stepq):
     graph.replay()
     z, r = _quantise(k, 8)
     assert torch.equal(s.read(torch.float32)[0], r.unsqueeze(-1) * z.float())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("size", [1e35, 1e37, 6e37])
+def test_attend_values_near_the_end_of_fp32(stepq, bits, dtype, size):
+    """Scores spread over 2^30: every token keeps its part of the sum, however large the values are, beside rows of ordinary ones
+    and of zeros."""
+    lens, d = [300, 70], 64
+    s = Seqs(stepq, lens, bits, 2, d, 32)
+    k, v = _randn(65, s.total, 2, d), _randn(66, s.total, 2, d).clamp(-4, 4) * size
+    v[5:300:7] = _randn(67, len(range(5, 300, 7)), 2, d)
+    v[6:300:7] = 0.0
+    s.fill(k, v)
+    q = (_randn(68, 2, 1, 4, d) * 2.5).to(TYPES[dtype])
+    o, l = _attend(s, q)
+    _check_attend(s, q, o, l, k, v, d ** -0.5)
+    wt = 2.0 ** -22 if dtype == "fp32" else 2.0 ** -11
+    for i in range(2):
+        p, vv, ref, ds = _exact_rows(s, q, k, v, i, 0, d ** -0.5)
+        mean = torch.einsum("hm,mhd->hd", p, vv.abs())
+        bound = (2 * torch.expm1(ds).unsqueeze(-1) + wt + p.shape[1] * 2.0 ** -23) * mean
+        bound = bound + torch.finfo(TYPES[dtype]).eps / 2 * (ref.abs() + bound)
+        err = (o[i, 0].double() - ref).abs()
+        assert (err <= bound).all(), (i, (err / bound).max().item())
