@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
         for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
         int ex = 0;
         if (m > 0.0f && m <= FLT_MAX) frexpf(m, &ex);
-        ex -= kLiftQ;
+        if (ex > -100) ex -= kLiftQ;                     // (the score factor below has to stay a normal number)
         // 2^-ex in two factors, each of which is a normal number
         const int e1 = ex / 2, e2 = ex - e1;
         const float f1 = ldexpf(1.0f, -e1), f2 = ldexpf(1.0f, -e2);

@@ -568,3 +568,14 @@ def test_attend_values_near_the_end_of_fp32(stepq, bits, dtype, size):
         bound = bound + torch.finfo(TYPES[dtype]).eps / 2 * (ref.abs() + bound)
         err = (o[i, 0].double() - ref).abs()
         assert (err <= bound).all(), (i, (err / bound).max().item())
+
+
+def test_attend_tiny_queries_of_large_keys(stepq):
+    """Queries near the lower end of fp32 and keys near its upper one: scores of order 1 keep their bits."""
+    n, d = 200, 64
+    s = Seqs(stepq, [n], 8, 1, d, 32)
+    k, v = _randn(69, n, 1, d).clamp(-4, 4) * 2.0 ** 124, _randn(70, n, 1, d)
+    s.fill(k, v)
+    q = _randn(71, 1, 1, 4, d) * 2.0 ** -125
+    o, l = _attend(s, q)
+    _check_attend(s, q, o, l, k, v, d ** -0.5)
