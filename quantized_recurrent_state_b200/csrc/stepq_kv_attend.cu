@@ -19,7 +19,7 @@
 //
 // The weight p r_v has to fit fp16, whatever r_v is, while the sum of p wants p near 1 at the largest score.  So a row has two
 // references: one of the scores, near the largest, which p = 2^(s - ref) is taken against, and an integer power of two for the value
-// scales on top of it, which the weight p r_v is multiplied by: 2^7 at the largest.  Both stay where they are until a weight would
+// scales on top of it, which the weight p r_v is multiplied by: 2^7 exactly at the largest.  Both stay where they are until a weight would
 // exceed 2^15 or a p 2^16: sums are fp32; a move costs six shuffles a row and the rescaling, a vote otherwise.  fp16 weights carry
 // up to 2^-11 of themselves as rounding error, or 2^-32 of the largest's where that is more (fp16 ends at 2^-25); fp32 outputs take
 // them as sums of two fp16 values, the second held 2^11 times as large (2^-22 of the weight, or 2^-43 of the largest's), and q
@@ -221,12 +221,7 @@ __device__ __forceinline__ void put_out(const KvAttendArgs &a, int64_t at, float
     else static_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
 }
 // Natural logarithm of 2^m l.
-__device__ __forceinline__ float log_sum(float m, float l) {
-    if (l == 0.0f) return -INFINITY;
-    int e;
-    const float f = frexpf(l, &e);
-    return (m + (float)e) * kLn2 + logf(f);
-}
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l)); }
 // The value scales' reference k (an integer within [-60, 126]) as the factor of the weights, and what undoes it at the end.
 __device__ __forceinline__ float factor_of(int k) { return __uint_as_float((uint32_t)(127 + kLift - k) << 23); }
 __device__ __forceinline__ float undo_of(int k) { return __uint_as_float((uint32_t)(127 - kLift + k) << 23); }
@@ -534,19 +529,19 @@ __global__ void __launch_bounds__(32 * kWarps + 32, TERMS == 1 ? 0 : NR * D > 25
                     ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, w));
                     mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, w));
                 }
-                // the row's own need, whatever its neighbours': down only while there are no sums (a row that sees nothing in
-                // its first tile sees nothing at all)
-                const int was = k_of(fac[j]);
-                const bool own = ms > 8.0f || mw - (float)was > 8.0f;
-                float to = ref[j];
-                int k = was;
-                if (first) to = ms == -INFINITY ? 0.0f : ms;
-                else if (own) to += fmaxf(ms, 0.0f);
-                const float by = to - ref[j];
-                if (first) k = mw > -INFINITY ? scale_ref(mw - by) : 0;
-                else if (own) k = scale_ref(fmaxf((float)was, mw) - by);
-                const float f = first ? 1.0f : ex2(-by), fa = first ? 1.0f : ex2((float)(was - k) - by);
-                ref[j] = to;
+                // the row's own need, whatever its neighbours': down only while there are no sums (a row that sees nothing in its first
+                // tile sees nothing at all).  The largest weight becomes 2^7 exactly, so that fp16 takes nothing from it (one token
+                // that outweighs the rest is the common case); the score's reference is then within 1 of the largest score.
+                const float was = (float)k_of(fac[j]);
+                float by = 0.0f;
+                int k = first ? 0 : (int)was;
+                if (first ? mw > -INFINITY : ms > 8.0f || mw - was > 8.0f) {
+                    const float most = first ? mw : fmaxf(mw, was);   // against the score's reference as it was
+                    k = scale_ref(most - (first ? ms : fmaxf(ms, 0.0f)));
+                    by = ref[j] + (most - (float)k) - ref[j];
+                }
+                const float f = first ? 1.0f : ex2(-by), fa = first ? 1.0f : ex2(was - (float)k - by);
+                ref[j] += by;
                 fac[j] = factor_of(k);
                 sc[j / 2][j & 1] = s0 - by;
                 sc[j / 2][2 + (j & 1)] = s1 - by;

@@ -579,3 +579,20 @@ def test_attend_tiny_queries_of_large_keys(stepq):
     q = _randn(71, 1, 1, 4, d) * 2.0 ** -125
     o, l = _attend(s, q)
     _check_attend(s, q, o, l, k, v, d ** -0.5)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_attend_one_token_gives_its_value_row(stepq, bits, dtype):
+    """A weight that stands alone is exact in fp16: o is the value row, rounded once (2^-21 for the exponential, logarithm and
+    quotient)."""
+    n, d = 64, 128
+    s = Seqs(stepq, [1] * n, bits, 2, d, 16)
+    k, v = _randn(72, n, 2, d), _randn(73, n, 2, d)
+    s.fill(k, v)
+    q = _randn(74, n, 1, 4, d).to(TYPES[dtype])
+    o, _ = _attend(s, q)
+    z, r = _quantise(v, bits)
+    ref = (r.double().unsqueeze(-1) * z.double()).repeat_interleave(2, 1).unsqueeze(1)
+    bound = (torch.finfo(TYPES[dtype]).eps / 2 + 2.0 ** -21) * ref.abs()
+    assert ((o.double() - ref).abs() <= bound).all()
