@@ -40,8 +40,8 @@
 //
 // Measured: 70 requests of up to 8,192 tokens, 8 cache heads of 128, 8 bits, 32 query heads: 131 to 139 us, 0.66 GB, 5 TB/s (the stages
 // alone run at the copy's rate; the start of a block costs 6 us, the end of a unit 3 to 4, the join 7).  One request of
-// 131,072 tokens at 4 bits: 49 us against 22: 4-bit codes cost 350 instructions a tile of 16 tokens, and the SM issues 59 % of the
-// time.  16 requests of up to 20,000 tokens, two heads of 256: 53 us against 29.  Few short ones: 14 us, launch and host.
+// 131,072 tokens at 4 bits: 50 us against 22: 4-bit codes cost 350 instructions a tile of 16 tokens, and the SM issues 59 % of the
+// time.  16 requests of up to 20,000 tokens, two heads of 256: 54.5 us against 29.  Few short ones: 14 us, launch and host.
 #include <float.h>
 
 #include <type_traits>
